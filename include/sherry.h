@@ -70,7 +70,9 @@ typedef enum {
   SHERRY_ERR_WORKSPACE = 8,   /* workspace NULL or smaller than sherry_workspace_bytes */
   SHERRY_ERR_BATCH = 9,       /* batch outside 1..16, m < 1, count < 1, or a
                                  stride too small for its operand */
-  SHERRY_ERR_HIP = 10         /* the HIP runtime reported an error at launch */
+  SHERRY_ERR_HIP = 10,        /* the HIP runtime reported an error at launch */
+  SHERRY_ERR_ARG = 11         /* an argument of an operator in sherry_ops.h is
+                                 out of its range */
 } sherry_status;
 
 /* Scale granules ("Sherry, Tequila and Fairies in Python", section 1.1,

@@ -23,6 +23,8 @@ __all__ = [
     "workspace_bytes", "SherryError", "load", "fake_quant", "fake_quant_ste", "gemv_batched",
     "FusedWeight", "quantize_pack_fused", "gemv_fused", "arenas_lambda", "arenas_gemm",
     "compare_repack", "compare_gemv", "gemm_fused", "quantize_pack_noalloc",
+    "AdapterSet", "adapter_gemv", "adapter_gemm", "block_norm", "block_norm_backward", "block_norm_ad",
+    "orthogonalize", "muon_step", "NEWTON_SCHULZ",
 ]
 
 
@@ -482,3 +484,8 @@ def gemm(pw: PackedWeight, x, stream=None, out=None):
         check(lib.sherry_gemm(pw.n, pw.k, gran, pw.group_size, _ptr(pw.packed), _ptr(pw.alpha), _ptr(x), m,
                               _ptr(y), _ptr(ws), 0 if ws is None else ws.numel(), _stream(stream)))
     return y
+
+
+from .adapters import AdapterSet, adapter_gemm, adapter_gemv  # noqa: E402
+from .muon import NEWTON_SCHULZ, muon_step, orthogonalize  # noqa: E402
+from .norms import block_norm, block_norm_ad, block_norm_backward  # noqa: E402

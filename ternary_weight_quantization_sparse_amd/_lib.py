@@ -23,6 +23,8 @@ GRANULARITY = {"per_tensor": PER_TENSOR, "per_channel": PER_CHANNEL, "per_group"
 CMP_2BIT, CMP_TL2 = 0, 1
 F32, BF16, I8 = 0, 1, 2
 OP_QUANTIZE_PACK, OP_UNPACK, OP_GEMV, OP_GEMM, OP_FAKE_QUANT, OP_ARENAS_GEMM = 0, 1, 2, 3, 4, 5
+ERR_ARG = 11
+GATE_NONE, GATE_TOKEN, GATE_CHANNEL, GATE_ROWS = 0, 1, 2, 3
 QUANTIZE_SCRATCH_BYTES = 8 << 20   # SHERRY_QUANTIZE_SCRATCH_BYTES
 
 # every symbol include/sherry.h declares
@@ -33,7 +35,16 @@ SYMBOLS = (
     "sherry_compare_gemv", "sherry_arenas_lambda", "sherry_quantize_pack_noalloc",
 )
 
+# every symbol include/sherry_ops.h declares
+OPS_SYMBOLS = (
+    "sherry_block_norm", "sherry_block_norm_backward_bytes", "sherry_block_norm_backward",
+    "sherry_adapter_workspace_bytes", "sherry_adapter_gemv", "sherry_adapter_gemm",
+    "sherry_muon_workspace_bytes", "sherry_orthogonalize", "sherry_muon_step",
+)
+
 _i32, _i64, _sz, _vp = ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t, ctypes.c_void_p
+
+_f32 = ctypes.c_float
 
 _SIGNATURES = {
     "sherry_abi_version": ([], _i32),
@@ -54,6 +65,20 @@ _SIGNATURES = {
     "sherry_compare_bytes": ([_i32, _i64, _i64], _sz),
     "sherry_compare_repack": ([_i32, _i64, _i64, _vp, _vp, _vp], _i32),
     "sherry_compare_gemv": ([_i32, _i64, _i64, _vp, _vp, _vp, _vp, _i32, _i64, _i64, _i64, _vp], _i32),
+    "sherry_block_norm": ([_i64, _i64, _vp, _vp, _i32, _vp, _vp, _i32, _vp, _i32, _i64, _f32, _f32, _vp, _vp, _vp],
+                          _i32),
+    "sherry_block_norm_backward_bytes": ([_i64, _i64, _i32, _i64], _sz),
+    "sherry_block_norm_backward": ([_i64, _i64, _vp, _vp, _vp, _vp, _i32, _vp, _vp, _i32, _vp, _i32, _i64, _f32, _f32,
+                                    _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp], _i32),
+    "sherry_adapter_workspace_bytes": ([_i64, _i64, _i32, _i32, _i64, _i32, _i32], _sz),
+    "sherry_adapter_gemv": ([_i64, _i64, _i32, _i32, _vp, _vp, _vp, _i32, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _i32,
+                             _i32, _vp, _sz, _vp], _i32),
+    "sherry_adapter_gemm": ([_i64, _i64, _i32, _i32, _vp, _vp, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32,
+                             _vp, _sz, _vp], _i32),
+    "sherry_muon_workspace_bytes": ([_i32, _i64, _i64], _sz),
+    "sherry_orthogonalize": ([_i32, _i64, _i64, _vp, _i32, _vp, _i32, _f32, _f32, _f32, _f32, _vp, _sz, _vp], _i32),
+    "sherry_muon_step": ([_i32, _i64, _i64, _vp, _vp, _vp, _i32, _vp, _vp, _f32, _f32, _i32, _f32, _f32, _i32, _f32,
+                          _f32, _f32, _f32, _vp, _sz, _vp], _i32),
 }
 
 _lib = None

@@ -38,10 +38,17 @@
 // Split K: launches with few tiles split K into `splits` ranges of whole
 // groups; each writes fp32 partial tiles to the workspace, and a second
 // kernel sums them in split order (deterministic), scales and rounds to bf16.
+//
+// Adapters (AD): the epilogue adds each token's low-rank product to the fp32
+// accumulators before their one rounding, on MFMA: for every adapter in use by
+// the tile's tokens, its b rows as the A operand and the tokens' scaled a x as
+// the B operand, added to the tokens of that adapter only.  The fp32 a x go in as two
+// bf16 terms (hi + lo, 16 bits), so the delta loses nothing that y's rounding
+// would keep.
 #include <cmath>
 #include <type_traits>
 
-#include "sherry_internal.h"
+#include "ops_internal.h"
 
 namespace sherry {
 namespace {
@@ -117,14 +124,15 @@ using Slot = std::integral_constant<int, J>;
 // grid: x = tiles (tiles_m * tiles_n), y = K splits.  partial == nullptr:
 // write bf16 Y; else write fp32 partial[split][m][n] (per_group already
 // scaled, per_channel / per_tensor not yet; AR: fully scaled).
-template <int GRAN, int TM, bool AR, int TN, bool MERGE>
+template <int GRAN, int TM, bool AR, int TN, bool MERGE, bool AD>
 __global__ __launch_bounds__(kThreads, AR ? (GRAN != SHERRY_PER_GROUP || MERGE ? 2 : 1) : (TN == 4 ? 2 : 3)) void gemm_kernel(const uint8_t* packed,
                                                      const float* __restrict__ alpha,
                                                      const uint16_t* __restrict__ x,
                                                      uint16_t* __restrict__ y, float* __restrict__ partial,
                                                      int64_t n, int64_t k, int64_t m, int group_sbs,
                                                      int tiles_m, int tiles_n, int sb_per_split,
-                                                     const uint16_t* __restrict__ wd, float lam) {
+                                                     const uint16_t* __restrict__ wd, float lam,
+                                                     AdapterTerm ad) {
   using C = GemmCfg<GRAN, TM, AR, TN, MERGE>;
   static_assert(!MERGE || (AR && GRAN == SHERRY_PER_GROUP), "MERGE is the per_group Arenas variant");
   constexpr int kTM = C::kTM, kBM = C::kBM, kXLoads = C::kXLoads, kRecWave = C::kRecWave;
@@ -435,6 +443,90 @@ __global__ __launch_bounds__(kThreads, AR ? (GRAN != SHERRY_PER_GROUP || MERGE ?
   }
   wait_vmcnt<0>();  // the trailing repeat copies have landed before the wave ends
 
+  if constexpr (AD) {
+    // accumulators to their final scale first, then split 0 adds the adapters
+    if constexpr (!C::kGroup) {
+#pragma unroll
+      for (int i = 0; i < kTN; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int64_t gn = n0 + wave * kWN + i * 16 + 4 * q + e;
+          const float sc = GRAN == SHERRY_PER_TENSOR ? alpha[0] : (gn < n ? alpha[gn] : 0.f);
+#pragma unroll
+          for (int jj = 0; jj < kTM; ++jj) acc[i][jj][e] *= sc;
+        }
+    }
+    if (kz == 0) {
+      int id[kTM];
+#pragma unroll
+      for (int jj = 0; jj < kTM; ++jj) {
+        const int64_t gm = m0 + jj * 16 + r;
+        id[jj] = gm < m ? ad.a.ids[gm] : -1;
+      }
+      for (int done = -1;;) {
+        // the smallest adapter in use beyond the last one: the lanes of a
+        // 16-lane row hold all the tile's tokens
+        int next = ad.a.count;
+#pragma unroll
+        for (int jj = 0; jj < kTM; ++jj)
+          if (id[jj] > done && id[jj] < next) next = id[jj];
+#pragma unroll
+        for (int o = 1; o < 16; o <<= 1) next = min(next, __shfl_xor(next, o));
+        const int c = __builtin_amdgcn_readfirstlane(next);
+        if (c >= ad.a.count) break;
+        done = c;
+        const int rank = adapter_rank(ad.a, c);
+        for (int k0 = 0; k0 < rank; k0 += 32) {
+          const int kr = k0 + 8 * q;            // this lane's 8 columns of b
+          bf16x8 bw[kTN];
+#pragma unroll
+          for (int i = 0; i < kTN; ++i) {
+            const int64_t gn = n0 + wave * kWN + i * 16 + r;
+            u32x4 w{0u, 0u, 0u, 0u};
+            if (kr < rank && gn < n)
+              w = *reinterpret_cast<const u32x4*>(ad.a.b + ((int64_t)c * n + gn) * ad.a.rank + kr);
+            bf16x8 v = __builtin_bit_cast(bf16x8, w);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = kr + e < rank ? v[e] : (__bf16)0.f;
+            bw[i] = v;
+          }
+#pragma unroll
+          for (int jj = 0; jj < kTM; ++jj) {
+            float v[8] = {};
+            if (id[jj] == c && kr < rank) {
+              const float* src = ad.v + (m0 + jj * 16 + r) * ad.a.rank + kr;
+              for (int z = 0; z < ad.parts; ++z) {
+                const f32x4 lo4 = *reinterpret_cast<const f32x4*>(src + z * ad.part_stride);
+                const f32x4 hi4 = *reinterpret_cast<const f32x4*>(src + z * ad.part_stride + 4);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  v[e] += lo4[e];
+                  v[4 + e] += hi4[e];
+                }
+              }
+            }
+            bf16x8 vh, vl;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const float t = kr + e < rank ? v[e] : 0.f;
+              vh[e] = (__bf16)t;
+              vl[e] = (__bf16)(t - (float)vh[e]);
+            }
+            // added by selection: an infinity or NaN in this adapter's b stays
+            // with its own tokens
+#pragma unroll
+            for (int i = 0; i < kTN; ++i) {
+              f32x4 d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bw[i], vl, f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
+              d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bw[i], vh, d, 0, 0, 0);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) acc[i][jj][e] += id[jj] == c ? d[e] : 0.f;
+            }
+          }
+        }
+      }
+    }
+  }
+
   // epilogue: lane holds Y[m0 + 16jj + r][n0 + 32 wave + 16i + 4q + e]
 #pragma unroll
   for (int i = 0; i < kTN; ++i) {
@@ -443,7 +535,7 @@ __global__ __launch_bounds__(kThreads, AR ? (GRAN != SHERRY_PER_GROUP || MERGE ?
     // scale applied here: per_channel / per_tensor when writing Y, and always
     // for AR (its partials carry the finished value); per_group is scaled
     float sc[4] = {1.f, 1.f, 1.f, 1.f};
-    if (partial == nullptr || AR) {
+    if (!AD && (partial == nullptr || AR)) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         if constexpr (GRAN == SHERRY_PER_CHANNEL) sc[e] = (gn0 + e < n) ? alpha[gn0 + e] : 0.f;
@@ -533,10 +625,10 @@ __global__ __launch_bounds__(256) void gemm_split_reduce(const float* __restrict
 // the end, stay below 2^31 bytes.
 int64_t gemm_chunk_rows(int64_t k) { return ((((int64_t)1 << 31) / (2 * k) - kMaxBM) / kMaxBM) * kMaxBM; }
 
-template <int GRAN, int TM, bool AR, int TN, bool MERGE = false>
+template <int GRAN, int TM, bool AR, int TN, bool MERGE = false, bool AD = false>
 hipError_t launch_g(const GemmPlan& p, int64_t n, int64_t k, int group_sbs, const uint8_t* packed,
                     const float* alpha, const uint16_t* x, int64_t m, uint16_t* y, float* ws,
-                    const uint16_t* wd, float lam, hipStream_t s) {
+                    const uint16_t* wd, float lam, hipStream_t s, AdapterTerm ad = AdapterTerm{}) {
   constexpr int kBM = GemmCfg<GRAN, TM, AR, TN, MERGE>::kBM, kBN = GemmCfg<GRAN, TM, AR, TN, MERGE>::kBN;
   const int64_t chunk = gemm_chunk_rows(k);
   if (chunk < kMaxBM) return hipErrorInvalidValue;
@@ -548,16 +640,20 @@ hipError_t launch_g(const GemmPlan& p, int64_t n, int64_t k, int group_sbs, cons
   for (int64_t r0 = 0; r0 < m; r0 += chunk) {
     const int64_t mc = m - r0 < chunk ? m - r0 : chunk;
     const int tiles_m = (int)((mc + kBM - 1) / kBM);
-    hipLaunchKernelGGL((gemm_kernel<GRAN, TM, AR, TN, MERGE>), dim3((unsigned)(tiles_m * tiles_n), (unsigned)splits),
+    hipLaunchKernelGGL((gemm_kernel<GRAN, TM, AR, TN, MERGE, AD>), dim3((unsigned)(tiles_m * tiles_n), (unsigned)splits),
                        dim3(kThreads), 0, s, packed, alpha, x + r0 * k, y + r0 * n, splits > 1 ? ws : nullptr, n, k,
-                       mc, group_sbs, tiles_m, tiles_n, sb_per_split, wd, lam);
+                       mc, group_sbs, tiles_m, tiles_n, sb_per_split, wd, lam, ad);
+    if constexpr (AD) {   // the next chunk's tokens
+      ad.a.ids += mc;
+      ad.v += mc * ad.a.rank;
+    }
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     if (splits > 1) {
       const int64_t mn = mc * n;
       const int64_t threads = (mn + 3) / 4;
-      // AR partials are already scaled: sum them with the scale-free reducer
-      hipLaunchKernelGGL((gemm_split_reduce<AR ? SHERRY_PER_GROUP : GRAN>), dim3((unsigned)((threads + 255) / 256)),
+      // AR and AD partials are already scaled: sum them with the scale-free reducer
+      hipLaunchKernelGGL((gemm_split_reduce<AR || AD ? SHERRY_PER_GROUP : GRAN>), dim3((unsigned)((threads + 255) / 256)),
                          dim3(256), 0, s, ws, alpha, y + r0 * n, mn, n, splits);
       e = hipGetLastError();
       if (e != hipSuccess) return e;
@@ -607,6 +703,24 @@ hipError_t launch_gemm(const GemmPlan& p, int64_t n, int64_t k, int gran, int gr
   const int group_sbs = gran == SHERRY_PER_GROUP ? group_size / kSuperblock : 1;
 #define SHERRY_GEMM_LAUNCH(G, TN) \
   return launch_g<G, kGemmTM, false, TN>(p, n, k, group_sbs, packed, alpha, x, m, y, ws, nullptr, 0.f, s)
+  if (p.tile_n == 256) {
+    if (gran == SHERRY_PER_GROUP) SHERRY_GEMM_LAUNCH(SHERRY_PER_GROUP, 4);
+    if (gran == SHERRY_PER_CHANNEL) SHERRY_GEMM_LAUNCH(SHERRY_PER_CHANNEL, 4);
+    SHERRY_GEMM_LAUNCH(SHERRY_PER_TENSOR, 4);
+  }
+  if (gran == SHERRY_PER_GROUP) SHERRY_GEMM_LAUNCH(SHERRY_PER_GROUP, 2);
+  if (gran == SHERRY_PER_CHANNEL) SHERRY_GEMM_LAUNCH(SHERRY_PER_CHANNEL, 2);
+  SHERRY_GEMM_LAUNCH(SHERRY_PER_TENSOR, 2);
+#undef SHERRY_GEMM_LAUNCH
+}
+
+hipError_t launch_gemm_adapted(const GemmPlan& p, int64_t n, int64_t k, int gran, int group_size,
+                               const uint8_t* packed, const float* alpha, const uint16_t* x, int64_t m,
+                               uint16_t* y, float* ws, const AdapterTerm& ad, hipStream_t s) {
+  const int group_sbs = gran == SHERRY_PER_GROUP ? group_size / kSuperblock : 1;
+#define SHERRY_GEMM_LAUNCH(G, TN)                                                                                \
+  return launch_g<G, kGemmTM, false, TN, false, true>(p, n, k, group_sbs, packed, alpha, x, m, y, ws, nullptr, \
+                                                      0.f, s, ad)
   if (p.tile_n == 256) {
     if (gran == SHERRY_PER_GROUP) SHERRY_GEMM_LAUNCH(SHERRY_PER_GROUP, 4);
     if (gran == SHERRY_PER_CHANNEL) SHERRY_GEMM_LAUNCH(SHERRY_PER_CHANNEL, 4);

@@ -64,6 +64,7 @@ const char* sherry_status_string(int32_t status) {
     case SHERRY_ERR_WORKSPACE: return "SHERRY_ERR_WORKSPACE: workspace missing or too small";
     case SHERRY_ERR_BATCH: return "SHERRY_ERR_BATCH: batch must be 1..16, m and count >= 1, strides large enough";
     case SHERRY_ERR_HIP: return "SHERRY_ERR_HIP: the HIP runtime reported an error";
+    case SHERRY_ERR_ARG: return "SHERRY_ERR_ARG: an argument of this operator is out of its range";
     default: return "unknown sherry status";
   }
 }
