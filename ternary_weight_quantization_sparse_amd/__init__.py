@@ -34,9 +34,12 @@ def _torch():
 
 
 def _stream(stream):
-    torch = _torch()
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return s.cuda_stream
+    """The stream's handle; the current one straight from torch's C layer (the
+    stream object that torch.cuda.current_stream() makes costs 2.7 us)."""
+    if stream is not None:
+        return stream.cuda_stream
+    c = _torch()._C
+    return c._cuda_getCurrentRawStream(c._cuda_getDevice())
 
 
 def _on_stream(stream):

@@ -14,70 +14,105 @@ from . import _lib, _need_gpu, _on_stream, _ptr, _stream, _torch, _workspace
 from ._lib import check, load
 
 
-def _dtype_code(t, name):
+def _codes():
     torch = _torch()
-    code = {torch.float32: _lib.F32, torch.bfloat16: _lib.BF16}.get(t.dtype)
-    if code is None:
-        raise ValueError(f"{name} must be float32 or bfloat16, got {t.dtype}")
-    return code
+    return {torch.float32: _lib.F32, torch.bfloat16: _lib.BF16}
 
 
-class _Norm:
-    """Checked operands of one call: contiguous, two-dimensional, on one GPU."""
+def _contiguous(t):
+    return t if t is None or t.is_contiguous() else t.contiguous()
 
-    def __init__(self, h, w_pre, y, w_post, gate, res_scale, eps):
-        _need_gpu(h, "h")
-        dev = h.device
-        if h.dim() < 1 or h.shape[-1] < 1:
-            raise ValueError(f"h must be [..., D], got {tuple(h.shape)}")
-        self.shape, self.dim = h.shape, int(h.shape[-1])
-        self.rows = h.numel() // self.dim
-        self.code = _dtype_code(h, "h")
-        if y is None and w_pre is None:
-            raise ValueError("nothing to do: neither a block output y nor a norm w_pre")
-        if y is None and (w_post is not None or gate is not None or res_scale != 1.0):
-            raise ValueError("w_post, gate and res_scale belong to a block output y")
-        if y is not None:
-            _need_gpu(y, "y", dev)
-            if y.shape != h.shape or y.dtype != h.dtype:
-                raise ValueError(f"y must be {h.dtype} {tuple(h.shape)} like h, got {y.dtype} {tuple(y.shape)}")
-        self.w_code = _lib.F32
-        for name, w in (("w_post", w_post), ("w_pre", w_pre)):
-            if w is None:
-                continue
-            _need_gpu(w, name, dev)
-            if tuple(w.shape) != (self.dim,):
-                raise ValueError(f"{name} must be [{self.dim}], got {tuple(w.shape)}")
-            self.w_code = _dtype_code(w, name)
-        if w_post is not None and w_pre is not None and w_post.dtype != w_pre.dtype:
-            raise ValueError("w_post and w_pre must have one dtype")
-        self.kind, self.gate_rows = _lib.GATE_NONE, 1
-        if gate is not None:
-            _need_gpu(gate, "gate", dev)
-            if gate.dtype != h.dtype:
-                raise ValueError(f"gate must be {h.dtype} like h, got {gate.dtype}")
-            if tuple(gate.shape) == (self.dim,):
-                self.kind = _lib.GATE_CHANNEL
-            elif gate.dim() == 2 and gate.shape[1] == self.dim and gate.shape[0] > 0 \
-                    and self.rows % gate.shape[0] == 0 and (self.dim > 1 or gate.shape[0] != self.rows):
-                self.kind, self.gate_rows = _lib.GATE_ROWS, max(self.rows // int(gate.shape[0]), 1)
-            elif tuple(gate.shape) == (self.rows, 1):
-                self.kind = _lib.GATE_TOKEN
-            else:
-                raise ValueError(f"gate must be [{self.dim}] (a channel), [{self.rows}, 1] (a token) or [S, {self.dim}] "
-                                 f"with S dividing {self.rows} rows, got {tuple(gate.shape)}")
-        self.h, self.y, self.w_post, self.w_pre, self.gate = (
-            None if t is None else t.contiguous() for t in (h, y, w_post, w_pre, gate))
-        self.res_scale, self.eps = float(res_scale), float(eps)
 
-    def like(self, t, name):
-        """An incoming gradient of an output: h's shape and dtype."""
-        if t is None:
-            return None
-        _need_gpu(t, name, self.h.device)
-        if t.shape != self.shape or t.dtype != self.h.dtype:
-            raise ValueError(f"{name} must be {self.h.dtype} {tuple(self.shape)}, got {t.dtype} {tuple(t.shape)}")
-        return t.contiguous()
+def _like(t, h, name):
+    """An operand of h's shape, dtype and device."""
+    _need_gpu(t, name, h.device)
+    if t.shape != h.shape or t.dtype != h.dtype:
+        raise ValueError(f"{name} must be {h.dtype} {tuple(h.shape)} like h, got {t.dtype} {tuple(t.shape)}")
+
+
+def _layout(h, w_pre, y, w_post, gate, res_scale):
+    """Checks one call's operands; (rows, D, dtype code, weight dtype code, gate
+    kind, rows that share a gate row)."""
+    _need_gpu(h, "h")
+    codes, dev = _codes(), h.device
+    if h.dim() < 1 or h.shape[-1] < 1:
+        raise ValueError(f"h must be [..., D], got {tuple(h.shape)}")
+    dim = h.shape[-1]
+    rows = h.numel() // dim
+    if h.dtype not in codes:
+        raise ValueError(f"h must be float32 or bfloat16, got {h.dtype}")
+    if y is not None:
+        _like(y, h, "y")
+    elif w_pre is None:
+        raise ValueError("nothing to do: neither a block output y nor a norm w_pre")
+    elif w_post is not None or gate is not None or res_scale != 1.0:
+        raise ValueError("w_post, gate and res_scale belong to a block output y")
+    w_dtype = None
+    for name, w in (("w_post", w_post), ("w_pre", w_pre)):
+        if w is None:
+            continue
+        _need_gpu(w, name, dev)
+        if w.shape != (dim,) or w.dtype not in codes or w_dtype not in (None, w.dtype):
+            raise ValueError(f"w_post and w_pre must be [{dim}], both float32 or both bfloat16, got {name} "
+                             f"{w.dtype} {tuple(w.shape)}")
+        w_dtype = w.dtype
+    kind, gate_rows = _lib.GATE_NONE, 1
+    if gate is not None:
+        _need_gpu(gate, "gate", dev)
+        if gate.dtype != h.dtype:
+            raise ValueError(f"gate must be {h.dtype} like h, got {gate.dtype}")
+        shape = gate.shape
+        if shape == (dim,):
+            kind = _lib.GATE_CHANNEL
+        elif shape == (rows, 1):
+            kind = _lib.GATE_TOKEN
+        elif len(shape) == 2 and shape[1] == dim and shape[0] > 0 and rows % shape[0] == 0:
+            kind, gate_rows = _lib.GATE_ROWS, max(rows // shape[0], 1)
+        else:
+            raise ValueError(f"gate must be [{dim}] (a channel), [{rows}, 1] (a token) or [S, {dim}] with S dividing "
+                             f"{rows} rows, got {tuple(shape)}")
+    return rows, dim, codes[h.dtype], codes.get(w_dtype, _lib.F32), kind, gate_rows
+
+
+def _forward(layout, h, w_pre, y, w_post, gate, res_scale, eps, stream):
+    rows, dim, code, w_code, kind, gate_rows = layout
+    empty_like = _torch().empty_like
+    h_, y, w_pre, w_post, gate = _contiguous(h), _contiguous(y), _contiguous(w_pre), _contiguous(w_post), _contiguous(gate)
+    h_out = h if y is None else empty_like(h_)
+    n = None if w_pre is None else empty_like(h_)
+    if rows:
+        check(load().sherry_block_norm(rows, dim, _ptr(h_), _ptr(y), code, _ptr(w_post), _ptr(w_pre), w_code, _ptr(gate),
+                                       kind, gate_rows, res_scale, eps, None if y is None else h_out.data_ptr(), _ptr(n),
+                                       _stream(stream)))
+    return h_out, n
+
+
+def _backward(layout, dh_out, dn, h, w_pre, y, w_post, gate, res_scale, eps, stream):
+    rows, dim, code, w_code, kind, gate_rows = layout
+    torch = _torch()
+    if dh_out is not None:
+        _like(dh_out, h, "dh_out")
+    if w_pre is None:
+        dn = None
+    elif dn is not None:
+        _like(dn, h, "dn")
+    h, y, w_pre, w_post, gate = _contiguous(h), _contiguous(y), _contiguous(w_pre), _contiguous(w_post), _contiguous(gate)
+    dh_out, dn = _contiguous(dh_out), _contiguous(dn)
+    dh, dw_pre, dy, dw_post, dgate = grads = [None if t is None else torch.empty_like(t)
+                                              for t in (h, w_pre, y, w_post, gate)]
+    if rows:
+        lib = load()
+        nbytes = lib.sherry_block_norm_backward_bytes(rows, dim, kind, gate_rows)
+        ws = _workspace(nbytes, h.device)
+        check(lib.sherry_block_norm_backward(
+            rows, dim, _ptr(h), _ptr(y), _ptr(dh_out), _ptr(dn), code, _ptr(w_post), _ptr(w_pre), w_code, _ptr(gate),
+            kind, gate_rows, res_scale, eps, _ptr(dh), _ptr(dy), _ptr(dw_post), _ptr(dw_pre), _ptr(dgate), _ptr(ws),
+            nbytes, _stream(stream)))
+    else:
+        for t in grads[1:]:
+            if t is not None:
+                t.zero_()
+    return tuple(grads)
 
 
 def block_norm(h, w_pre=None, y=None, w_post=None, gate=None, res_scale: float = 1.0, eps: float = 1e-6, stream=None):
@@ -88,16 +123,11 @@ def block_norm(h, w_pre=None, y=None, w_post=None, gate=None, res_scale: float =
     [rows, 1] or [S, D] for S equal runs of rows; ``w_pre`` [D] the norm before
     the next block (None: n is None).  Sums and norms are fp32, each output is
     rounded once."""
-    torch = _torch()
+    layout = _layout(h, w_pre, y, w_post, gate, res_scale)
+    if stream is None:
+        return _forward(layout, h, w_pre, y, w_post, gate, res_scale, eps, None)
     with _on_stream(stream):
-        a = _Norm(h, w_pre, y, w_post, gate, res_scale, eps)
-        h_out = torch.empty_like(a.h) if y is not None else h
-        n = torch.empty_like(a.h) if w_pre is not None else None
-        if a.rows:
-            check(load().sherry_block_norm(
-                a.rows, a.dim, _ptr(a.h), _ptr(a.y), a.code, _ptr(a.w_post), _ptr(a.w_pre), a.w_code, _ptr(a.gate),
-                a.kind, a.gate_rows, a.res_scale, a.eps, None if y is None else _ptr(h_out), _ptr(n), _stream(stream)))
-    return h_out, n
+        return _forward(layout, h, w_pre, y, w_post, gate, res_scale, eps, stream)
 
 
 def block_norm_backward(dh_out, dn, h, w_pre=None, y=None, w_post=None, gate=None, res_scale: float = 1.0,
@@ -106,27 +136,9 @@ def block_norm_backward(dh_out, dn, h, w_pre=None, y=None, w_post=None, gate=Non
     of its outputs (either may be None: zero), None for absent operands.
     h' is recomputed from y and h in fp32, and sums over rows and over a gate's
     broadcast are fp32 in a fixed order."""
-    torch = _torch()
+    layout = _layout(h, w_pre, y, w_post, gate, res_scale)
     with _on_stream(stream):
-        a = _Norm(h, w_pre, y, w_post, gate, res_scale, eps)
-        dh_out, dn = a.like(dh_out, "dh_out"), a.like(dn, "dn")
-        if a.w_pre is None:
-            dn = None
-        dh = torch.empty_like(a.h)
-        made = [None if t is None else torch.empty_like(t) for t in (a.w_pre, a.y, a.w_post, a.gate)]
-        if a.rows:
-            lib = load()
-            ws = _workspace(int(lib.sherry_block_norm_backward_bytes(a.rows, a.dim, a.kind, a.gate_rows)), h.device)
-            dw_pre, dy, dw_post, dgate = made
-            check(lib.sherry_block_norm_backward(
-                a.rows, a.dim, _ptr(a.h), _ptr(a.y), _ptr(dh_out), _ptr(dn), a.code, _ptr(a.w_post), _ptr(a.w_pre),
-                a.w_code, _ptr(a.gate), a.kind, a.gate_rows, a.res_scale, a.eps, _ptr(dh), _ptr(dy), _ptr(dw_post),
-                _ptr(dw_pre), _ptr(dgate), _ptr(ws), ws.numel(), _stream(stream)))
-        else:
-            for t in made:
-                if t is not None:
-                    t.zero_()
-    return (dh, *made)
+        return _backward(layout, dh_out, dn, h, w_pre, y, w_post, gate, res_scale, eps, stream)
 
 
 def _make_ad():
@@ -138,17 +150,18 @@ def _make_ad():
         @staticmethod
         def forward(ctx, h, w_pre, y, w_post, gate, res_scale, eps):
             ctx.save_for_backward(h, w_pre, y, w_post, gate)
-            ctx.args = (res_scale, eps)
             ctx.set_materialize_grads(False)
-            out, n = block_norm(h, w_pre, y, w_post, gate, res_scale, eps)
+            layout = _layout(h, w_pre, y, w_post, gate, res_scale)
+            ctx.args = layout, res_scale, eps
+            out, n = _forward(layout, h, w_pre, y, w_post, gate, res_scale, eps, None)
             return (h.view_as(h) if y is None else out), n
 
         @staticmethod
         def backward(ctx, dh_out, dn):
-            h, w_pre, y, w_post, gate = ctx.saved_tensors
             if dh_out is None and dn is None:
                 return (None,) * 7
-            return (*block_norm_backward(dh_out, dn, h, w_pre, y, w_post, gate, *ctx.args), None, None)
+            layout, res_scale, eps = ctx.args
+            return (*_backward(layout, dh_out, dn, *ctx.saved_tensors, res_scale, eps, None), None, None)
 
     return BlockNorm
 
