@@ -16,7 +16,19 @@
 // puts entries down to 1 / sqrt(L) well inside float16's range (lo parts stay
 // normal numbers to 2^-27) and leaves room to 4 for iterates and 7 for b A + c A A.
 //
-// The matrix cores bound it: 3 steps (3 R^2 L + R^3) multiply-adds of float16.
+// Steps in groups.  All factors of X are polynomials of one matrix and commute,
+// so three steps need X only at their start and end: with A = X X^T, B = b A +
+// c A A, P = a I + B, the next step's A is P A P, and X <- P'' P' P X.  P'' P' P is
+// kept as q I + D (the large part apart), D at 2^9: it reaches a^3.  Where L >=
+// 2 R the R x R products cost less than two passes over X: 38 R^3 against 65 R^3
+// multiply-adds at L = 4 R (1.19 ms against 1.89 ms for 2048 x 8192).  It loses some accuracy (3.0e-6 against
+// 1.8e-6 of the result there), so fp32 results of sherry_orthogonalize, which
+// shows them whole, take every step by itself; bf16 results and the update of
+// weights do not see it.
+//
+// The matrix cores bound the large sizes, at the clock that their power leaves:
+// 2048 x 8192 (fp32) runs its products over X at 1.1 PFLOP/s of float16, the matrix cores 79%
+// busy at 1.7 GHz.  Small ones are bound by 17 launches of about 5 us.
 #include <algorithm>
 
 #include "ops_internal.h"
@@ -25,25 +37,35 @@ namespace sherry {
 namespace {
 
 typedef _Float16 f16;
-typedef f16 f16x4 __attribute__((ext_vector_type(4)));
 typedef f16 f16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 constexpr int kThreads = 256;
-constexpr float kScale = 8192.f, kRScale = 1.f / 8192.f;
-constexpr int kBK = 32;                 // k of an LDS stage: one 128-byte piece (hi, lo) of a row
+constexpr float kScale = 8192.f, kRScale = 1.f / 8192.f, kScaleD = 512.f;
+constexpr int kBK = 16;                 // k of an LDS stage: one 64-byte piece (hi, lo) of a row
 constexpr int kRowB = kBK * 4;
+constexpr int kSlots = 4;               // LDS stages: one read, up to three in flight
 
-// A split matrix holds a row's values in pieces of 32: 32 hi, then 32 lo.
-__device__ inline int64_t split_at(int64_t row, int64_t cols, int64_t c) {
-  return row * (2 * cols) + (c >> 5) * 64 + (c & 31);
+// A split matrix of `rows` rows is kept in the order of the MFMA's operands:
+// for each 16 columns and 32 rows 2 KB, 1 KB of hi values and 1 KB of lo ones,
+// each as lane 32 h + r holds them: 8 columns from 8 h of row r.  A fragment
+// is 1 KB of consecutive memory, a stage of a tile one consecutive run, and
+// both are read from LDS without bank conflicts as they lie.
+constexpr int kLo = 512;   // from a hi value to its lo one
+__device__ inline int64_t split_at(int64_t row, int64_t rows, int64_t c) {
+  return ((c >> 4) * rows + (row & ~31)) * 32 + ((c >> 3) & 1) * 256 + (row & 31) * 8 + (c & 7);
 }
-__device__ inline void split_put(f16* m, int64_t at, float v) {
-  const f16 hi = (f16)v;
-  m[at] = hi;
-  m[at + 32] = (f16)(v - (float)hi);
+__device__ inline void split8(const float (&v)[8], f16* at) {
+  f16x8 hi, lo;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    hi[e] = (f16)v[e];
+    lo[e] = (f16)(v[e] - (float)hi[e]);
+  }
+  *reinterpret_cast<f16x8*>(at) = hi;
+  *reinterpret_cast<f16x8*>(at + kLo) = lo;
 }
-__device__ inline float split_get(const f16* m, int64_t at) { return (float)m[at] + (float)m[at + 32]; }
 
 template <bool BF16> __device__ inline float get1(const void* p, int64_t i) {
   if constexpr (BF16) return bf16_to_f32(static_cast<const uint16_t*>(p)[i]);
@@ -52,6 +74,36 @@ template <bool BF16> __device__ inline float get1(const void* p, int64_t i) {
 template <bool BF16> __device__ inline void put1(void* p, int64_t i, float v) {
   if constexpr (BF16) static_cast<uint16_t*>(p)[i] = __builtin_bit_cast(uint16_t, (__bf16)v);
   else static_cast<float*>(p)[i] = v;
+}
+
+template <bool BF16> __device__ inline void get8(const void* p, int64_t i, float (&v)[8]) {
+  if constexpr (BF16) {
+    const uint4 r = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + i);
+    const uint32_t d[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      v[2 * e] = __uint_as_float(d[e] << 16);
+      v[2 * e + 1] = __uint_as_float(d[e] & 0xFFFF0000u);
+    }
+  } else {
+    const f32x4* q = reinterpret_cast<const f32x4*>(static_cast<const float*>(p) + i);
+    const f32x4 a = q[0], b = q[1];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) { v[e] = a[e]; v[4 + e] = b[e]; }
+  }
+}
+template <bool BF16> __device__ inline void put8(void* p, int64_t i, const float (&v)[8]) {
+  if constexpr (BF16) {
+    uint32_t d[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      d[e] = __builtin_bit_cast(uint16_t, (__bf16)v[2 * e]) | ((uint32_t)__builtin_bit_cast(uint16_t, (__bf16)v[2 * e + 1]) << 16);
+    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + i) = make_uint4(d[0], d[1], d[2], d[3]);
+  } else {
+    f32x4* q = reinterpret_cast<f32x4*>(static_cast<float*>(p) + i);
+    q[0] = f32x4{v[0], v[1], v[2], v[3]};
+    q[1] = f32x4{v[4], v[5], v[6], v[7]};
+  }
 }
 
 // Momentum, and the sum of squares of u in doubles (no overflow or underflow
@@ -80,14 +132,21 @@ __global__ __launch_bounds__(kThreads) void muon_momentum(MuonArgs a, float* __r
   if (threadIdx.x == 0) sums[c * gridDim.x + blockIdx.x] = (part[0] + part[1]) + (part[2] + part[3]);
 }
 
-// u / (|u| + eps) as split rows and as split columns, zeros in the padding:
-// 32 x 32 tiles, transposed through LDS.
+constexpr int kPad = 36;   // floats of a scratch row: 32 and a pad, 16-byte aligned
+
+struct SplitOut {
+  f16* m;
+  int64_t rows, size;   // rows and halves of one matrix
+};
+
+// u / (|u| + eps) as split rows and as split columns, zeros in the padding: a
+// wave per 32 x 32 tile, transposed through LDS.
 __global__ __launch_bounds__(kThreads) void muon_split(const float* __restrict__ u, const double* __restrict__ sums,
                                                        int parts, float eps, int64_t n, int64_t k, int64_t np,
-                                                       int64_t kp, f16* __restrict__ rows, f16* __restrict__ cols) {
+                                                       int64_t kp, SplitOut rows, SplitOut cols) {
   __shared__ double part[kThreads];
-  __shared__ float tile[32][33];
-  const int64_t c = blockIdx.z;
+  __shared__ __attribute__((aligned(16))) float scratch[4][32 * kPad];
+  const int64_t c = blockIdx.y;
   double s = 0.0;
   for (int i = threadIdx.x; i < parts; i += kThreads) s += sums[c * parts + i];
   part[threadIdx.x] = s;
@@ -97,191 +156,537 @@ __global__ __launch_bounds__(kThreads) void muon_split(const float* __restrict__
     __syncthreads();
   }
   const float mul = (float)((double)kScale / (sqrt(part[0]) + (double)eps));
-  const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
-  const int64_t n0 = (int64_t)blockIdx.y * 32, k0 = (int64_t)blockIdx.x * 32;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  float* mine = scratch[wave];
   u += c * n * k;
-  rows += c * np * kp * 2;
-  cols += c * np * kp * 2;
-  for (int i = y; i < 32; i += 8) {
-    const float v = n0 + i < n && k0 + x < k ? u[(n0 + i) * k + k0 + x] * mul : 0.f;
-    split_put(rows, split_at(n0 + i, kp, k0 + x), v);
-    tile[i][x] = v;
+  rows.m += c * rows.size;
+  cols.m += c * cols.size;
+  const bool vec = k % 4 == 0;   // u is 256-byte aligned
+  const int64_t tiles_k = kp / 32, tiles = np / 32 * tiles_k;
+  for (int64_t t = (int64_t)blockIdx.x * 4 + wave; t < tiles; t += (int64_t)gridDim.x * 4) {
+    const int64_t n0 = t / tiles_k * 32, k0 = t % tiles_k * 32;
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = i * 8 + (lane >> 3), q = (lane & 7) * 4;
+      f32x4 v{0.f, 0.f, 0.f, 0.f};
+      if (n0 + r < n) {
+        const float* src = u + (n0 + r) * k + k0 + q;
+        if (vec) {
+          if (k0 + q < k) v = *reinterpret_cast<const f32x4*>(src);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (k0 + q + e < k) v[e] = src[e];
+        }
+      }
+      *reinterpret_cast<f32x4*>(mine + r * kPad + q) = v * mul;
+    }
+    __builtin_amdgcn_wave_barrier();
+    const int r = lane & 31, h = lane >> 5;
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+      float v[8], w[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        v[e] = mine[r * kPad + p * 16 + h * 8 + e];
+        w[e] = mine[(p * 16 + h * 8 + e) * kPad + r];
+      }
+      split8(v, rows.m + split_at(n0 + r, rows.rows, k0 + p * 16 + h * 8));
+      split8(w, cols.m + split_at(k0 + r, cols.rows, n0 + p * 16 + h * 8));
+    }
   }
-  __syncthreads();
-  for (int i = y; i < 32; i += 8) split_put(cols, split_at(k0 + i, np, n0 + x), tile[x][i]);
 }
 
-enum { kGram, kSquare, kApply, kLast };
+enum { kSym, kApply, kLast };
 
-struct ProductArgs {
-  const f16 *p, *q;        // split rows [rows of C, K], [columns of C, K]
-  const f16* own;          // kSquare: A; kApply, kLast: X in C's orientation
-  f16 *out, *out_t;        // C and its transpose (kGram, kSquare: the same matrix)
-  int64_t p_size, q_size, c_size;   // halves of one matrix
-  int64_t kdim, c_cols, ct_cols;
-  int tiles_m, tiles_n;
-  float ca, cb, cc;
+// C = kp P Q^T + k1 own1 + k2 own2, split rows.  Scales are folded into the factors.
+struct Product {
+  const f16 *p, *q;          // split rows [rows of C, K], [columns of C, K]
+  const f16 *own1, *own2;    // C's shape and orientation, or null
+  f16 *out, *out_t;          // C and its transpose (kSym: one matrix)
+  float kp, k1, k2;
+};
+struct ProductShape {
+  int64_t p_size, q_size, c_size, ct_size;   // halves of one matrix
+  int64_t kdim, p_rows, q_rows, c_rows, ct_rows;
+  int64_t c_high, c_wide;           // C's padded size
+  int count;                        // matrices of one product
+  int splits;                       // K ranges of a tile, joined by muon_join
+  int tiles_m, tiles_n, tiles;      // tiles of one matrix
+};
+struct ProductPair {
+  Product g[2];                     // independent products of one shape
 };
 
-// C = P Q^T by TILE x TILE tiles: four waves of TILE/2 x TILE/2, stages of 32 k
-// (both planes of both operands) copied straight into LDS one stage ahead.
-// The 16-byte chunks of a 128-byte LDS row are XORed with half the row's
-// number, so the 16 rows of a fragment read cover every bank once.
-template <int TILE, int EPI, bool BF16>
-__global__ __launch_bounds__(kThreads) void muon_product(ProductArgs g, MuonArgs m) {
-  constexpr int W = TILE / 2, S = W / 32;           // wave tile, 32 x 32 products of it
-  constexpr int kCopies = TILE * 2 / 8 / 4;         // 1 KB copies a wave and stage
-  __shared__ __attribute__((aligned(16))) char lds[2][2 * TILE * kRowB];
+template <int TM_, int TN_, int WM_, int WN_>
+struct Tile {   // WM x WN waves, each of TM x TN 32 x 32 products
+  static constexpr int TM = TM_, TN = TN_, WM = WM_, WN = WN_;
+  static constexpr int kRows = 32 * TM * WM, kCols = 32 * TN * WN, kWaves = WM * WN;
+};
+
+// Tile number -> (ti, tj); kSym: tiles that reach above the diagonal, row by
+// row (tiles WIDE times as wide as high).
+template <int EPI, int WIDE = 1>
+__device__ inline void tile_at(const ProductShape& sh, int at, int& ti, int& tj) {
+  if constexpr (EPI == kSym) {
+    ti = 0;
+    while (at >= sh.tiles_n - ti / WIDE) at -= sh.tiles_n - ti++ / WIDE;
+    tj = ti / WIDE + at;
+  } else if (sh.tiles_m < sh.tiles_n) {   // the shorter side inside: an XCD's run needs fewer rows of the longer one
+    ti = at % sh.tiles_m;
+    tj = at / sh.tiles_m;
+  } else {
+    ti = at / sh.tiles_n;
+    tj = at % sh.tiles_n;
+  }
+}
+
+// Tile and K range of a workgroup.  Workgroups go to the eight XCDs in turn;
+// each XCD gets a contiguous run of (K range, tile), so its L2 holds the rows
+// that its tiles share.
+__device__ inline int run_of_xcd(int id, int all) {
+  const int per = all >> 3, rest = all & 7, x = id & 7;
+  return x * per + (x < rest ? x : rest) + (id >> 3);
+}
+
+// Finish of one 32 x 32 product: its sums go through LDS (32 x kPad floats of
+// this wave) so that own values are read and results written 16 bytes a lane,
+// 1 KB of consecutive memory an instruction.  `acc` holds
+// C[8 (e / 4) + 4 h + e % 4][r] in lane 32 h + r.
+template <int EPI, bool BF16>
+__device__ inline void finish(const Product& g, const ProductShape& sh, const MuonArgs& m, int64_t c, int64_t row0,
+                              int64_t col0, const f32x16& acc, float* scratch) {
+  if (EPI == kSym && col0 < row0) return;   // written by the product above the diagonal
+  const bool mirror = EPI == kApply || (EPI == kSym && col0 > row0);
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int e = 0; e < 16; ++e)
+    scratch[(8 * (e / 4) + 4 * (lane >> 5) + e % 4) * kPad + (lane & 31)] = acc[e] * g.kp;
+  __builtin_amdgcn_wave_barrier();
+  const int r = lane & 31, h = lane >> 5;
+  // own values of 8 columns of a row added to v
+  auto add_own = [&](const f16* own, float k, int64_t row, int64_t col, float (&v)[8]) {
+    own += c * sh.c_size + split_at(row, sh.c_rows, col);
+    const f16x8 hi = *reinterpret_cast<const f16x8*>(own), lo = *reinterpret_cast<const f16x8*>(own + kLo);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] += k * ((float)hi[e] + (float)lo[e]);
+  };
+  auto take = [&](int row, int col, float (&v)[8]) {
+    const f32x4 a = *reinterpret_cast<const f32x4*>(scratch + row * kPad + col);
+    const f32x4 b = *reinterpret_cast<const f32x4*>(scratch + row * kPad + col + 4);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) { v[e] = a[e]; v[4 + e] = b[e]; }
+  };
+  if constexpr (EPI == kLast) {
+    const float keep = 1.f - m.lr * m.decay, lr = m.lr * m.scale;
+    const bool wide = m.k % 8 == 0 && ((reinterpret_cast<uintptr_t>(m.w_out) | reinterpret_cast<uintptr_t>(m.w)) & 15) == 0;
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      const int lr_ = t * 16 + (lane >> 2), lc = (lane & 3) * 8;
+      const int64_t row = row0 + lr_, col = col0 + lc;
+      float v[8];
+      take(lr_, lc, v);
+      add_own(g.own1, g.k1, row, col, v);
+      if (row >= m.n || col >= m.k) continue;
+      const int64_t o = (c * m.n + row) * m.k + col;
+      if (wide) {
+        float w[8];
+        if (m.w) {
+          get8<BF16>(m.w, o, w);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[e] = w[e] * keep - lr * v[e];
+        }
+        put8<BF16>(m.w_out, o, v);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (col + e < m.k) put1<BF16>(m.w_out, o + e, m.w ? get1<BF16>(m.w, o + e) * keep - lr * v[e] : v[e]);
+      }
+    }
+    return;
+  }
+#pragma unroll
+  for (int p = 0; p < 2; ++p) {
+    const int lc = p * 16 + h * 8;
+    float v[8];
+    take(r, lc, v);
+    if (g.own1) add_own(g.own1, g.k1, row0 + r, col0 + lc, v);
+    if (EPI == kSym && g.own2) add_own(g.own2, g.k2, row0 + r, col0 + lc, v);
+    split8(v, g.out + c * sh.c_size + split_at(row0 + r, sh.c_rows, col0 + lc));
+    if (mirror) {
+      *reinterpret_cast<f32x4*>(scratch + r * kPad + lc) = f32x4{v[0], v[1], v[2], v[3]};
+      *reinterpret_cast<f32x4*>(scratch + r * kPad + lc + 4) = f32x4{v[4], v[5], v[6], v[7]};
+    }
+  }
+  __builtin_amdgcn_wave_barrier();
+  if (!mirror) return;
+#pragma unroll
+  for (int p = 0; p < 2; ++p) {
+    const int lc = p * 16 + h * 8;
+    float v[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = scratch[(lc + e) * kPad + r];
+    split8(v, g.out_t + c * sh.ct_size + split_at(col0 + r, sh.ct_rows, row0 + lc));
+  }
+  __builtin_amdgcn_wave_barrier();
+}
+
+// K loop.  A stage is 16 k of both operands, both planes: one MFMA's depth.
+// Copies go straight into LDS, three stages ahead.  The two halves of the
+// waves (one of each on every SIMD) take turns, a barrier between the turns:
+// while one reads its fragments from LDS and issues its copies, the other
+// multiplies, so the matrix cores wait for neither.
+template <class T, int EPI, bool BF16>
+__global__ __launch_bounds__(64 * T::kWaves) void muon_product(ProductPair pair, ProductShape sh, MuonArgs m,
+                                                              f32x4* __restrict__ partial) {
+  constexpr int kRows = T::kRows;
+  constexpr int kPieces = (T::kRows + T::kCols) / 16;   // 1 KB copies of a stage
+  constexpr int kCopies = kPieces / T::kWaves;
+  constexpr int kStageB = (T::kRows + T::kCols) * kRowB;
+  static_assert(kPieces % T::kWaves == 0, "whole copies a wave");
+  __shared__ __attribute__((aligned(16))) char lds[kSlots * kStageB];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wm = wave >> 1, wn = wave & 1;
-  const int64_t c = blockIdx.z;
-
+  const int wm = wave / T::WN, wn = wave % T::WN;
+  const int z = blockIdx.z;
+  const Product& g = pair.g[z >= sh.count];
+  const int64_t c = z >= sh.count ? z - sh.count : z;
+  const int run = run_of_xcd(blockIdx.x, sh.tiles * sh.splits);
+  const int tile = run % sh.tiles, split = run / sh.tiles;
   int ti, tj;
-  if constexpr (EPI == kGram || EPI == kSquare) {   // tiles on and above the diagonal, row by row
-    int left = blockIdx.x;
-    ti = 0;
-    while (left >= g.tiles_m - ti) left -= g.tiles_m - ti++;
-    tj = ti + left;
-  } else {
-    ti = blockIdx.x / g.tiles_n;
-    tj = blockIdx.x % g.tiles_n;
-  }
-  const int64_t i0 = (int64_t)ti * TILE, j0 = (int64_t)tj * TILE;
-  const int64_t pitch = g.kdim * 4;                 // bytes of a split row
+  tile_at<EPI, T::kCols / T::kRows>(sh, tile, ti, tj);
+  const int64_t i0 = (int64_t)ti * T::kRows, j0 = (int64_t)tj * T::kCols;
+  const int p_pitch = (int)(sh.p_rows * kRowB), q_pitch = (int)(sh.q_rows * kRowB);   // bytes of 16 columns
   const __amdgpu_buffer_rsrc_t pr = __builtin_amdgcn_make_buffer_rsrc(
-      const_cast<f16*>(g.p + c * g.p_size + i0 * g.kdim * 2), (short)0, (int)(TILE * pitch), kBufferWord3);
+      const_cast<f16*>(g.p + c * sh.p_size + i0 * 32), (short)0, (int)((sh.p_size - i0 * 32) * 2), kBufferWord3);
   const __amdgpu_buffer_rsrc_t qr = __builtin_amdgcn_make_buffer_rsrc(
-      const_cast<f16*>(g.q + c * g.q_size + j0 * g.kdim * 2), (short)0, (int)(TILE * pitch), kBufferWord3);
+      const_cast<f16*>(g.q + c * sh.q_size + j0 * 32), (short)0, (int)((sh.q_size - j0 * 32) * 2), kBufferWord3);
 
   auto issue = [&](int slot, int stage) {
 #pragma unroll
     for (int i = 0; i < kCopies; ++i) {
-      const int piece = wave * kCopies + i;         // 8 rows: of P, then of Q
-      const int row = (piece * 8) % TILE + (lane >> 3);
-      const uint32_t chunk = (uint32_t)((lane & 7) ^ ((row >> 1) & 7));
-      const uint32_t off = (uint32_t)(row * pitch) + chunk * 16u + (uint32_t)stage * kRowB;
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(piece * 8 < TILE ? pr : qr, (lds_void*)(lds[slot] + piece * 1024), 16,
-                                               off, 0, 0, 0);
+      const int piece = wave * kCopies + i;             // 16 rows: of P, then of Q
+      const bool in_p = piece * 16 < kRows;
+      const uint32_t off = (uint32_t)(in_p ? piece : piece - kRows / 16) * 1024 + (uint32_t)lane * 16;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(in_p ? pr : qr, (lds_void*)(lds + slot * kStageB + piece * 1024), 16,
+                                               off, stage * (in_p ? p_pitch : q_pitch), 0, 0);
     }
   };
 
-  f32x16 acc[S][S];
+  f32x16 acc[T::TM][T::TN];
 #pragma unroll
-  for (int i = 0; i < S; ++i)
+  for (int i = 0; i < T::TM; ++i)
 #pragma unroll
-    for (int j = 0; j < S; ++j)
+    for (int j = 0; j < T::TN; ++j)
 #pragma unroll
       for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.f;
 
-  const int r = lane & 31, h = lane >> 5;
-  auto frag = [&](const char* base, int row, int chunk) {
-    return *reinterpret_cast<const f16x8*>(base + row * kRowB + ((chunk ^ ((row >> 1) & 7)) << 4));
+  struct Frags {
+    f16x8 ph[T::TM], pl[T::TM], qh[T::TN], ql[T::TN];
   };
-  const int stages = (int)(g.kdim / kBK);
-  issue(0, 0);
-  for (int s = 0; s < stages; ++s) {
-    wait_vmcnt<0>();
-    lds_barrier();                                  // stage s is here, and stage s - 1 has been read
-    if (s + 1 < stages) issue((s + 1) & 1, s + 1);
-    const char* pb = lds[s & 1];
-    const char* qb = pb + TILE * kRowB;
+  auto read = [&](Frags& f, int slot) {
+    const char* pb = lds + slot * kStageB + wm * T::TM * 2048 + lane * 16;
+    const char* qb = lds + slot * kStageB + kRows * kRowB + wn * T::TN * 2048 + lane * 16;
 #pragma unroll
-    for (int kk = 0; kk < 2; ++kk) {
-      f16x8 ph[S], pl[S], qh[S], ql[S];
-#pragma unroll
-      for (int i = 0; i < S; ++i) {
-        ph[i] = frag(pb, wm * W + i * 32 + r, kk * 2 + h);
-        pl[i] = frag(pb, wm * W + i * 32 + r, 4 + kk * 2 + h);
-        qh[i] = frag(qb, wn * W + i * 32 + r, kk * 2 + h);
-        ql[i] = frag(qb, wn * W + i * 32 + r, 4 + kk * 2 + h);
-      }
-#pragma unroll
-      for (int i = 0; i < S; ++i)
-#pragma unroll
-        for (int j = 0; j < S; ++j) {
-          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(ph[i], ql[j], acc[i][j], 0, 0, 0);
-          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(pl[i], qh[j], acc[i][j], 0, 0, 0);
-          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(ph[i], qh[j], acc[i][j], 0, 0, 0);
-        }
+    for (int j = 0; j < T::TN; ++j) {
+      f.qh[j] = *reinterpret_cast<const f16x8*>(qb + j * 2048);
+      f.ql[j] = *reinterpret_cast<const f16x8*>(qb + j * 2048 + 1024);
     }
+#pragma unroll
+    for (int i = 0; i < T::TM; ++i) {
+      f.ph[i] = *reinterpret_cast<const f16x8*>(pb + i * 2048);
+      f.pl[i] = *reinterpret_cast<const f16x8*>(pb + i * 2048 + 1024);
+    }
+  };
+  auto multiply = [&](const Frags& f) {
+#pragma unroll
+    for (int i = 0; i < T::TM; ++i) {
+#pragma unroll
+      for (int j = 0; j < T::TN; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(f.ph[i], f.ql[j], acc[i][j], 0, 0, 0);
+#pragma unroll
+      for (int j = 0; j < T::TN; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(f.pl[i], f.qh[j], acc[i][j], 0, 0, 0);
+#pragma unroll
+      for (int j = 0; j < T::TN; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(f.ph[i], f.qh[j], acc[i][j], 0, 0, 0);
+    }
+  };
+  const int all = (int)(sh.kdim / kBK);
+  const int s0 = (int)((int64_t)all * split / sh.splits), s1 = (int)((int64_t)all * (split + 1) / sh.splits);
+  const int stages = s1 - s0;                           // at least 4 (the plan's K ranges)
+  auto copy = [&](int t) { issue(t & (kSlots - 1), s0 + t); };
+#pragma unroll
+  for (int t = 0; t < kSlots - 1; ++t) copy(t);
+  wait_vmcnt<2 * kCopies>();
+  lds_barrier();                                        // stage 0 is here
+  const bool second = wave >= T::kWaves / 2;
+  if (second) lds_barrier();
+  for (int t = 0; t < stages; ++t) {
+    Frags f;
+    read(f, t & (kSlots - 1));
+    if (t + 3 < stages) copy(t + 3);                    // into the slot that both halves have read
+    if (t + 3 < stages) wait_vmcnt<2 * kCopies>();      // this wave's part of stage t + 1 is here
+    else wait_vmcnt<0>();
+    lds_barrier();
+    __builtin_amdgcn_s_setprio(1);
+    multiply(f);
+    __builtin_amdgcn_s_setprio(0);
+    lds_barrier();
   }
+  if (!second) lds_barrier();
 
-  // lane holds C[8 (e / 4) + 4 h + e % 4][r] of each 32 x 32 product
-  const f16* own = g.own + c * g.c_size;
-  f16* out = g.out + c * g.c_size;
-  f16* out_t = g.out_t + c * g.c_size;
-  const float lr = m.lr * m.scale, keep = 1.f - m.lr * m.decay;
+  if (sh.splits > 1) {   // [z][tile][split][wave][product][4 rows][lane]
+    partial += ((((int64_t)z * sh.tiles + tile) * sh.splits + split) * T::kWaves + wave) * (T::TM * T::TN * 4 * 64) + lane;
 #pragma unroll
-  for (int i = 0; i < S; ++i)
+    for (int i = 0; i < T::TM; ++i)
 #pragma unroll
-    for (int j = 0; j < S; ++j)
+      for (int j = 0; j < T::TN; ++j)
 #pragma unroll
-      for (int e4 = 0; e4 < 4; ++e4) {
-        const int64_t row = i0 + wm * W + i * 32 + e4 * 8 + h * 4;
-        const int64_t col = j0 + wn * W + j * 32 + r;
-        f16x4 hi, lo;
+        for (int e4 = 0; e4 < 4; ++e4)
+          partial[((i * T::TN + j) * 4 + e4) * 64] =
+              f32x4{acc[i][j][4 * e4], acc[i][j][4 * e4 + 1], acc[i][j][4 * e4 + 2], acc[i][j][4 * e4 + 3]};
+    return;
+  }
+  __syncthreads();   // every wave has read its last stage: LDS becomes scratch
+  auto end = [&](int i, int j, const f32x16& v, float* scratch) {
+    finish<EPI, BF16>(g, sh, m, c, i0 + (wm * T::TM + i) * 32, j0 + (wn * T::TN + j) * 32, v,
+                      scratch);
+  };
+  float* scratch = reinterpret_cast<float*>(lds) + wave * (32 * kPad);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          float v = acc[i][j][e4 * 4 + e] * kRScale;
-          const int64_t at = split_at(row + e, g.c_cols, col);
-          if constexpr (EPI == kSquare) v = g.cb * split_get(own, at) + g.cc * v;
-          if constexpr (EPI == kApply || EPI == kLast) v = g.ca * split_get(own, at) + v;
-          if constexpr (EPI == kLast) {
-            if (row + e < m.n && col < m.k) {
-              const int64_t o = (c * m.n + row + e) * m.k + col;
-              const float w = v * kRScale;
-              put1<BF16>(m.w_out, o, m.w ? get1<BF16>(m.w, o) * keep - lr * w : w);
-            }
-          } else {
-            hi[e] = (f16)v;
-            lo[e] = (f16)(v - (float)hi[e]);
-            out[at] = hi[e];
-            out[at + 32] = lo[e];
-          }
-        }
-        if constexpr (EPI != kLast) {
-          if (EPI == kApply || ti != tj) {
-            f16* t = out_t + split_at(col, g.ct_cols, row);
-            *reinterpret_cast<f16x4*>(t) = hi;
-            *reinterpret_cast<f16x4*>(t + 32) = lo;
-          }
-        }
-      }
+  for (int i = 0; i < T::TM; ++i)
+#pragma unroll
+    for (int j = 0; j < T::TN; ++j) end(i, j, acc[i][j], scratch);
 }
 
-template <int TILE, int EPI, bool BF16 = false>
-hipError_t product(const ProductArgs& g, const MuonArgs& m, hipStream_t s) {
-  const int tiles = EPI == kGram || EPI == kSquare ? g.tiles_m * (g.tiles_m + 1) / 2 : g.tiles_m * g.tiles_n;
-  hipLaunchKernelGGL((muon_product<TILE, EPI, BF16>), dim3((unsigned)tiles, 1, (unsigned)m.count), dim3(kThreads), 0,
-                     s, g, m);
+// Sums of a split tile's partials, in split order, and the product's finish:
+// one wave per 32 x 32 product.
+template <class T, int EPI, bool BF16>
+__global__ __launch_bounds__(64) void muon_join(ProductPair pair, ProductShape sh, MuonArgs m,
+                                                const f32x4* __restrict__ partial) {
+  constexpr int kPer = T::TM * T::TN;
+  __shared__ __attribute__((aligned(16))) float scratch[32 * kPad];
+  const int z = blockIdx.z;
+  const Product& g = pair.g[z >= sh.count];
+  const int64_t c = z >= sh.count ? z - sh.count : z;
+  const int tile = blockIdx.x / (T::kWaves * kPer), at = blockIdx.x % (T::kWaves * kPer);
+  const int wave = at / kPer, i = at % kPer / T::TN, j = at % T::TN;
+  int ti, tj;
+  tile_at<EPI, T::kCols / T::kRows>(sh, tile, ti, tj);
+  partial += (((int64_t)z * sh.tiles + tile) * sh.splits * T::kWaves + wave) * (kPer * 4 * 64) + at % kPer * 256 + threadIdx.x;
+  f32x16 s;
+#pragma unroll
+  for (int e = 0; e < 16; ++e) s[e] = 0.f;
+  for (int k = 0; k < sh.splits; ++k)
+#pragma unroll
+    for (int e4 = 0; e4 < 4; ++e4) {
+      const f32x4 v = partial[(int64_t)k * T::kWaves * (kPer * 4 * 64) + e4 * 64];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[4 * e4 + e] += v[e];
+    }
+  finish<EPI, BF16>(g, sh, m, c, (int64_t)ti * T::kRows + (wave / T::WN * T::TM + i) * 32,
+                    (int64_t)tj * T::kCols + (wave % T::WN * T::TN + j) * 32, s, scratch);
+}
+
+// The same for small matrices, where a launch has few tiles and latency counts:
+// every wave of the workgroup takes a part of K of one tile, its fragments
+// straight from memory into registers (no LDS stage, no barrier in the loop),
+// kAhead steps ahead; the parts are added through LDS in wave order.
+template <int TM, int TN, int W, int EPI, bool BF16>
+__global__ __launch_bounds__(64 * W) void muon_product_small(ProductPair pair, ProductShape sh, MuonArgs m) {
+  constexpr int kAhead = TM * TN == 1 ? 8 : TM * TN == 4 ? 4 : 2;
+  constexpr int kProducts = TM * TN;
+  constexpr int kRound = kProducts <= 4 ? kProducts : TN;   // products added at a time (LDS)
+  __shared__ f32x4 part[W][kRound][4][64];
+  __shared__ __attribute__((aligned(16))) float scratch[kRound][32 * kPad];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int z = blockIdx.z;
+  const Product& g = pair.g[z >= sh.count];
+  const int64_t c = z >= sh.count ? z - sh.count : z;
+  int ti, tj;
+  tile_at<EPI>(sh, run_of_xcd(blockIdx.x, sh.tiles), ti, tj);
+  const int64_t i0 = (int64_t)ti * (32 * TM), j0 = (int64_t)tj * (32 * TN);
+  const f16* pp = g.p + c * sh.p_size + i0 * 32 + lane * 8;
+  const f16* qp = g.q + c * sh.q_size + j0 * 32 + lane * 8;
+  const int64_t p_pitch = sh.p_rows * 32, q_pitch = sh.q_rows * 32;   // 16 columns
+  const int all = (int)(sh.kdim / kBK);
+  const int s0 = all * wave / W, s1 = all * (wave + 1) / W;
+
+  struct Frags {
+    f16x8 ph[TM], pl[TM], qh[TN], ql[TN];
+  } f[kAhead];
+  auto load = [&](Frags& x, int s) {
+    const f16* p = pp + s * p_pitch;
+    const f16* q = qp + s * q_pitch;
+#pragma unroll
+    for (int i = 0; i < TM; ++i) {
+      x.ph[i] = *reinterpret_cast<const f16x8*>(p + i * 1024);
+      x.pl[i] = *reinterpret_cast<const f16x8*>(p + i * 1024 + kLo);
+    }
+#pragma unroll
+    for (int j = 0; j < TN; ++j) {
+      x.qh[j] = *reinterpret_cast<const f16x8*>(q + j * 1024);
+      x.ql[j] = *reinterpret_cast<const f16x8*>(q + j * 1024 + kLo);
+    }
+  };
+  f32x16 acc[TM][TN];
+#pragma unroll
+  for (int i = 0; i < TM; ++i)
+#pragma unroll
+    for (int j = 0; j < TN; ++j)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.f;
+#pragma unroll
+  for (int u = 0; u < kAhead; ++u)
+    if (s0 + u < s1) load(f[u], s0 + u);
+  for (int s = s0; s < s1; s += kAhead) {
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      if (s + u < s1) {
+        const Frags& x = f[u];
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+#pragma unroll
+          for (int j = 0; j < TN; ++j) {
+            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(x.ph[i], x.ql[j], acc[i][j], 0, 0, 0);
+            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(x.pl[i], x.qh[j], acc[i][j], 0, 0, 0);
+            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(x.ph[i], x.qh[j], acc[i][j], 0, 0, 0);
+          }
+        if (s + u + kAhead < s1) load(f[u], s + u + kAhead);
+      }
+    }
+  }
+#pragma unroll
+  for (int q0 = 0; q0 < kProducts; q0 += kRound) {
+    if (q0 > 0) __syncthreads();   // the last round's sums have been read
+#pragma unroll
+    for (int q = 0; q < kRound; ++q) {
+      const f32x16& v = acc[(q0 + q) / TN][(q0 + q) % TN];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) part[wave][q][e][lane] = f32x4{v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]};
+    }
+    __syncthreads();
+    const int mine = (wave + W - q0 % W) % W;   // another set of waves each round
+    if (mine >= kRound) continue;
+    f32x16 s;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) s[e] = 0.f;
+#pragma unroll
+    for (int w = 0; w < W; ++w)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const f32x4 v = part[w][mine][q][lane];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[4 * q + e] += v[e];
+      }
+    const int at = q0 + mine;
+    finish<EPI, BF16>(g, sh, m, c, i0 + at / TN * 32, j0 + at % TN * 32, s, scratch[mine]);
+  }
+}
+
+template <int EPI>
+int tiles_of(const ProductShape& sh, int wide) {
+  if (EPI != kSym) return sh.tiles_m * sh.tiles_n;
+  int all = 0;
+  for (int i = 0; i < sh.tiles_m; ++i) all += sh.tiles_n - i / wide;
+  return all;
+}
+
+template <int TM, int TN, int W, int EPI, bool BF16>
+hipError_t product_small(const ProductPair& g, int pairs, ProductShape sh, const MuonArgs& m, hipStream_t s) {
+  sh.tiles = tiles_of<EPI>(sh, 1);
+  hipLaunchKernelGGL((muon_product_small<TM, TN, W, EPI, BF16>),
+                     dim3((unsigned)sh.tiles, 1, (unsigned)(pairs * sh.count)), dim3(64 * W), 0, s, g, sh, m);
   return hipGetLastError();
 }
 
-template <int TILE>
+typedef Tile<2, 2, 2, 4> TileBig;   // 128 x 256
+
+template <class T, int EPI, bool BF16>
+hipError_t product_t(const ProductPair& g, int pairs, ProductShape sh, const MuonArgs& m, f32x4* partial,
+                     hipStream_t s) {
+  sh.tiles = tiles_of<EPI>(sh, T::kCols / T::kRows);
+  const unsigned z = (unsigned)(pairs * sh.count);
+  hipLaunchKernelGGL((muon_product<T, EPI, BF16>), dim3((unsigned)(sh.tiles * sh.splits), 1, z),
+                     dim3(64 * T::kWaves), 0, s, g, sh, m, partial);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || sh.splits == 1) return e;
+  hipLaunchKernelGGL((muon_join<T, EPI, BF16>), dim3((unsigned)(sh.tiles * T::kWaves * T::TM * T::TN), 1, z),
+                     dim3(64), 0, s, g, sh, m, partial);
+  return hipGetLastError();
+}
+
+template <int EPI, bool BF16 = false>
+hipError_t product(const ProductPair& g, int pairs, ProductShape sh, MuonCut cut, const MuonArgs& m, f32x4* partial,
+                   hipStream_t s) {
+  sh.tiles_m = (int)(sh.c_high / cut.rows);
+  sh.tiles_n = (int)(sh.c_wide / cut.cols);
+  sh.splits = cut.splits;
+  if (cut.rows == 128) return product_t<TileBig, EPI, BF16>(g, pairs, sh, m, partial, s);
+  if (cut.rows == 64) return product_small<2, 2, 4, EPI, BF16>(g, pairs, sh, m, s);
+  return product_small<1, 1, 4, EPI, BF16>(g, pairs, sh, m, s);
+}
+
 hipError_t steps(const MuonPlan& p, const MuonArgs& m, bool bf16, char* ws, hipStream_t s) {
-  f16* x = reinterpret_cast<f16*>(ws + p.x);
-  f16* xt[2] = {reinterpret_cast<f16*>(ws + p.xt0), reinterpret_cast<f16*>(ws + p.xt1)};
-  f16* a = reinterpret_cast<f16*>(ws + p.a);
-  f16* b = reinterpret_cast<f16*>(ws + p.b);
-  const int64_t xs = p.rp * p.lp * 2, as = p.rp * p.rp * 2;
-  const int tr = (int)(p.rp / TILE), tl = (int)(p.lp / TILE);
-  for (int i = 0; i < m.steps; ++i) {
-    const bool last = i + 1 == m.steps;
-    f16 *now = xt[i & 1], *next = xt[(i + 1) & 1];
-    hipError_t e;
-    const ProductArgs gram{x, x, x, a, a, xs, xs, as, p.lp, p.rp, p.rp, tr, tr, m.ca, m.cb, m.cc};
-    if ((e = product<TILE, kGram>(gram, m, s)) != hipSuccess) return e;
-    const ProductArgs square{a, a, a, b, b, as, as, as, p.rp, p.rp, p.rp, tr, tr, m.ca, m.cb, m.cc};
-    if ((e = product<TILE, kSquare>(square, m, s)) != hipSuccess) return e;
-    if (!last) {
-      const ProductArgs apply{b, now, x, x, next, as, xs, xs, p.rp, p.lp, p.rp, tr, tl, m.ca, m.cb, m.cc};
-      e = product<TILE, kApply>(apply, m, s);
+  auto at = [&](size_t o) { return reinterpret_cast<f16*>(ws + o); };
+  f16 *x = at(p.x), *xt[2] = {at(p.xt0), at(p.xt1)}, *a = at(p.a), *b = at(p.b), *pa = at(p.pa);
+  f16* d[2] = {at(p.d0), at(p.d1)};
+  f32x4* partial = reinterpret_cast<f32x4*>(ws + p.partial);
+  const int64_t xs = p.rp * p.lp * 2, as = p.rp * p.rp * 2, R = p.rp, L = p.lp;
+  const ProductShape gram{xs, xs, as, as, L, R, R, R, R, R, R, m.count, 1, 0, 0, 0};
+  const ProductShape sym{as, as, as, as, R, R, R, R, R, R, R, m.count, 1, 0, 0, 0};
+  const ProductShape apply{as, xs, xs, xs, R, R, L, R, L, R, L, m.count, 1, 0, 0, 0};
+  hipError_t e = hipSuccess;
+  auto run = [&](const Product& g, const ProductShape& sh, MuonCut cut) {
+    if (e == hipSuccess) e = product<kSym>(ProductPair{{g, g}}, 1, sh, cut, m, partial, s);
+  };
+  const float one = kRScale;   // a product of two values at kScale, back at kScale
+  int now = 0;
+  for (int done = 0; done < m.steps;) {
+    const int group = std::min(p.group, m.steps - done);
+    // Q = q I + D with X <- Q X after `group` steps; D at kScale for one step, kScaleD for more
+    run({x, x, nullptr, nullptr, a, a, one, 0.f, 0.f}, gram, p.gram);
+    float q = 1.f;
+    int cur = 0;
+    for (int i = 0; i < group; ++i) {
+      f16* bi = i == 0 ? d[0] : b;      // B = b A + c A A; P = a I + B
+      run({a, a, a, nullptr, bi, bi, m.cc * one, m.cb, 0.f}, sym, p.sym);
+      // A <- P A P
+      const Product half{bi, a, a, nullptr, pa, pa, one, m.ca, 0.f};
+      // D <- a D + q B + B D, of the scale of the ones before (i == 1: D is the first step's B)
+      const float sd = i == 1 ? kScale : kScaleD;
+      const Product delta{bi, d[cur], d[cur], bi, d[cur ^ 1], d[cur ^ 1], kScaleD / (kScale * sd), m.ca * (kScaleD / sd),
+                          q * (kScaleD / kScale)};
+      const bool more = i + 1 < group;
+      if (i > 0 && more) {
+        if (e == hipSuccess) e = product<kSym>(ProductPair{{half, delta}}, 2, sym, p.pair, m, partial, s);
+      } else if (i > 0) {
+        run(delta, sym, p.sym);
+      } else if (more) {
+        run(half, sym, p.sym);
+      }
+      if (i > 0) cur ^= 1;
+      if (more) run({bi, pa, pa, nullptr, a, a, one, m.ca, 0.f}, sym, p.sym);
+      q *= m.ca;
+    }
+    done += group;
+    const float kd = 1.f / (group > 1 ? kScaleD : kScale);
+    if (e != hipSuccess) return e;
+    if (done < m.steps) {
+      const Product g{d[cur], xt[now], x, nullptr, x, xt[now ^ 1], kd, q, 0.f};
+      e = product<kApply>(ProductPair{{g, g}}, 1, apply, p.apply, m, partial, s);
+      now ^= 1;
     } else {
-      // the result's own orientation: rows n, columns k
-      ProductArgs end{b, now, x, x, x, as, xs, xs, p.rp, p.lp, p.rp, tr, tl, m.ca, m.cb, m.cc};
-      if (m.n > m.k) end = ProductArgs{now, b, now, x, x, xs, as, xs, p.rp, p.rp, p.lp, tl, tr, m.ca, m.cb, m.cc};
-      e = bf16 ? product<TILE, kLast, true>(end, m, s) : product<TILE, kLast, false>(end, m, s);
+      // the result's own orientation: rows n, columns k; its values at 1
+      Product g{d[cur], xt[now], x, nullptr, nullptr, nullptr, kd * kRScale, q * kRScale, 0.f};
+      ProductShape sh = apply;
+      if (m.n > m.k) {
+        g = Product{xt[now], d[cur], xt[now], nullptr, nullptr, nullptr, kd * kRScale, q * kRScale, 0.f};
+        sh = ProductShape{xs, as, xs, xs, R, L, R, L, R, L, R, m.count, 1, 0, 0, 0};
+      }
+      const ProductPair pair{{g, g}};
+      e = bf16 ? product<kLast, true>(pair, 1, sh, p.last, m, partial, s)
+               : product<kLast, false>(pair, 1, sh, p.last, m, partial, s);
     }
     if (e != hipSuccess) return e;
   }
@@ -290,13 +695,41 @@ hipError_t steps(const MuonPlan& p, const MuonArgs& m, bool bf16, char* ws, hipS
 
 }  // namespace
 
-MuonPlan plan_muon(int count, int64_t n, int64_t k) {
+// Tile and K ranges of a product of `z` matrices C [high, wide], K deep,
+// symmetric or not.  Measured on single products from 128 to 8192 a side:
+// * up to 320 tiles of 32 x 32 (one a CU and some): these.  C 512 x 512
+//   symmetric, K 512 and 2048: 4.8 and 9.2 us against 6.8 and 14.7 us by 64 x
+//   64 tiles; C 1024 x 1024 has 528 and takes 12.6 against 10.5 us.
+// * up to 500 K tiles x k of 64 x 64: these.  C 1024 x 1024, K 1024: 10.5 us
+//   against 17.8 by the big tile; C 1024 x 4096, K 1024 (1050 K): 46.8 against 38.3.
+// * else 128 x 256 tiles through LDS, K split while the launch stays within 224
+//   workgroups, 24 stages of 16 and 8 ranges: C 2048 x 2048 symmetric, K
+//   2048: 59 us whole, 40 in 3 ranges, 51 in 4; C 1024 x 4096, K 1024: 38 whole, 41 in 2.
+static MuonCut cut_of(int64_t high, int64_t wide, int64_t k, int64_t z, bool sym) {
+  auto tiles = [&](int64_t h, int64_t w) {
+    const int64_t m = (high + h - 1) / h, n = (wide + w - 1) / w;
+    return (sym ? m * (n + 1) / 2 : m * n) * z;
+  };
+  if (tiles(32, 32) <= 320) return {32, 32, 1};
+  if (tiles(64, 64) * k <= 500000) return {64, 64, 1};
+  const int64_t most = std::min<int64_t>(std::min<int64_t>(8, k / 16 / 24), 224 / tiles(128, 256));
+  return {128, 256, (int)std::max<int64_t>(1, most)};
+}
+
+MuonPlan plan_muon(int count, int64_t n, int64_t k, bool loose) {
   MuonPlan p{};
   p.r = std::min(n, k);
   p.l = std::max(n, k);
-  p.tile = p.r > 256 ? 128 : 64;
-  p.rp = (p.r + p.tile - 1) / p.tile * p.tile;
-  p.lp = (p.l + p.tile - 1) / p.tile * p.tile;
+  p.gram = cut_of(p.r, p.r, p.l, count, true);
+  p.sym = cut_of(p.r, p.r, p.r, count, true);
+  p.pair = cut_of(p.r, p.r, p.r, 2 * (int64_t)count, true);
+  p.apply = cut_of(p.r, p.l, p.r, count, false);
+  p.last = n > k ? cut_of(p.l, p.r, p.r, count, false) : p.apply;
+  int64_t pad = 32;   // both sides, so that the tiles of every product are whole
+  for (const MuonCut& c : {p.gram, p.sym, p.pair, p.apply, p.last}) pad = std::max<int64_t>(pad, c.cols);
+  p.rp = (p.r + pad - 1) / pad * pad;
+  p.lp = (p.l + pad - 1) / pad * pad;
+  p.group = loose && p.l >= 2 * p.r ? 3 : 1;
   p.parts = std::min<int64_t>(1024, (n * k + 4 * kThreads - 1) / (4 * kThreads));
   const size_t c = (size_t)count;
   size_t at = 0;
@@ -305,13 +738,29 @@ MuonPlan plan_muon(int count, int64_t n, int64_t k) {
     at += (bytes + 255) & ~(size_t)255;
     return o;
   };
+  const size_t big = c * (size_t)(p.rp * p.lp) * 4, small = c * (size_t)(p.rp * p.rp) * 4;
   p.u = take(c * (size_t)(n * k) * 4);
   p.sums = take(c * (size_t)p.parts * 8);
-  p.x = take(c * (size_t)(p.rp * p.lp) * 4);
-  p.xt0 = take(c * (size_t)(p.rp * p.lp) * 4);
-  p.xt1 = take(c * (size_t)(p.rp * p.lp) * 4);
-  p.a = take(c * (size_t)(p.rp * p.rp) * 4);
-  p.b = take(c * (size_t)(p.rp * p.rp) * 4);
+  p.x = take(big);
+  p.xt0 = take(big);
+  p.xt1 = take(big);
+  p.a = take(small);
+  p.b = take(small);
+  p.pa = take(small);
+  p.d0 = take(small);
+  p.d1 = take(small);
+  // fp32 partials of the products with split K: a tile for each range
+  auto part = [&](const MuonCut& cut, int64_t high, int64_t wide, bool sym, size_t pairs) -> size_t {
+    if (cut.splits == 1) return 0;
+    const int64_t tm = high / cut.rows, tn = wide / cut.cols;
+    return (size_t)((sym ? tm * (tn + 1) / 2 : tm * tn) * cut.splits * cut.rows * cut.cols) * pairs * c * 4;
+  };
+  size_t most = part(p.gram, p.rp, p.rp, true, 1);
+  most = std::max(most, part(p.sym, p.rp, p.rp, true, 1));
+  most = std::max(most, part(p.pair, p.rp, p.rp, true, 2));
+  most = std::max(most, part(p.apply, p.rp, p.lp, false, 1));
+  most = std::max(most, part(p.last, p.lp, p.rp, false, 1));
+  p.partial = take(most);
   p.workspace_bytes = at;
   return p;
 }
@@ -326,13 +775,13 @@ hipError_t launch_muon(const MuonPlan& p, const MuonArgs& a, bool bf16, char* ws
   if (e != hipSuccess) return e;
   const bool wide = a.n <= a.k;
   const int64_t np = wide ? p.rp : p.lp, kp = wide ? p.lp : p.rp;
-  f16* x = reinterpret_cast<f16*>(ws + p.x);
-  f16* xt = reinterpret_cast<f16*>(ws + p.xt0);
-  hipLaunchKernelGGL(muon_split, dim3((unsigned)(kp / 32), (unsigned)(np / 32), (unsigned)a.count), dim3(kThreads), 0,
-                     s, u, sums, (int)p.parts, a.eps, a.n, a.k, np, kp, wide ? x : xt, wide ? xt : x);
+  const SplitOut x{reinterpret_cast<f16*>(ws + p.x), p.rp, p.rp * p.lp * 2};
+  const SplitOut xt{reinterpret_cast<f16*>(ws + p.xt0), p.lp, p.lp * p.rp * 2};
+  hipLaunchKernelGGL(muon_split, dim3((unsigned)std::min<int64_t>(2048, (np / 32 * (kp / 32) + 3) / 4), (unsigned)a.count),
+                     dim3(kThreads), 0, s, u, sums, (int)p.parts, a.eps, a.n, a.k, np, kp, wide ? x : xt, wide ? xt : x);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
-  return p.tile == 128 ? steps<128>(p, a, bf16, ws, s) : steps<64>(p, a, bf16, ws, s);
+  return steps(p, a, bf16, ws, s);
 }
 
 }  // namespace sherry

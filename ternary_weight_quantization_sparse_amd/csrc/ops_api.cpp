@@ -77,7 +77,10 @@ int run_muon(MuonArgs a, int32_t dtype, void* workspace, size_t workspace_bytes,
   if (!multiple_of(a.w, item) || !multiple_of(a.grad, item) || !multiple_of(a.buf, item) ||
       !multiple_of(a.w_out, item) || !multiple_of(a.buf_out, item))
     return SHERRY_ERR_ALIGN;
-  const MuonPlan plan = plan_muon(a.count, a.n, a.k);
+  // groups of steps: not for fp32 results, and only where the coefficients keep
+  // a group's product in the range of its float16 planes
+  const bool loose = (dtype == SHERRY_BF16 || a.w) && std::fabs(a.ca) <= 4.0f;
+  const MuonPlan plan = plan_muon(a.count, a.n, a.k, loose);
   if (!workspace || workspace_bytes < plan.workspace_bytes) return SHERRY_ERR_WORKSPACE;
   if (!aligned16(workspace)) return SHERRY_ERR_ALIGN;
   return hip_status(launch_muon(plan, a, dtype == SHERRY_BF16, static_cast<char*>(workspace),
@@ -191,7 +194,7 @@ int32_t sherry_adapter_gemm(int64_t n, int64_t k, int32_t granularity, int32_t g
 }
 
 size_t sherry_muon_workspace_bytes(int32_t count, int64_t n, int64_t k) {
-  return check_muon_shape(count, n, k) == SHERRY_OK ? plan_muon(count, n, k).workspace_bytes : (size_t)-1;
+  return check_muon_shape(count, n, k) == SHERRY_OK ? plan_muon(count, n, k, false).workspace_bytes : (size_t)-1;
 }
 
 int32_t sherry_orthogonalize(int32_t count, int64_t n, int64_t k, const void* g, int32_t dtype, void* out,

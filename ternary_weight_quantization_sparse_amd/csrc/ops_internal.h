@@ -91,13 +91,18 @@ struct MuonArgs {
   int steps;
   float ca, cb, cc;
 };
-struct MuonPlan {
-  int tile;                       // rows and columns of an output tile
-  int64_t r, l, rp, lp;           // smaller and larger side, padded to whole tiles
-  int64_t parts;                  // workgroups of the sum of squares
-  size_t u, sums, x, xt0, xt1, a, b, workspace_bytes;
+struct MuonCut {
+  int rows, cols, splits;         // an output tile, and the K ranges of it
 };
-MuonPlan plan_muon(int count, int64_t n, int64_t k);
+struct MuonPlan {
+  int group;                      // steps between two looks at X
+  MuonCut gram, sym, pair, apply, last;
+  int64_t r, l, rp, lp;           // smaller and larger side, and padded to whole tiles
+  int64_t parts;                  // workgroups of the sum of squares
+  size_t u, sums, x, xt0, xt1, a, b, pa, d0, d1, partial, workspace_bytes;
+};
+// loose: steps may be taken in groups (see muon.hip).
+MuonPlan plan_muon(int count, int64_t n, int64_t k, bool loose);
 hipError_t launch_muon(const MuonPlan& p, const MuonArgs& a, bool bf16, char* ws, hipStream_t s);
 
 }  // namespace sherry
