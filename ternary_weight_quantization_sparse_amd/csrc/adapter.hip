@@ -49,79 +49,118 @@ __global__ __launch_bounds__(256) void adapter_shrink(AdapterArgs ad, const uint
   if (lane == 0) v[token * ad.rank + row] = s * ad.scale[c];
 }
 
-// Decode: y = base + B_c v, a thread per output.
-template <bool YBF16>
+// Decode: y = base + B_c v.  G lanes read one output's row of b (16 bytes a
+// lane, so an instruction reads consecutive memory: a thread per output, its
+// row read alone, took 51 us for 16 x 16384 outputs of rank 64), G outputs of
+// a group in turn, and lane j keeps the j-th.
+template <int G, bool YBF16>
 __global__ __launch_bounds__(256) void adapter_expand(AdapterArgs ad, const float* __restrict__ base,
                                                       const float* __restrict__ v, int64_t n, void* __restrict__ y) {
-  const int64_t col = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int64_t token = blockIdx.y;
-  if (col >= n) return;
-  float s = base[token * n + col];
+  const int lane = threadIdx.x & 63, j = lane % G;
+  const int64_t col0 = (int64_t)blockIdx.x * 256 + (threadIdx.x & ~63);   // of the wave's 64 outputs
+  const int64_t token = blockIdx.y, col = col0 + lane;
+  if (col0 >= n) return;
+  float s = col < n ? base[token * n + col] : 0.f;
   const int c = adapter_of(ad, token);
   if (c >= 0) {
-    const int rank = adapter_rank(ad, c);
-    const uint16_t* b = ad.b + ((int64_t)c * n + col) * ad.rank;
-    float d = 0.f;
-    for (int r = 0; r < rank; ++r) d += bf16_to_f32(b[r]) * v[token * ad.rank + r];
-    s += d;
+    const int rank = adapter_rank(ad, c), live = rank - 8 * j;   // of this lane's 8 columns
+    float w[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) w[e] = e < live ? v[token * ad.rank + 8 * j + e] : 0.f;
+    const uint16_t* b = ad.b + ((int64_t)c * n + col0 + (lane - j)) * ad.rank + 8 * j;
+    u32x4 rows[G];
+#pragma unroll
+    for (int i = 0; i < G; ++i)
+      rows[i] = live > 0 && col - j + i < n ? *reinterpret_cast<const u32x4*>(b + (int64_t)i * ad.rank) : u32x4{0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int i = 0; i < G; ++i) {
+      float d = 0.f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const uint32_t u = rows[i][e / 2];
+        const float t = __uint_as_float(e % 2 ? u & 0xFFFF0000u : u << 16);
+        d += e < live ? t * w[e] : 0.f;   // columns past the rank do not count, whatever they hold
+      }
+#pragma unroll
+      for (int o = 1; o < G; o <<= 1) d += __shfl_xor(d, o);
+      if (i == j) s += d;
+    }
   }
+  if (col >= n) return;
   if constexpr (YBF16) static_cast<uint16_t*>(y)[token * n + col] = __builtin_bit_cast(uint16_t, (__bf16)s);
   else static_cast<float*>(y)[token * n + col] = s;
 }
 
-// Prefill: v of 16 tokens on MFMA (A operand: 16 rows of a, B operand: the
-// tokens), one pass over the workgroup's K range for each adapter in use among
-// them and each 64 of its rows.  The workgroup's four waves take the 32-k
-// steps in turn and add their sums through LDS, in wave order.
-__global__ __launch_bounds__(256) void adapter_shrink_mfma(AdapterArgs ad, const uint16_t* __restrict__ x, int64_t k,
-                                                           int64_t tokens, int64_t k_part, float* __restrict__ v) {
-  __shared__ f32x4 part[3][4][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+// Prefill: v of 16 tokens and 16 rows of a on MFMA (A operand: the rows, B
+// operand: the tokens).  The workgroup's waves take every 8th step of 32 k,
+// eight steps' loads in flight each, and add their sums through LDS in wave
+// order.  The tile's adapters, in rising order, go to kShrinkSlots workgroups in
+// turn, so a tile in which one request ends and the next begins takes no longer.  v is
+// kept as two bf16 terms, hi + lo (16 bits), as the product's epilogue multiplies it.
+// Latency bounds it: 16 tokens x 64 rows x 2048 k by one workgroup, adapters one after
+// another, took 23 us for 2048 tokens, so the work is spread as thin as MFMA tiles allow.
+constexpr int kShrinkWaves = 8, kShrinkAhead = 8, kShrinkSlots = 2;
+__global__ __launch_bounds__(64 * kShrinkWaves) void adapter_shrink_mfma(AdapterArgs ad, const uint16_t* __restrict__ x,
+                                                                         int64_t k, int64_t tokens,
+                                                                         uint16_t* __restrict__ vh,
+                                                                         uint16_t* __restrict__ vl) {
+  __shared__ f32x4 part[kShrinkWaves][64];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, q = lane >> 4;
+  const int r0 = blockIdx.y * 16;
   const int64_t token = (int64_t)blockIdx.x * 16 + r;
-  const int64_t k0 = (int64_t)blockIdx.y * k_part;
   const int id = token < tokens ? ad.ids[token] : -1;
-  const uint16_t* xr = x + (token < tokens ? token : tokens - 1) * k + k0 + 8 * q;
-  v += (int64_t)blockIdx.y * tokens * ad.rank;
-  for (int done = -1;;) {
+  const uint16_t* xr = x + (token < tokens ? token : tokens - 1) * k + 8 * q;
+  const int steps = (int)(k / 32);
+  int slot = 0;
+  for (int done = -1;; slot = (slot + 1) % kShrinkSlots) {
     int next = id > done && id < ad.count ? id : ad.count;
 #pragma unroll
     for (int o = 1; o < 16; o <<= 1) next = min(next, __shfl_xor(next, o));
     const int c = __builtin_amdgcn_readfirstlane(next);
     if (c >= ad.count) break;
     done = c;
+    if (slot != (int)blockIdx.z) continue;
     const int rank = adapter_rank(ad, c);
+    if (r0 >= rank) continue;
     const float scale = ad.scale[c];
-    for (int r0 = 0; r0 < rank; r0 += 64) {
-      const uint16_t* ar[4];
+    // rows past the rank repeat its last: their sums are not used
+    const uint16_t* ar = ad.a + ((int64_t)c * ad.rank + min(r0 + r, rank - 1)) * k + 8 * q;
+    f32x4 acc{0.f, 0.f, 0.f, 0.f};
+    for (int s = wave; s < steps; s += kShrinkAhead * kShrinkWaves) {
+      u32x4 xv[kShrinkAhead], av[kShrinkAhead];
 #pragma unroll
-      for (int i = 0; i < 4; ++i)   // rows past the stored ones repeat the last: never stored
-        ar[i] = ad.a + ((int64_t)c * ad.rank + min(r0 + i * 16 + r, ad.rank - 1)) * k + k0 + 8 * q;
-      f32x4 acc[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-      for (int64_t kk = 32 * wave; kk < k_part; kk += 128) {
-        const bf16x8 xv = *reinterpret_cast<const bf16x8*>(xr + kk);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (r0 + i * 16 < rank)
-            acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(*reinterpret_cast<const bf16x8*>(ar[i] + kk), xv, acc[i],
-                                                             0, 0, 0);
+      for (int u = 0; u < kShrinkAhead; ++u) {
+        // a step past the end repeats this turn's first one; it is not added
+        const int64_t at = (int64_t)(s + u * kShrinkWaves < steps ? s + u * kShrinkWaves : s) * 32;
+        xv[u] = *reinterpret_cast<const u32x4*>(xr + at);
+        av[u] = *reinterpret_cast<const u32x4*>(ar + at);
       }
-      __syncthreads();
-      if (wave > 0)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) part[wave - 1][i][lane] = acc[i];
-      __syncthreads();
-      if (wave == 0 && id == c) {
+      for (int u = 0; u < kShrinkAhead; ++u)
+        if (s + u * kShrinkWaves < steps)
+          acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, av[u]),
+                                                        __builtin_bit_cast(bf16x8, xv[u]), acc, 0, 0, 0);
+    }
+    __syncthreads();   // the last adapter's sums have been read
+    part[wave][lane] = acc;
+    __syncthreads();
+    const int row = r0 + 4 * q;   // D[row 4q + e][token r]
+    if (wave == 0 && id == c && row < ad.rank) {
+      f32x4 s = part[0][lane];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int row = r0 + i * 16 + 4 * q;   // D[row 4q + e][token r]
-          f32x4 s = acc[i];
-          for (int w = 0; w < 3; ++w) s += part[w][i][lane];
-          if (row < ad.rank) *reinterpret_cast<f32x4*>(v + token * ad.rank + row) = s * scale;
-        }
+      for (int w = 1; w < kShrinkWaves; ++w) s += part[w][lane];
+      uint32_t hi[4], lo[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float v = s[e] * scale;
+        const __bf16 h = (__bf16)v;
+        hi[e] = __builtin_bit_cast(uint16_t, h);
+        lo[e] = __builtin_bit_cast(uint16_t, (__bf16)(v - (float)h));
       }
+      *reinterpret_cast<uint2*>(vh + token * ad.rank + row) = make_uint2(hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16));
+      *reinterpret_cast<uint2*>(vl + token * ad.rank + row) = make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
     }
   }
 }
@@ -134,18 +173,12 @@ AdapterPlan plan_adapter(int64_t n, int64_t k, int gran, int group_size, int64_t
   p.base_offset = 0;
   if (decode) {
     const size_t base = plan_gemv(n, k, gran, group_size, (int)tokens, 1).workspace_bytes;
-    p.ksplit = 1;
     p.y_offset = up(base);
     p.v_offset = p.y_offset + up((size_t)tokens * (size_t)n * 4);
   } else {
-    const size_t base = plan_gemm(n, k, gran, group_size, tokens, true).workspace_bytes;
-    p.ksplit = 1;
-    const int64_t tiles = (tokens + 15) / 16;
-    while (tiles * p.ksplit < 512 && p.ksplit < 8 && k % (128 * 2 * p.ksplit) == 0) p.ksplit *= 2;
-    p.y_offset = 0;
-    p.v_offset = up(base);
+    p.v_offset = up(plan_gemm(n, k, gran, group_size, tokens, true).workspace_bytes);   // hi, then lo
   }
-  p.workspace_bytes = p.v_offset + up((size_t)p.ksplit * (size_t)tokens * (size_t)rank * 4);
+  p.workspace_bytes = p.v_offset + up((size_t)tokens * (size_t)rank * 4);
   return p;
 }
 
@@ -162,21 +195,32 @@ hipError_t launch_adapter_gemv(const AdapterPlan& p, int64_t n, int64_t k, int g
                   reinterpret_cast<float*>(ws + p.base_offset), s);
   if (e != hipSuccess) return e;
   const dim3 grid((unsigned)((n + 255) / 256), (unsigned)batch);
-  if (y_bf16) hipLaunchKernelGGL(adapter_expand<true>, grid, dim3(256), 0, s, ad, base, v, n, y);
-  else hipLaunchKernelGGL(adapter_expand<false>, grid, dim3(256), 0, s, ad, base, v, n, y);
+#define SHERRY_EXPAND(G)                                                                                       \
+  do {                                                                                                         \
+    if (y_bf16) hipLaunchKernelGGL((adapter_expand<G, true>), grid, dim3(256), 0, s, ad, base, v, n, y);       \
+    else hipLaunchKernelGGL((adapter_expand<G, false>), grid, dim3(256), 0, s, ad, base, v, n, y);             \
+  } while (0)
+  if (ad.rank <= 8) SHERRY_EXPAND(1);
+  else if (ad.rank <= 16) SHERRY_EXPAND(2);
+  else if (ad.rank <= 32) SHERRY_EXPAND(4);
+  else if (ad.rank <= 64) SHERRY_EXPAND(8);
+  else if (ad.rank <= 128) SHERRY_EXPAND(16);
+  else SHERRY_EXPAND(32);
+#undef SHERRY_EXPAND
   return hipGetLastError();
 }
 
 hipError_t launch_adapter_gemm(const AdapterPlan& p, int64_t n, int64_t k, int gran, int group_size,
                                const uint8_t* packed, const float* alpha, const uint16_t* x, int64_t m, uint16_t* y,
                                const AdapterArgs& ad, char* ws, hipStream_t s) {
-  float* v = reinterpret_cast<float*>(ws + p.v_offset);
-  hipLaunchKernelGGL(adapter_shrink_mfma, dim3((unsigned)((m + 15) / 16), (unsigned)p.ksplit), dim3(256), 0, s, ad, x,
-                     k, m, k / p.ksplit, v);
+  uint16_t* vh = reinterpret_cast<uint16_t*>(ws + p.v_offset);
+  uint16_t* vl = vh + m * ad.rank;
+  hipLaunchKernelGGL(adapter_shrink_mfma, dim3((unsigned)((m + 15) / 16), (unsigned)((ad.rank + 15) / 16), kShrinkSlots),
+                     dim3(64 * kShrinkWaves), 0, s, ad, x, k, m, vh, vl);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const GemmPlan g = plan_gemm(n, k, gran, group_size, m, true);
-  const AdapterTerm term{ad, v, p.ksplit, m * ad.rank};
+  const AdapterTerm term{ad, vh, vl};
   return launch_gemm_adapted(g, n, k, gran, group_size, packed, alpha, x, m, y,
                              reinterpret_cast<float*>(ws + p.base_offset), term, s);
 }

@@ -478,46 +478,44 @@ __global__ __launch_bounds__(kThreads, AR ? (GRAN != SHERRY_PER_GROUP || MERGE ?
         const int rank = adapter_rank(ad.a, c);
         for (int k0 = 0; k0 < rank; k0 += 32) {
           const int kr = k0 + 8 * q;            // this lane's 8 columns of b
-          bf16x8 bw[kTN];
+          u32x4 bw[kTN], vh[kTM], vl[kTM];
 #pragma unroll
           for (int i = 0; i < kTN; ++i) {
             const int64_t gn = n0 + wave * kWN + i * 16 + r;
-            u32x4 w{0u, 0u, 0u, 0u};
-            if (kr < rank && gn < n)
-              w = *reinterpret_cast<const u32x4*>(ad.a.b + ((int64_t)c * n + gn) * ad.a.rank + kr);
-            bf16x8 v = __builtin_bit_cast(bf16x8, w);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = kr + e < rank ? v[e] : (__bf16)0.f;
-            bw[i] = v;
+            bw[i] = kr < rank && gn < n ? *reinterpret_cast<const u32x4*>(ad.a.b + ((int64_t)c * n + gn) * ad.a.rank + kr)
+                                        : u32x4{0u, 0u, 0u, 0u};
           }
 #pragma unroll
           for (int jj = 0; jj < kTM; ++jj) {
-            float v[8] = {};
-            if (id[jj] == c && kr < rank) {
-              const float* src = ad.v + (m0 + jj * 16 + r) * ad.a.rank + kr;
-              for (int z = 0; z < ad.parts; ++z) {
-                const f32x4 lo4 = *reinterpret_cast<const f32x4*>(src + z * ad.part_stride);
-                const f32x4 hi4 = *reinterpret_cast<const f32x4*>(src + z * ad.part_stride + 4);
+            const bool mine = id[jj] == c && kr < rank;
+            const int64_t at = (m0 + jj * 16 + r) * ad.a.rank + kr;
+            vh[jj] = mine ? *reinterpret_cast<const u32x4*>(ad.vh + at) : u32x4{0u, 0u, 0u, 0u};
+            vl[jj] = mine ? *reinterpret_cast<const u32x4*>(ad.vl + at) : u32x4{0u, 0u, 0u, 0u};
+          }
+          // columns past the rank, in b and in v, are zero whatever they hold
+          if (kr + 8 > rank) {
+            u32x4 keep;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  v[e] += lo4[e];
-                  v[4 + e] += hi4[e];
-                }
-              }
-            }
-            bf16x8 vh, vl;
+            for (int e = 0; e < 4; ++e)
+              keep[e] = (kr + 2 * e < rank ? 0xFFFFu : 0u) | (kr + 2 * e + 1 < rank ? 0xFFFF0000u : 0u);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const float t = kr + e < rank ? v[e] : 0.f;
-              vh[e] = (__bf16)t;
-              vl[e] = (__bf16)(t - (float)vh[e]);
+            for (int i = 0; i < kTN; ++i) bw[i] &= keep;
+#pragma unroll
+            for (int jj = 0; jj < kTM; ++jj) {
+              vh[jj] &= keep;
+              vl[jj] &= keep;
             }
+          }
+#pragma unroll
+          for (int jj = 0; jj < kTM; ++jj) {
             // added by selection: an infinity or NaN in this adapter's b stays
             // with its own tokens
 #pragma unroll
             for (int i = 0; i < kTN; ++i) {
-              f32x4 d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bw[i], vl, f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
-              d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bw[i], vh, d, 0, 0, 0);
+              const bf16x8 w = __builtin_bit_cast(bf16x8, bw[i]);
+              f32x4 d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, __builtin_bit_cast(bf16x8, vl[jj]),
+                                                                f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
+              d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, __builtin_bit_cast(bf16x8, vh[jj]), d, 0, 0, 0);
 #pragma unroll
               for (int e = 0; e < 4; ++e) acc[i][jj][e] += id[jj] == c ? d[e] : 0.f;
             }
@@ -645,7 +643,8 @@ hipError_t launch_g(const GemmPlan& p, int64_t n, int64_t k, int group_sbs, cons
                        mc, group_sbs, tiles_m, tiles_n, sb_per_split, wd, lam, ad);
     if constexpr (AD) {   // the next chunk's tokens
       ad.a.ids += mc;
-      ad.v += mc * ad.a.rank;
+      ad.vh += mc * ad.a.rank;
+      ad.vl += mc * ad.a.rank;
     }
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;

@@ -54,13 +54,11 @@ struct AdapterArgs {
 __device__ inline int adapter_rank(const AdapterArgs& a, int c) {
   return a.ranks ? min(max(a.ranks[c], 0), a.rank) : a.rank;
 }
-// The adapters' term of a product: scale * a x of each token, as `parts` fp32
-// partials [tokens, rank].
+// The adapters' term of a product: scale * a x of each token, [tokens, rank],
+// as two bf16 terms.
 struct AdapterTerm {
   AdapterArgs a;
-  const float* v;
-  int parts;
-  int64_t part_stride;
+  const uint16_t *vh, *vl;
 };
 hipError_t launch_gemm_adapted(const GemmPlan& p, int64_t n, int64_t k, int gran, int group_size,
                                const uint8_t* packed, const float* alpha, const uint16_t* x, int64_t m,
@@ -68,8 +66,7 @@ hipError_t launch_gemm_adapted(const GemmPlan& p, int64_t n, int64_t k, int gran
 struct AdapterPlan {
   size_t base_offset;       // the packed product's own workspace
   size_t y_offset;          // fp32 base product (decode)
-  size_t v_offset;          // fp32 low-rank products, `ksplit` partials of [tokens, rank]
-  int ksplit;
+  size_t v_offset;          // low-rank products [tokens, rank]: fp32 (decode), or bf16 hi and lo
   size_t workspace_bytes;
 };
 AdapterPlan plan_adapter(int64_t n, int64_t k, int gran, int group_size, int64_t tokens, int rank, bool decode);
