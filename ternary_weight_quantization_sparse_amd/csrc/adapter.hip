@@ -91,24 +91,27 @@ __global__ __launch_bounds__(256) void adapter_expand(AdapterArgs ad, const floa
   else static_cast<float*>(y)[token * n + col] = s;
 }
 
-// Prefill: v of 16 tokens and 16 rows of a on MFMA (A operand: the rows, B
-// operand: the tokens).  The workgroup's waves take every 8th step of 32 k,
-// eight steps' loads in flight each, and add their sums through LDS in wave
+// Prefill: v of 16 tokens and 16 kShrinkRows rows of a on MFMA (A operand: the
+// rows, B operand: the tokens).  The workgroup's waves take every 8th step of
+// 32 k, four steps' loads in flight each, and add their sums through LDS in wave
 // order.  The tile's adapters, in rising order, go to kShrinkSlots workgroups in
-// turn, so a tile in which one request ends and the next begins takes no longer.  v is
-// kept as two bf16 terms, hi + lo (16 bits), as the product's epilogue multiplies it.
-// Latency bounds it: 16 tokens x 64 rows x 2048 k by one workgroup, adapters one after
-// another, took 23 us for 2048 tokens, so the work is spread as thin as MFMA tiles allow.
-constexpr int kShrinkWaves = 8, kShrinkAhead = 8, kShrinkSlots = 2;
+// turn, so a tile in which one request ends and the next begins takes no
+// longer.  v is kept as two bf16 terms, hi + lo (16 bits), as the product's
+// epilogue multiplies it.
+// Latency bounds it (look up the adapter, its rank, the rows): 2048 tokens x
+// 64 rows x 2048 k in 13.9 us with four row tiles a workgroup, 17.6 with one; 517
+// tokens x 16 rows in 7.1 with one, so ranks up to 16 take one.
+constexpr int kShrinkWaves = 8, kShrinkAhead = 4, kShrinkSlots = 2;
+template <int kShrinkRows>
 __global__ __launch_bounds__(64 * kShrinkWaves) void adapter_shrink_mfma(AdapterArgs ad, const uint16_t* __restrict__ x,
                                                                          int64_t k, int64_t tokens,
                                                                          uint16_t* __restrict__ vh,
                                                                          uint16_t* __restrict__ vl) {
-  __shared__ f32x4 part[kShrinkWaves][64];
+  __shared__ f32x4 part[kShrinkWaves][kShrinkRows][64];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, q = lane >> 4;
-  const int r0 = blockIdx.y * 16;
+  const int r0 = blockIdx.y * (16 * kShrinkRows);
   const int64_t token = (int64_t)blockIdx.x * 16 + r;
   const int id = token < tokens ? ad.ids[token] : -1;
   const uint16_t* xr = x + (token < tokens ? token : tokens - 1) * k + 8 * q;
@@ -126,31 +129,40 @@ __global__ __launch_bounds__(64 * kShrinkWaves) void adapter_shrink_mfma(Adapter
     if (r0 >= rank) continue;
     const float scale = ad.scale[c];
     // rows past the rank repeat its last: their sums are not used
-    const uint16_t* ar = ad.a + ((int64_t)c * ad.rank + min(r0 + r, rank - 1)) * k + 8 * q;
-    f32x4 acc{0.f, 0.f, 0.f, 0.f};
+    const uint16_t* ar[kShrinkRows];
+#pragma unroll
+    for (int i = 0; i < kShrinkRows; ++i)
+      ar[i] = ad.a + ((int64_t)c * ad.rank + min(r0 + i * 16 + r, rank - 1)) * k + 8 * q;
+    f32x4 acc[kShrinkRows];
+#pragma unroll
+    for (int i = 0; i < kShrinkRows; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
     for (int s = wave; s < steps; s += kShrinkAhead * kShrinkWaves) {
-      u32x4 xv[kShrinkAhead], av[kShrinkAhead];
+      u32x4 xv[kShrinkAhead], av[kShrinkAhead][kShrinkRows];
 #pragma unroll
       for (int u = 0; u < kShrinkAhead; ++u) {
         // a step past the end repeats this turn's first one; it is not added
         const int64_t at = (int64_t)(s + u * kShrinkWaves < steps ? s + u * kShrinkWaves : s) * 32;
         xv[u] = *reinterpret_cast<const u32x4*>(xr + at);
-        av[u] = *reinterpret_cast<const u32x4*>(ar + at);
+#pragma unroll
+        for (int i = 0; i < kShrinkRows; ++i) av[u][i] = *reinterpret_cast<const u32x4*>(ar[i] + at);
       }
 #pragma unroll
       for (int u = 0; u < kShrinkAhead; ++u)
         if (s + u * kShrinkWaves < steps)
-          acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, av[u]),
-                                                        __builtin_bit_cast(bf16x8, xv[u]), acc, 0, 0, 0);
+#pragma unroll
+          for (int i = 0; i < kShrinkRows; ++i)
+            acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, av[u][i]),
+                                                             __builtin_bit_cast(bf16x8, xv[u]), acc[i], 0, 0, 0);
     }
     __syncthreads();   // the last adapter's sums have been read
-    part[wave][lane] = acc;
-    __syncthreads();
-    const int row = r0 + 4 * q;   // D[row 4q + e][token r]
-    if (wave == 0 && id == c && row < ad.rank) {
-      f32x4 s = part[0][lane];
 #pragma unroll
-      for (int w = 1; w < kShrinkWaves; ++w) s += part[w][lane];
+    for (int i = 0; i < kShrinkRows; ++i) part[wave][i][lane] = acc[i];
+    __syncthreads();
+    const int row = r0 + wave * 16 + 4 * q;   // D[row 4q + e][token r]
+    if (wave < kShrinkRows && id == c && row < ad.rank) {
+      f32x4 s = part[0][wave][lane];
+#pragma unroll
+      for (int w = 1; w < kShrinkWaves; ++w) s += part[w][wave][lane];
       uint32_t hi[4], lo[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
@@ -215,8 +227,13 @@ hipError_t launch_adapter_gemm(const AdapterPlan& p, int64_t n, int64_t k, int g
                                const AdapterArgs& ad, char* ws, hipStream_t s) {
   uint16_t* vh = reinterpret_cast<uint16_t*>(ws + p.v_offset);
   uint16_t* vl = vh + m * ad.rank;
-  hipLaunchKernelGGL(adapter_shrink_mfma, dim3((unsigned)((m + 15) / 16), (unsigned)((ad.rank + 15) / 16), kShrinkSlots),
-                     dim3(64 * kShrinkWaves), 0, s, ad, x, k, m, vh, vl);
+  const unsigned tiles = (unsigned)((m + 15) / 16);
+  if (ad.rank <= 16)
+    hipLaunchKernelGGL(adapter_shrink_mfma<1>, dim3(tiles, 1, kShrinkSlots), dim3(64 * kShrinkWaves), 0, s, ad, x, k, m,
+                       vh, vl);
+  else
+    hipLaunchKernelGGL(adapter_shrink_mfma<4>, dim3(tiles, (unsigned)((ad.rank + 63) / 64), kShrinkSlots),
+                       dim3(64 * kShrinkWaves), 0, s, ad, x, k, m, vh, vl);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const GemmPlan g = plan_gemm(n, k, gran, group_size, m, true);

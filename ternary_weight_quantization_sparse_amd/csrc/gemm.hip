@@ -297,6 +297,29 @@ __global__ __launch_bounds__(kThreads, AR ? (GRAN != SHERRY_PER_GROUP || MERGE ?
     }
   };
 
+  // AD: the tile's tokens' adapters (in LDS through the K loop), and the
+  // smallest in use with its rank, looked up before the loop
+  __shared__ int tile_ids[AD ? kBM : 1];
+  int ad_next = 0, ad_rank = 0;
+  auto find_adapter = [&](int done) {
+    int next = ad.a.count;
+#pragma unroll
+    for (int jj = 0; jj < kTM; ++jj) {
+      const int t = tile_ids[AD ? jj * 16 + r : 0];
+      if (t > done && t < next) next = t;
+    }
+#pragma unroll
+    for (int o = 1; o < 16; o <<= 1) next = min(next, __shfl_xor(next, o));   // a row of 16 lanes holds all tokens
+    ad_next = __builtin_amdgcn_readfirstlane(next);
+    ad_rank = ad_next < ad.a.count ? __builtin_amdgcn_readfirstlane(adapter_rank(ad.a, ad_next)) : 0;
+  };
+  if constexpr (AD) {
+    if (tid < kBM) tile_ids[tid] = m0 + tid < m ? ad.a.ids[m0 + tid] : -1;
+    __syncthreads();
+    if (kz == 0) find_adapter(-1);
+    else ad_next = ad.a.count;
+  }
+
   f32x4 acc[kTN][kTM];
   f32x4 accg[C::kGroup ? kTN : 1][C::kGroup ? kTM : 1];
   constexpr bool kAccD = AR && !MERGE;
@@ -456,26 +479,13 @@ __global__ __launch_bounds__(kThreads, AR ? (GRAN != SHERRY_PER_GROUP || MERGE ?
           for (int jj = 0; jj < kTM; ++jj) acc[i][jj][e] *= sc;
         }
     }
-    if (kz == 0) {
+    if (kz == 0 && ad_next < ad.a.count) {
       int id[kTM];
 #pragma unroll
-      for (int jj = 0; jj < kTM; ++jj) {
-        const int64_t gm = m0 + jj * 16 + r;
-        id[jj] = gm < m ? ad.a.ids[gm] : -1;
-      }
-      for (int done = -1;;) {
-        // the smallest adapter in use beyond the last one: the lanes of a
-        // 16-lane row hold all the tile's tokens
-        int next = ad.a.count;
-#pragma unroll
-        for (int jj = 0; jj < kTM; ++jj)
-          if (id[jj] > done && id[jj] < next) next = id[jj];
-#pragma unroll
-        for (int o = 1; o < 16; o <<= 1) next = min(next, __shfl_xor(next, o));
-        const int c = __builtin_amdgcn_readfirstlane(next);
-        if (c >= ad.a.count) break;
-        done = c;
-        const int rank = adapter_rank(ad.a, c);
+      for (int jj = 0; jj < kTM; ++jj) id[jj] = tile_ids[jj * 16 + r];
+      while (ad_next < ad.a.count) {
+        const int c = ad_next, rank = ad_rank;
+        find_adapter(c);                        // the next one, its rank on the way
         for (int k0 = 0; k0 < rank; k0 += 32) {
           const int kr = k0 + 8 * q;            // this lane's 8 columns of b
           u32x4 bw[kTN], vh[kTM], vl[kTM];
@@ -493,7 +503,7 @@ __global__ __launch_bounds__(kThreads, AR ? (GRAN != SHERRY_PER_GROUP || MERGE ?
             vl[jj] = mine ? *reinterpret_cast<const u32x4*>(ad.vl + at) : u32x4{0u, 0u, 0u, 0u};
           }
           // columns past the rank, in b and in v, are zero whatever they hold
-          if (kr + 8 > rank) {
+          if (k0 + 32 > rank) {
             u32x4 keep;
 #pragma unroll
             for (int e = 0; e < 4; ++e)
@@ -506,10 +516,10 @@ __global__ __launch_bounds__(kThreads, AR ? (GRAN != SHERRY_PER_GROUP || MERGE ?
               vl[jj] &= keep;
             }
           }
+          // added by selection: an infinity or NaN in this adapter's b stays
+          // with its own tokens
 #pragma unroll
-          for (int jj = 0; jj < kTM; ++jj) {
-            // added by selection: an infinity or NaN in this adapter's b stays
-            // with its own tokens
+          for (int jj = 0; jj < kTM; ++jj)
 #pragma unroll
             for (int i = 0; i < kTN; ++i) {
               const bf16x8 w = __builtin_bit_cast(bf16x8, bw[i]);
@@ -519,7 +529,6 @@ __global__ __launch_bounds__(kThreads, AR ? (GRAN != SHERRY_PER_GROUP || MERGE ?
 #pragma unroll
               for (int e = 0; e < 4; ++e) acc[i][jj][e] += id[jj] == c ? d[e] : 0.f;
             }
-          }
         }
       }
     }
