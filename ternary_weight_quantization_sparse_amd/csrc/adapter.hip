@@ -16,62 +16,43 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
-__device__ inline int adapter_of(const AdapterArgs& a, int64_t token) {
-  const int c = a.ids[token];
-  return c >= 0 && c < a.count ? c : -1;
-}
-
-// 8 products of bf16 pairs, added in fp32
-__device__ inline float dot8(const u32x4 a, const u32x4 b, float s) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    s += __uint_as_float(a[i] << 16) * __uint_as_float(b[i] << 16);
-    s += __uint_as_float(a[i] & 0xFFFF0000u) * __uint_as_float(b[i] & 0xFFFF0000u);
-  }
-  return s;
-}
-
-// Decode: a wave per (token, row of a).
-__global__ __launch_bounds__(256) void adapter_shrink(AdapterArgs ad, const uint16_t* __restrict__ x, int64_t k,
-                                                      float* __restrict__ v) {
-  const int lane = threadIdx.x & 63;
-  const int row = blockIdx.x * 4 + (threadIdx.x >> 6);
-  const int64_t token = blockIdx.y;
-  if (row >= ad.rank) return;
-  const int c = adapter_of(ad, token);
-  if (c < 0 || row >= adapter_rank(ad, c)) return;   // never read
-  const u32x4* ar = reinterpret_cast<const u32x4*>(ad.a + ((int64_t)c * ad.rank + row) * k);
-  const u32x4* xr = reinterpret_cast<const u32x4*>(x + token * k);
-  float s = 0.f;
-  for (int64_t i = lane; i < k / 8; i += 64) s = dot8(ar[i], xr[i], s);
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) s += __shfl_xor(s, o);
-  if (lane == 0) v[token * ad.rank + row] = s * ad.scale[c];
-}
-
-// Decode: y = base + B_c v.  G lanes read one output's row of b (16 bytes a
-// lane, so an instruction reads consecutive memory: a thread per output, its
-// row read alone, took 51 us for 16 x 16384 outputs of rank 64), G outputs of
-// a group in turn, and lane j keeps the j-th.
+// Decode: y = (sum of the packed product's K ranges, in order) * alpha + B_c v.
+// G lanes read one output's row of b (16 bytes a lane, so an instruction reads
+// consecutive memory: a thread per output, its row read alone, took 51 us for
+// 16 x 16384 outputs of rank 64), G outputs of a group in turn, and lane j keeps the j-th.
 template <int G, bool YBF16>
-__global__ __launch_bounds__(256) void adapter_expand(AdapterArgs ad, const float* __restrict__ base,
+__global__ __launch_bounds__(256) void adapter_finish(AdapterArgs ad, const float* __restrict__ partial, int splits,
+                                                      const float* __restrict__ alpha, int gran,
                                                       const float* __restrict__ v, int64_t n, void* __restrict__ y) {
   const int lane = threadIdx.x & 63, j = lane % G;
   const int64_t col0 = (int64_t)blockIdx.x * 256 + (threadIdx.x & ~63);   // of the wave's 64 outputs
   const int64_t token = blockIdx.y, col = col0 + lane;
   if (col0 >= n) return;
-  float s = col < n ? base[token * n + col] : 0.f;
+  // b's rows are on their way while the partials are added
   const int c = adapter_of(ad, token);
+  const int live = c < 0 ? 0 : adapter_rank(ad, c) - 8 * j;   // of this lane's 8 columns
+  const uint16_t* b = ad.b + ((int64_t)(c < 0 ? 0 : c) * n + col0 + (lane - j)) * ad.rank + 8 * j;
+  u32x4 rows[G];
+#pragma unroll
+  for (int i = 0; i < G; ++i)
+    rows[i] = live > 0 && col - j + i < n ? *reinterpret_cast<const u32x4*>(b + (int64_t)i * ad.rank) : u32x4{0u, 0u, 0u, 0u};
+  const int64_t per = gridDim.y * n;
+  const float* p = partial + token * n + (col < n ? col : n - 1);
+  float s = 0.f;
+  for (int z = 0; z < splits; z += 16) {   // 16 loads ahead of their adds (one latency per 16 ranges)
+    float t[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) t[i] = z + i < splits ? p[(z + i) * per] : 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (z + i < splits) s += t[i];
+  }
+  if (gran == SHERRY_PER_CHANNEL) s *= alpha[col < n ? col : n - 1];
+  if (gran == SHERRY_PER_TENSOR) s *= alpha[0];
   if (c >= 0) {
-    const int rank = adapter_rank(ad, c), live = rank - 8 * j;   // of this lane's 8 columns
     float w[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) w[e] = e < live ? v[token * ad.rank + 8 * j + e] : 0.f;
-    const uint16_t* b = ad.b + ((int64_t)c * n + col0 + (lane - j)) * ad.rank + 8 * j;
-    u32x4 rows[G];
-#pragma unroll
-    for (int i = 0; i < G; ++i)
-      rows[i] = live > 0 && col - j + i < n ? *reinterpret_cast<const u32x4*>(b + (int64_t)i * ad.rank) : u32x4{0u, 0u, 0u, 0u};
 #pragma unroll
     for (int i = 0; i < G; ++i) {
       float d = 0.f;
@@ -182,11 +163,9 @@ __global__ __launch_bounds__(64 * kShrinkWaves) void adapter_shrink_mfma(Adapter
 AdapterPlan plan_adapter(int64_t n, int64_t k, int gran, int group_size, int64_t tokens, int rank, bool decode) {
   AdapterPlan p{};
   auto up = [](size_t b) { return (b + 255) & ~(size_t)255; };
-  p.base_offset = 0;
   if (decode) {
-    const size_t base = plan_gemv(n, k, gran, group_size, (int)tokens, 1).workspace_bytes;
-    p.y_offset = up(base);
-    p.v_offset = p.y_offset + up((size_t)tokens * (size_t)n * 4);
+    const int splits = plan_gemv(n, k, gran, group_size, (int)tokens, 1).ksplit;
+    p.v_offset = up((size_t)splits * (size_t)tokens * (size_t)n * 4);
   } else {
     p.v_offset = up(plan_gemm(n, k, gran, group_size, tokens, true).workspace_bytes);   // hi, then lo
   }
@@ -198,27 +177,28 @@ hipError_t launch_adapter_gemv(const AdapterPlan& p, int64_t n, int64_t k, int g
                                const uint8_t* packed, const float* alpha, const uint16_t* x, int batch, void* y,
                                bool y_bf16, const AdapterArgs& ad, char* ws, hipStream_t s) {
   float* v = reinterpret_cast<float*>(ws + p.v_offset);
-  float* base = reinterpret_cast<float*>(ws + p.y_offset);
-  hipLaunchKernelGGL(adapter_shrink, dim3((unsigned)((ad.rank + 3) / 4), (unsigned)batch), dim3(256), 0, s, ad, x, k, v);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
+  float* partial = reinterpret_cast<float*>(ws + p.partial_offset);
   const GemvPlan g = plan_gemv(n, k, gran, group_size, batch, 1);
-  e = launch_gemv(g, n, k, gran, group_size, packed, alpha, x, batch, base, false, 1, 0, 0, 0,
-                  reinterpret_cast<float*>(ws + p.base_offset), s);
+  const hipError_t e = launch_gemv_partials(g, n, k, gran, group_size, packed, alpha, x, batch, partial,
+                                            AdapterShrink{ad, v, batch, 0}, s);
   if (e != hipSuccess) return e;
   const dim3 grid((unsigned)((n + 255) / 256), (unsigned)batch);
-#define SHERRY_EXPAND(G)                                                                                       \
-  do {                                                                                                         \
-    if (y_bf16) hipLaunchKernelGGL((adapter_expand<G, true>), grid, dim3(256), 0, s, ad, base, v, n, y);       \
-    else hipLaunchKernelGGL((adapter_expand<G, false>), grid, dim3(256), 0, s, ad, base, v, n, y);             \
+#define SHERRY_FINISH(G)                                                                                             \
+  do {                                                                                                               \
+    if (y_bf16)                                                                                                      \
+      hipLaunchKernelGGL((adapter_finish<G, true>), grid, dim3(256), 0, s, ad, partial, g.ksplit, alpha, gran, v, n, \
+                         y);                                                                                         \
+    else                                                                                                             \
+      hipLaunchKernelGGL((adapter_finish<G, false>), grid, dim3(256), 0, s, ad, partial, g.ksplit, alpha, gran, v,   \
+                         n, y);                                                                                      \
   } while (0)
-  if (ad.rank <= 8) SHERRY_EXPAND(1);
-  else if (ad.rank <= 16) SHERRY_EXPAND(2);
-  else if (ad.rank <= 32) SHERRY_EXPAND(4);
-  else if (ad.rank <= 64) SHERRY_EXPAND(8);
-  else if (ad.rank <= 128) SHERRY_EXPAND(16);
-  else SHERRY_EXPAND(32);
-#undef SHERRY_EXPAND
+  if (ad.rank <= 8) SHERRY_FINISH(1);
+  else if (ad.rank <= 16) SHERRY_FINISH(2);
+  else if (ad.rank <= 32) SHERRY_FINISH(4);
+  else if (ad.rank <= 64) SHERRY_FINISH(8);
+  else if (ad.rank <= 128) SHERRY_FINISH(16);
+  else SHERRY_FINISH(32);
+#undef SHERRY_FINISH
   return hipGetLastError();
 }
 
@@ -239,7 +219,7 @@ hipError_t launch_adapter_gemm(const AdapterPlan& p, int64_t n, int64_t k, int g
   const GemmPlan g = plan_gemm(n, k, gran, group_size, m, true);
   const AdapterTerm term{ad, vh, vl};
   return launch_gemm_adapted(g, n, k, gran, group_size, packed, alpha, x, m, y,
-                             reinterpret_cast<float*>(ws + p.base_offset), term, s);
+                             reinterpret_cast<float*>(ws + p.partial_offset), term, s);
 }
 
 }  // namespace sherry

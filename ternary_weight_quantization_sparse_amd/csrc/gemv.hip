@@ -24,7 +24,7 @@
 // and activations reach LDS by DMA copies (details at the kernel).
 #include <type_traits>
 
-#include "sherry_internal.h"
+#include "ops_internal.h"
 
 namespace sherry {
 namespace {
@@ -201,11 +201,17 @@ __device__ inline void window_accumulate(const float* tbl, const RowWindow<MODE,
 // workgroup instead of across workgroups, so a call is one kernel with no
 // workspace.  Latency is hidden by occupancy: ~55 VGPRs and 16-64 KB of LDS
 // per workgroup, 8 waves per SIMD.
-template <int MODE, int WIN, int M, bool YBF16, int RW, int KW, bool ONEWIN = false>
+// With AD = AdapterShrink the launch has further workgroups for the adapters'
+// low-rank products beside these, and the sums stay fp32 partials (for
+// adapter_finish).
+template <int MODE, int WIN, int M, bool YBF16, int RW, int KW, bool ONEWIN = false, typename... AD>
 __global__ __launch_bounds__(64 * RW * KW) void gemv_b1_lut_kernel(
     const uint8_t* __restrict__ packed, const float* __restrict__ alpha,
     const uint16_t* __restrict__ x, void* __restrict__ y, float* __restrict__ partial, int64_t n, int64_t k,
-    int group_sbs, int ksplit, int64_t packed_stride, int64_t alpha_stride, int64_t y_stride) {
+    int group_sbs, int ksplit, int64_t packed_stride, int64_t alpha_stride, int64_t y_stride, AD... ad) {
+  if constexpr (sizeof...(AD) > 0) {
+    if (adapter_shrink_block<RW * KW>(x, k, ad...)) return;
+  }
   constexpr int kRows = 64 * RW;  // rows per row slot
   constexpr int kThreadsWg = 64 * RW * KW;
   __shared__ __attribute__((aligned(16))) float tbl[KW][WIN * kTableFloatsPerSb];
@@ -332,7 +338,7 @@ __global__ __launch_bounds__(64 * RW * KW) void gemv_b1_lut_kernel(
     const int64_t row = row_base + (int64_t)i * kRows;
     if (row >= n) continue;
     float v = acc[i];
-    if (ksplit == 1) {
+    if (sizeof...(AD) == 0 && ksplit == 1) {
       if constexpr (MODE == kChannel) v *= al[row];
       if constexpr (MODE == kTensor) v *= al[0];
       store_y<YBF16>(y, c * y_stride + row, v);
@@ -393,11 +399,14 @@ template <int XR> constexpr int kXChunkOf = XR == 4 ? SHERRY_XCHUNK_SMALL : 4;
 template <int XR> constexpr int kXPitchOf = kXChunkOf<XR> * kSuperblock * 2 + 16;
 constexpr int kMRecNib = 0, kMRecSgn = 1024, kMRecAlpha = 1280;
 
-template <int MODE, int XR, bool YBF16>
+template <int MODE, int XR, bool YBF16, typename... AD>
 __global__ __launch_bounds__(256) void gemv_mfma_kernel(
     const uint8_t* packed, const float* alpha, const uint16_t* __restrict__ x, void* __restrict__ y,
     float* __restrict__ partial, int64_t n, int64_t k, int group_sbs, int batch, int ksplit,
-    int64_t packed_stride, int64_t alpha_stride, int64_t y_stride) {
+    int64_t packed_stride, int64_t alpha_stride, int64_t y_stride, AD... ad) {
+  if constexpr (sizeof...(AD) > 0) {   // (see gemv_b1_lut_kernel)
+    if (adapter_shrink_block<4>(x, k, ad...)) return;
+  }
   constexpr bool kGroup = MODE == kGroup1 || MODE == kGroupN;
   constexpr int kRec = kGroup ? 1536 : 1280;  // record bytes per wave per superblock
   constexpr int kOps = kGroup ? 3 : 2;        // record copies per wave per superblock
@@ -653,7 +662,7 @@ __global__ __launch_bounds__(256) void gemv_mfma_kernel(
       const int b = 4 * q + e;
       if (b >= batch) continue;
       float v = acc[i][e];
-      if (ksplit == 1) {
+      if (sizeof...(AD) == 0 && ksplit == 1) {
         if constexpr (MODE == kChannel) v *= al[row];
         if constexpr (MODE == kTensor) v *= al[0];
         store_y<YBF16>(y, c * y_stride + (int64_t)b * n + row, v);
@@ -730,30 +739,32 @@ __global__ __launch_bounds__(256) void gemv_split_reduce4(const float* __restric
   }
 }
 
-template <int MODE, int WIN, int M, bool YBF16, int RW, int KW>
+template <int MODE, int WIN, int M, bool YBF16, int RW, int KW, typename... AD>
 void launch_lut_one(dim3 grid, hipStream_t s, const uint8_t* packed, const float* alpha, const uint16_t* x,
                     void* y, float* ws, int64_t n, int64_t k, int group_sbs, int ksplit, int64_t ps, int64_t as,
-                    int64_t ys) {
+                    int64_t ys, AD... ad) {
+  if constexpr (sizeof...(AD) > 0) grid.x += adapter_shrink_blocks<RW * KW>(grid.z, ad...);
   if constexpr (KW == 1 && M == 1) {
     // one window per workgroup (a split across workgroups into single windows,
     // or K of one window)
     if (SHERRY_LUT_ONEWIN && k / kSuperblock / ksplit == WIN) {
-      hipLaunchKernelGGL((gemv_b1_lut_kernel<MODE, WIN, M, YBF16, RW, KW, true>), grid, dim3(64 * RW * KW), 0, s,
-                         packed, alpha, x, y, ws, n, k, group_sbs, ksplit, ps, as, ys);
+      hipLaunchKernelGGL((gemv_b1_lut_kernel<MODE, WIN, M, YBF16, RW, KW, true, AD...>), grid, dim3(64 * RW * KW), 0,
+                         s, packed, alpha, x, y, ws, n, k, group_sbs, ksplit, ps, as, ys, ad...);
       return;
     }
   }
-  hipLaunchKernelGGL((gemv_b1_lut_kernel<MODE, WIN, M, YBF16, RW, KW>), grid, dim3(64 * RW * KW), 0, s, packed,
-                     alpha, x, y, ws, n, k, group_sbs, ksplit, ps, as, ys);
+  hipLaunchKernelGGL((gemv_b1_lut_kernel<MODE, WIN, M, YBF16, RW, KW, false, AD...>), grid, dim3(64 * RW * KW), 0, s,
+                     packed, alpha, x, y, ws, n, k, group_sbs, ksplit, ps, as, ys, ad...);
 }
 
 // (rw, kw, win, m) -> instantiation; the plan only produces these shapes
-template <int MODE, bool YBF16>
+template <int MODE, bool YBF16, typename... AD>
 hipError_t launch_lut(const GemvPlan& p, dim3 grid, hipStream_t s, const uint8_t* packed, const float* alpha,
                       const uint16_t* x, void* y, float* ws, int64_t n, int64_t k, int group_sbs, int64_t ps,
-                      int64_t as, int64_t ys) {
+                      int64_t as, int64_t ys, AD... ad) {
 #define SHERRY_LUT(W, M_, RW_, KW_) \
-  launch_lut_one<MODE, W, M_, YBF16, RW_, KW_>(grid, s, packed, alpha, x, y, ws, n, k, group_sbs, p.ksplit, ps, as, ys)
+  launch_lut_one<MODE, W, M_, YBF16, RW_, KW_>(grid, s, packed, alpha, x, y, ws, n, k, group_sbs, p.ksplit, ps, as, \
+                                               ys, ad...)
 #define SHERRY_LUT_WIN(M_, RW_, KW_)                 \
   do {                                               \
     if (p.window_sbs >= 4) SHERRY_LUT(4, M_, RW_, KW_); \
@@ -761,9 +772,19 @@ hipError_t launch_lut(const GemvPlan& p, dim3 grid, hipStream_t s, const uint8_t
     else SHERRY_LUT(1, M_, RW_, KW_);                \
   } while (0)
   const int cfg = p.rw * 100 + p.kw;
-  if (cfg == 401 && p.rows_per_thread == 4) SHERRY_LUT_WIN(4, 4, 1);
-  else if (cfg == 401) SHERRY_LUT_WIN(1, 4, 1);
-  else if (cfg == 801) SHERRY_LUT_WIN(1, 8, 1);
+  if constexpr (sizeof...(AD) == 0) {   // launches over many matrices
+    if (cfg == 401 && p.rows_per_thread == 4) {
+      SHERRY_LUT_WIN(4, 4, 1);
+      return hipSuccess;
+    }
+    if (cfg == 801) {
+      SHERRY_LUT_WIN(1, 8, 1);
+      return hipSuccess;
+    }
+  } else if (p.rows_per_thread != 1) {
+    return hipErrorInvalidValue;
+  }
+  if (cfg == 401) SHERRY_LUT_WIN(1, 4, 1);
   else if (cfg == 402) SHERRY_LUT_WIN(1, 4, 2);
   else if (cfg == 404) SHERRY_LUT_WIN(1, 4, 4);
   else if (cfg == 208) {
@@ -776,11 +797,11 @@ hipError_t launch_lut(const GemvPlan& p, dim3 grid, hipStream_t s, const uint8_t
   return hipSuccess;
 }
 
-template <int GRAN, bool YBF16>
+template <int GRAN, bool YBF16, typename... AD>
 hipError_t launch_gemv_t(const GemvPlan& p, int64_t n, int64_t k, int group_size,
                          const uint8_t* packed, const float* alpha, const uint16_t* x, int batch,
                          void* y, int count, int64_t packed_stride, int64_t alpha_stride,
-                         int64_t y_stride, float* ws, hipStream_t s) {
+                         int64_t y_stride, float* ws, hipStream_t s, AD... ad) {
   const int group_sbs = GRAN == SHERRY_PER_GROUP ? group_size / kSuperblock : 1;
   const dim3 grid((unsigned)p.panels, (unsigned)count, (unsigned)p.ksplit);
   if (p.kind == 0) {
@@ -788,18 +809,20 @@ hipError_t launch_gemv_t(const GemvPlan& p, int64_t n, int64_t k, int group_size
                    : GRAN == SHERRY_PER_TENSOR  ? kTensor
                    : (group_sbs == 1 ? kGroup1 : kGroupN);
     hipError_t le;
-    if (mode == kGroup1) le = launch_lut<kGroup1, YBF16>(p, grid, s, packed, alpha, x, y, ws, n, k, group_sbs, packed_stride, alpha_stride, y_stride);
-    else if (mode == kGroupN) le = launch_lut<kGroupN, YBF16>(p, grid, s, packed, alpha, x, y, ws, n, k, group_sbs, packed_stride, alpha_stride, y_stride);
-    else if (mode == kChannel) le = launch_lut<kChannel, YBF16>(p, grid, s, packed, alpha, x, y, ws, n, k, group_sbs, packed_stride, alpha_stride, y_stride);
-    else le = launch_lut<kTensor, YBF16>(p, grid, s, packed, alpha, x, y, ws, n, k, group_sbs, packed_stride, alpha_stride, y_stride);
+    if (mode == kGroup1) le = launch_lut<kGroup1, YBF16>(p, grid, s, packed, alpha, x, y, ws, n, k, group_sbs, packed_stride, alpha_stride, y_stride, ad...);
+    else if (mode == kGroupN) le = launch_lut<kGroupN, YBF16>(p, grid, s, packed, alpha, x, y, ws, n, k, group_sbs, packed_stride, alpha_stride, y_stride, ad...);
+    else if (mode == kChannel) le = launch_lut<kChannel, YBF16>(p, grid, s, packed, alpha, x, y, ws, n, k, group_sbs, packed_stride, alpha_stride, y_stride, ad...);
+    else le = launch_lut<kTensor, YBF16>(p, grid, s, packed, alpha, x, y, ws, n, k, group_sbs, packed_stride, alpha_stride, y_stride, ad...);
     if (le != hipSuccess) return le;
   } else {
     const int mode = GRAN == SHERRY_PER_CHANNEL ? kChannel
                    : GRAN == SHERRY_PER_TENSOR  ? kTensor
                    : (group_sbs == 1 ? kGroup1 : kGroupN);
-#define SHERRY_MFMA_XR(MD, XR)                                                                           \
-  hipLaunchKernelGGL((gemv_mfma_kernel<MD, XR, YBF16>), grid, dim3(256), 0, s, packed, alpha, x, y, ws, n, \
-                     k, group_sbs, batch, p.ksplit, packed_stride, alpha_stride, y_stride)
+    dim3 g = grid;
+    if constexpr (sizeof...(AD) > 0) g.x += adapter_shrink_blocks<4>(grid.z, ad...);
+#define SHERRY_MFMA_XR(MD, XR)                                                                                  \
+  hipLaunchKernelGGL((gemv_mfma_kernel<MD, XR, YBF16, AD...>), g, dim3(256), 0, s, packed, alpha, x, y, ws, n, \
+                     k, group_sbs, batch, p.ksplit, packed_stride, alpha_stride, y_stride, ad...)
 #define SHERRY_MFMA_CASE(MD)                                 \
   do {                                                       \
     if (batch <= 4) SHERRY_MFMA_XR(MD, 4);                   \
@@ -814,7 +837,7 @@ hipError_t launch_gemv_t(const GemvPlan& p, int64_t n, int64_t k, int group_size
 #undef SHERRY_MFMA_XR
   }
   hipError_t e = hipGetLastError();
-  if (e != hipSuccess || p.ksplit == 1) return e;
+  if (e != hipSuccess || p.ksplit == 1 || sizeof...(AD) > 0) return e;
   const int64_t items = (int64_t)count * batch * n;
   // four outputs per thread only for large outputs: a single call (N <= 8192
   // outputs, often tens of splits) needs the thread count of one output per
@@ -939,6 +962,17 @@ hipError_t launch_gemv(const GemvPlan& p, int64_t n, int64_t k, int gran, int gr
     SHERRY_GEMV_CASE(SHERRY_PER_TENSOR, false);
   }
 #undef SHERRY_GEMV_CASE
+}
+
+hipError_t launch_gemv_partials(const GemvPlan& p, int64_t n, int64_t k, int gran, int group_size,
+                                const uint8_t* packed, const float* alpha, const uint16_t* x, int batch,
+                                float* partial, AdapterShrink ad, hipStream_t s) {
+  ad.panels = (int)p.panels;
+  if (gran == SHERRY_PER_GROUP)
+    return launch_gemv_t<SHERRY_PER_GROUP, false>(p, n, k, group_size, packed, alpha, x, batch, nullptr, 1, 0, 0, 0, partial, s, ad);
+  if (gran == SHERRY_PER_CHANNEL)
+    return launch_gemv_t<SHERRY_PER_CHANNEL, false>(p, n, k, group_size, packed, alpha, x, batch, nullptr, 1, 0, 0, 0, partial, s, ad);
+  return launch_gemv_t<SHERRY_PER_TENSOR, false>(p, n, k, group_size, packed, alpha, x, batch, nullptr, 1, 0, 0, 0, partial, s, ad);
 }
 
 }  // namespace sherry

@@ -64,8 +64,7 @@ hipError_t launch_gemm_adapted(const GemmPlan& p, int64_t n, int64_t k, int gran
                                const uint8_t* packed, const float* alpha, const uint16_t* x, int64_t m,
                                uint16_t* y, float* ws, const AdapterTerm& ad, hipStream_t s);
 struct AdapterPlan {
-  size_t base_offset;       // the packed product's own workspace
-  size_t y_offset;          // fp32 base product (decode)
+  size_t partial_offset;    // the packed product's workspace: decode, fp32 partials [splits, tokens, N]
   size_t v_offset;          // low-rank products [tokens, rank]: fp32 (decode), or bf16 hi and lo
   size_t workspace_bytes;
 };
@@ -76,6 +75,63 @@ hipError_t launch_adapter_gemv(const AdapterPlan& p, int64_t n, int64_t k, int g
 hipError_t launch_adapter_gemm(const AdapterPlan& p, int64_t n, int64_t k, int gran, int group_size,
                                const uint8_t* packed, const float* alpha, const uint16_t* x, int64_t m, uint16_t* y,
                                const AdapterArgs& ad, char* ws, hipStream_t s);
+
+// Decode's low-rank products v = scale * a x, computed by workgroups of the
+// packed product's launch past its own `panels`: a wave per (token, row of a).
+// They run beside the packed product instead of before it.
+struct AdapterShrink {
+  AdapterArgs a;
+  float* v;        // [tokens, rank]
+  int tokens, panels;
+};
+hipError_t launch_gemv_partials(const GemvPlan& p, int64_t n, int64_t k, int gran, int group_size,
+                                const uint8_t* packed, const float* alpha, const uint16_t* x, int batch,
+                                float* partial, AdapterShrink ad, hipStream_t s);
+template <int WAVES>
+unsigned adapter_shrink_blocks(unsigned depth, const AdapterShrink& ad) {
+  const unsigned items = (unsigned)(ad.tokens * ad.a.rank), per = WAVES * depth;
+  return (items + per - 1) / per;
+}
+__device__ inline int adapter_of(const AdapterArgs& a, int64_t token) {
+  const int c = a.ids[token];
+  return c >= 0 && c < a.count ? c : -1;
+}
+// 8 products of bf16 pairs, added in fp32
+typedef uint32_t adapter_u32x4 __attribute__((ext_vector_type(4)));
+__device__ inline float dot8(const adapter_u32x4 a, const adapter_u32x4 b, float s) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    s += __uint_as_float(a[i] << 16) * __uint_as_float(b[i] << 16);
+    s += __uint_as_float(a[i] & 0xFFFF0000u) * __uint_as_float(b[i] & 0xFFFF0000u);
+  }
+  return s;
+}
+template <int WAVES>
+__device__ inline bool adapter_shrink_block(const uint16_t* x, int64_t k, const AdapterShrink& ad) {
+  if ((int)blockIdx.x < ad.panels) return false;
+  const int lane = threadIdx.x & 63;
+  const int item = (int)((blockIdx.x - ad.panels) * gridDim.z + blockIdx.z) * WAVES +
+                   __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int token = item / ad.a.rank, row = item % ad.a.rank;
+  if (token >= ad.tokens) return true;
+  const int c = adapter_of(ad.a, token);
+  if (c < 0 || row >= adapter_rank(ad.a, c)) return true;   // never read
+  const adapter_u32x4* ar = reinterpret_cast<const adapter_u32x4*>(ad.a.a + ((int64_t)c * ad.a.rank + row) * k);
+  const adapter_u32x4* xr = reinterpret_cast<const adapter_u32x4*>(x + token * k);
+  float s = 0.f;
+  const int all = (int)(k / 8);
+  int i = lane;
+  for (; i + 3 * 64 < all; i += 4 * 64) {   // four steps' loads in flight
+    const adapter_u32x4 a0 = ar[i], a1 = ar[i + 64], a2 = ar[i + 128], a3 = ar[i + 192];
+    const adapter_u32x4 x0 = xr[i], x1 = xr[i + 64], x2 = xr[i + 128], x3 = xr[i + 192];
+    s = dot8(a3, x3, dot8(a2, x2, dot8(a1, x1, dot8(a0, x0, s))));
+  }
+  for (; i < all; i += 64) s = dot8(ar[i], xr[i], s);
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) s += __shfl_xor(s, o);
+  if (lane == 0) ad.v[token * ad.a.rank + row] = s * ad.a.scale[c];
+  return true;
+}
 
 // ---------------------------------------------------------------- orthogonalised updates
 struct MuonArgs {
