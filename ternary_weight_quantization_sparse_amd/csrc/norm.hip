@@ -27,7 +27,6 @@ namespace sherry {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kMaxRegDim = 8192;   // channels a thread group keeps in registers (32 a thread)
 
 // ------------------------------------------------------------- element access
 template <typename T, int V> struct Raw;
@@ -131,6 +130,23 @@ __device__ inline void group_sum2(float& a, float& b, float (*slot)[8]) {
   __syncthreads();
   a = ((*slot)[0] + (*slot)[1]) + ((*slot)[2] + (*slot)[3]);
   b = ((*slot)[4] + (*slot)[5]) + ((*slot)[6] + (*slot)[7]);
+}
+
+template <int TPR>
+__device__ inline void group_sum3(float& a, float& b, float& c, float (*slot)[12]) {
+  a = wave_sum(a);
+  b = wave_sum(b);
+  c = wave_sum(c);
+  if constexpr (TPR == 64) return;
+  if ((threadIdx.x & 63) == 0) {
+    (*slot)[threadIdx.x >> 6] = a;
+    (*slot)[4 + (threadIdx.x >> 6)] = b;
+    (*slot)[8 + (threadIdx.x >> 6)] = c;
+  }
+  __syncthreads();
+  a = ((*slot)[0] + (*slot)[1]) + ((*slot)[2] + (*slot)[3]);
+  b = ((*slot)[4] + (*slot)[5]) + ((*slot)[6] + (*slot)[7]);
+  c = ((*slot)[8] + (*slot)[9]) + ((*slot)[10] + (*slot)[11]);
 }
 
 __device__ inline float rnorm(float sum, float rdim, float eps) { return 1.0f / sqrtf(sum * rdim + eps); }
@@ -240,11 +256,14 @@ __device__ inline void rows_of(const NormSplit& s, int64_t b, int64_t q, int64_t
   }
 }
 
+// Rows of up to 16 channels a thread keep the norm weights in registers and
+// load the next row while the current one is worked on.
 template <typename T, typename W, int V, int NPT, int TPR>
 __global__ __launch_bounds__(kThreads) void norm_backward(NormArgs a, NormGrads d, NormSplit sp) {
   typedef typename Raw<T, V>::type R;
   constexpr int kGroups = kThreads / TPR;
-  __shared__ float red1[2][4], red2[4][8];
+  constexpr bool kHold = NPT * V <= 16;
+  __shared__ float red1[2][4], red2[4][8], red3[2][12];
   __shared__ float join[kGroups > 1 ? kGroups : 1][kGroups > 1 ? TPR * V : 1];
   const int t = threadIdx.x % TPR, group = threadIdx.x / TPR;
   const int dim = a.dim;
@@ -254,6 +273,40 @@ __global__ __launch_bounds__(kThreads) void norm_backward(NormArgs a, NormGrads 
   const bool elem_gate = a.gate_kind == SHERRY_GATE_ROWS && a.gate_rows == 1;
   const bool sum_gate = col_gate && !elem_gate;   // summed over rows
   const GateAt ga{a.gate_kind, a.gate_rows};
+
+  auto load_weights = [&](int j, float (&w)[V], float (&wp)[V]) {
+    const int col = (j * TPR + t) * V;
+#pragma unroll
+    for (int e = 0; e < V; ++e) { w[e] = 1.f; wp[e] = 0.f; }
+    if (col < dim) {
+      if (post) load_param(static_cast<const W*>(a.w_post) + col, w);
+      if (pre) load_param(static_cast<const W*>(a.w_pre) + col, wp);
+    }
+  };
+  float w_held[kHold ? NPT : 1][V], wp_held[kHold ? NPT : 1][V];
+  if constexpr (kHold)
+#pragma unroll
+    for (int j = 0; j < NPT; ++j) load_weights(j, w_held[j], wp_held[j]);
+
+  struct Row {
+    R h[NPT], y[NPT], d[NPT], n[NPT];
+    T tok;
+  };
+  auto load_row = [&](Row& x, int64_t row) {
+    const int64_t at = row * dim;
+    if (a.gate_kind == SHERRY_GATE_TOKEN) x.tok = static_cast<const T*>(a.gate)[row];
+#pragma unroll
+    for (int j = 0; j < NPT; ++j) {
+      const int col = (j * TPR + t) * V;
+      x.h[j] = R{}; x.y[j] = R{}; x.d[j] = R{}; x.n[j] = R{};
+      if (col < dim) {
+        x.h[j] = *reinterpret_cast<const R*>(static_cast<const T*>(a.h) + at + col);
+        if (has_y) x.y[j] = *reinterpret_cast<const R*>(static_cast<const T*>(a.y) + at + col);
+        if (d.dh_out) x.d[j] = *reinterpret_cast<const R*>(static_cast<const T*>(d.dh_out) + at + col);
+        if (d.dn_out) x.n[j] = *reinterpret_cast<const R*>(static_cast<const T*>(d.dn_out) + at + col);
+      }
+    }
+  };
 
   float dwpre[NPT][V], dwpost[NPT][V], dgate[NPT][V];
 #pragma unroll
@@ -281,68 +334,79 @@ __global__ __launch_bounds__(kThreads) void norm_backward(NormArgs a, NormGrads 
     }
   };
 
+  auto y_squares = [&](const Row& x) {   // this thread's part of sum(y^2)
+    float s = 0.f;
+#pragma unroll
+    for (int j = 0; j < NPT; ++j) {
+      float yv[V];
+      widen(x.y[j], yv);
+#pragma unroll
+      for (int e = 0; e < V; ++e) s += yv[e] * yv[e];
+    }
+    return s;
+  };
+  auto load_gate = [&](int j, int64_t row, float (&g)[V]) {   // of a column gate
+    const int col = (j * TPR + t) * V;
+    if (col_gate && col < dim) load_param(static_cast<const T*>(a.gate) + gate_row(ga, row) * dim + col, g);
+  };
+
   const int64_t b = blockIdx.x;
   const Share sh = share_of(sp, b);
   int odd = 0;
   for (int64_t q = sh.q0; q < sh.q1; ++q) {
     int64_t r0, r1;
     rows_of(sp, b, q, r0, r1);
+    Row x;
+    float gate[kHold ? NPT : 1][V];   // the same for all rows of a sequence
+#pragma unroll
+    for (int j = 0; j < (kHold ? NPT : 1); ++j)
+#pragma unroll
+      for (int e = 0; e < V; ++e) gate[j][e] = 1.f;
+    float s_yy = 0.f;                 // kHold: sum(y^2) of the row at hand, taken with the last row's sums
+    if (kHold && r0 + group < r1) {
+      load_row(x, r0 + group);
+#pragma unroll
+      for (int j = 0; j < NPT; ++j) load_gate(j, r0, gate[kHold ? j : 0]);
+      if (post) {
+        s_yy = group_sum<TPR>(y_squares(x), &red1[odd]);
+        odd ^= 1;
+      }
+    }
     for (int64_t base = r0; base < r1; base += kGroups, odd ^= 1) {
       const int64_t row = base + group;
-      const bool live = row < r1;
-      if (kGroups > 1 && !live) continue;   // a wave by itself: no barrier in its row
+      if (kGroups > 1 && row >= r1) continue;   // a wave by itself: no barrier in its row
+      Row ahead;
+      const bool more = row + kGroups < r1;
+      if constexpr (kHold) {
+        if (more) load_row(ahead, row + kGroups);
+      } else {
+        load_row(x, row);
+        if (post) s_yy = group_sum<TPR>(y_squares(x), &red1[odd]);
+      }
       const int64_t at = row * dim;
-      R rh[NPT], ry[NPT], rd[NPT], rn[NPT];
-#pragma unroll
-      for (int j = 0; j < NPT; ++j) {
-        const int col = (j * TPR + t) * V;
-        rh[j] = R{}; ry[j] = R{}; rd[j] = R{}; rn[j] = R{};
-        if (col < dim) {
-          rh[j] = *reinterpret_cast<const R*>(static_cast<const T*>(a.h) + at + col);
-          if (has_y) ry[j] = *reinterpret_cast<const R*>(static_cast<const T*>(a.y) + at + col);
-          if (d.dh_out) rd[j] = *reinterpret_cast<const R*>(static_cast<const T*>(d.dh_out) + at + col);
-          if (d.dn_out) rn[j] = *reinterpret_cast<const R*>(static_cast<const T*>(d.dn_out) + at + col);
-        }
-      }
-      float r_y = 1.f, tok = 1.f;
-      if (post) {
-        float s = 0.f;
-#pragma unroll
-        for (int j = 0; j < NPT; ++j) {
-          float yv[V];
-          widen(ry[j], yv);
-#pragma unroll
-          for (int e = 0; e < V; ++e) s += yv[e] * yv[e];
-        }
-        r_y = rnorm(group_sum<TPR>(s, &red1[odd]), rdim, a.eps);
-      }
-      if (a.gate_kind == SHERRY_GATE_TOKEN) {
-        float g1[1];
-        load_param(static_cast<const T*>(a.gate) + row, g1);
-        tok = g1[0];
-      }
-      const T* grow = static_cast<const T*>(a.gate) + (col_gate ? gate_row(ga, row) * dim : 0);
+      const float r_y = post ? rnorm(s_yy, rdim, a.eps) : 1.f;
+      float tok[1] = {1.f};
+      if (a.gate_kind == SHERRY_GATE_TOKEN) load_param(&x.tok, tok);
 
       // h' and the sums of its norm's gradient
       float h2[NPT][V];
       float s_hh = 0.f, s_uh = 0.f;
 #pragma unroll
       for (int j = 0; j < NPT; ++j) {
-        const int col = (j * TPR + t) * V;
-        float g[V], w[V], wp[V], yv[V], nv[V];
-#pragma unroll
-        for (int e = 0; e < V; ++e) { g[e] = tok; w[e] = 1.f; wp[e] = 0.f; }
-        if (col < dim) {
-          if (col_gate) load_param(grow + col, g);
-          if (post) load_param(static_cast<const W*>(a.w_post) + col, w);
-          if (pre) load_param(static_cast<const W*>(a.w_pre) + col, wp);
+        float w_[V], wp_[V], yv[V], nv[V];
+        float (&g)[V] = gate[kHold ? j : 0];
+        if constexpr (!kHold) {
+          load_gate(j, row, g);
+          load_weights(j, w_, wp_);
         }
-        widen(rh[j], h2[j]);
-        widen(ry[j], yv);
-        widen(rn[j], nv);
+        const float (&w)[V] = kHold ? w_held[kHold ? j : 0] : w_;
+        const float (&wp)[V] = kHold ? wp_held[kHold ? j : 0] : wp_;
+        widen(x.h[j], h2[j]);
+        widen(x.y[j], yv);
+        widen(x.n[j], nv);
 #pragma unroll
         for (int e = 0; e < V; ++e) {
-          if (has_y) h2[j][e] = a.res_scale * h2[j][e] + g[e] * (yv[e] * r_y * w[e]);
+          if (has_y) h2[j][e] = a.res_scale * h2[j][e] + tok[0] * g[e] * (yv[e] * r_y * w[e]);
           s_hh += h2[j][e] * h2[j][e];
           s_uh += wp[e] * nv[e] * h2[j][e];
         }
@@ -359,18 +423,17 @@ __global__ __launch_bounds__(kThreads) void norm_backward(NormArgs a, NormGrads 
 #pragma unroll
       for (int j = 0; j < NPT; ++j) {
         const int col = (j * TPR + t) * V;
-        float g[V], w[V], wp[V], yv[V], nv[V], dv[V], tv[V];
-#pragma unroll
-        for (int e = 0; e < V; ++e) { g[e] = tok; w[e] = 1.f; wp[e] = 0.f; }
-        if (col < dim) {
-          if (col_gate) load_param(grow + col, g);
-          if (post) load_param(static_cast<const W*>(a.w_post) + col, w);
-          if (pre) load_param(static_cast<const W*>(a.w_pre) + col, wp);
+        float w_[V], wp_[V], yv[V], nv[V], dv[V], tv[V], eg[V];
+        float (&g)[V] = gate[kHold ? j : 0];
+        if constexpr (!kHold) {
+          load_gate(j, row, g);
+          load_weights(j, w_, wp_);
         }
-        widen(ry[j], yv);
-        widen(rn[j], nv);
-        widen(rd[j], dv);
-        float eg[V];
+        const float (&w)[V] = kHold ? w_held[kHold ? j : 0] : w_;
+        const float (&wp)[V] = kHold ? wp_held[kHold ? j : 0] : wp_;
+        widen(x.y[j], yv);
+        widen(x.n[j], nv);
+        widen(x.d[j], dv);
 #pragma unroll
         for (int e = 0; e < V; ++e) {
           const float yh = yv[e] * r_y;
@@ -383,7 +446,7 @@ __global__ __launch_bounds__(kThreads) void norm_backward(NormArgs a, NormGrads 
           eg[e] = tp;
           dgate[j][e] += tp;
           s_tp += tp;
-          const float qv = tv[e] * g[e];
+          const float qv = tv[e] * (tok[0] * g[e]);
           dwpost[j][e] += qv * yh;
           v[j][e] = qv * w[e];
           s_vy += v[j][e] * yv[e];
@@ -394,23 +457,30 @@ __global__ __launch_bounds__(kThreads) void norm_backward(NormArgs a, NormGrads 
           if (elem_gate) store_vec(static_cast<T*>(d.dgate) + at + col, eg);
         }
       }
-      if (!has_y) continue;
-      group_sum2<TPR>(s_vy, s_tp, &red2[2 + odd]);
-      if (a.gate_kind == SHERRY_GATE_TOKEN && t == 0) {
-        const float g1[1] = {s_tp};
-        store_vec(static_cast<T*>(d.dgate) + row, g1);
-      }
-      const float c_y = post ? r_y * r_y * r_y * s_vy * rdim : 0.f;
+      if (has_y) {
+        if constexpr (kHold) {
+          s_yy = post && more ? y_squares(ahead) : 0.f;
+          group_sum3<TPR>(s_vy, s_tp, s_yy, &red3[odd]);
+        } else {
+          group_sum2<TPR>(s_vy, s_tp, &red2[2 + odd]);
+        }
+        if (a.gate_kind == SHERRY_GATE_TOKEN && t == 0) {
+          const float g1[1] = {s_tp};
+          store_vec(static_cast<T*>(d.dgate) + row, g1);
+        }
+        const float c_y = post ? r_y * r_y * r_y * s_vy * rdim : 0.f;
 #pragma unroll
-      for (int j = 0; j < NPT; ++j) {
-        const int col = (j * TPR + t) * V;
-        float yv[V];
-        widen(ry[j], yv);
+        for (int j = 0; j < NPT; ++j) {
+          const int col = (j * TPR + t) * V;
+          float yv[V];
+          widen(x.y[j], yv);
 #pragma unroll
-        for (int e = 0; e < V; ++e)
-          if (post) v[j][e] = r_y * v[j][e] - c_y * yv[e];
-        if (col < dim) store_vec(static_cast<T*>(d.dy) + at + col, v[j]);
+          for (int e = 0; e < V; ++e)
+            if (post) v[j][e] = r_y * v[j][e] - c_y * yv[e];
+          if (col < dim) store_vec(static_cast<T*>(d.dy) + at + col, v[j]);
+        }
       }
+      if constexpr (kHold) x = ahead;
     }
     if (sum_gate && (sp.seqs_per_block > 1 || sp.blocks_per_seq == 1)) {   // this workgroup holds all its rows
       flush(dgate, static_cast<T*>(d.dgate) + q * dim);
@@ -614,7 +684,8 @@ __global__ __launch_bounds__(kThreads) void norm_columns_long(NormArgs a, NormGr
 
 // -------------------------------------------------------------------- dispatch
 // Thread groups by the row's load count: a wave for up to two 64-lane loads
-// (no barrier in a row), else the workgroup with up to 32 channels a thread.
+// (no barrier in a row), else the workgroup with up to 32 channels a thread (16
+// where a load is one channel: 32 spill).
 template <typename T, typename W, int V, typename F>
 bool with_shape(int64_t dim, F&& f) {
   const int64_t vecs = (dim + V - 1) / V;
@@ -625,7 +696,6 @@ bool with_shape(int64_t dim, F&& f) {
   else if (vecs <= 1024) f(std::integral_constant<int, 4>{}, std::integral_constant<int, 256>{});
   else if (V < 8 && vecs <= 2048) f(std::integral_constant<int, V < 8 ? 8 : 4>{}, std::integral_constant<int, 256>{});
   else if (V < 4 && vecs <= 4096) f(std::integral_constant<int, V < 4 ? 16 : 4>{}, std::integral_constant<int, 256>{});
-  else if (V < 4 && vecs <= 8192) f(std::integral_constant<int, V < 4 ? 32 : 4>{}, std::integral_constant<int, 256>{});
   else return false;
   return true;
 }
