@@ -144,18 +144,17 @@ struct SplitOut {
 __global__ __launch_bounds__(kThreads) void muon_split(const float* __restrict__ u, const double* __restrict__ sums,
                                                        int parts, float eps, int64_t n, int64_t k, int64_t np,
                                                        int64_t kp, SplitOut rows, SplitOut cols) {
-  __shared__ double part[kThreads];
+  __shared__ double part[kThreads / 64];
   __shared__ __attribute__((aligned(16))) float scratch[4][32 * kPad];
   const int64_t c = blockIdx.y;
   double s = 0.0;
   for (int i = threadIdx.x; i < parts; i += kThreads) s += sums[c * parts + i];
-  part[threadIdx.x] = s;
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) s += __shfl_xor(s, o);
+  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = s;
   __syncthreads();
-  for (int o = kThreads / 2; o > 0; o >>= 1) {
-    if ((int)threadIdx.x < o) part[threadIdx.x] += part[threadIdx.x + o];
-    __syncthreads();
-  }
-  const float mul = (float)((double)kScale / (sqrt(part[0]) + (double)eps));
+  s = (part[0] + part[1]) + (part[2] + part[3]);
+  const float mul = (float)((double)kScale / (sqrt(s) + (double)eps));
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   float* mine = scratch[wave];
   u += c * n * k;
@@ -242,12 +241,35 @@ __device__ inline void tile_at(const ProductShape& sh, int at, int& ti, int& tj)
   }
 }
 
-// Tile and K range of a workgroup.  Workgroups go to the eight XCDs in turn;
-// each XCD gets a contiguous run of (K range, tile), so its L2 holds the rows
-// that its tiles share.
+// Workgroup -> (matrix, K range, tile).  Workgroups go to the eight XCDs in
+// turn; each XCD gets a contiguous run, so its L2 fetches the rows that its
+// tiles share once, and of few matrices.
 __device__ inline int run_of_xcd(int id, int all) {
   const int per = all >> 3, rest = all & 7, x = id & 7;
   return x * per + (x < rest ? x : rest) + (id >> 3);
+}
+
+// Own values of a 32 x 32 product, as `finish` adds them: 8 columns of row r in
+// each half of 16 columns.
+struct Own {
+  f16x8 hi[2], lo[2], hi2[2], lo2[2];
+};
+template <int EPI>
+__device__ inline void load_own(const Product& g, const ProductShape& sh, int64_t c, int64_t row0, int64_t col0, Own& o) {
+  if (EPI == kLast || (EPI == kSym && col0 < row0)) return;
+  const int lane = threadIdx.x & 63, r = lane & 31, h = lane >> 5;
+#pragma unroll
+  for (int p = 0; p < 2; ++p) {
+    const int64_t at = c * sh.c_size + split_at(row0 + r, sh.c_rows, col0 + p * 16 + h * 8);
+    if (g.own1) {
+      o.hi[p] = *reinterpret_cast<const f16x8*>(g.own1 + at);
+      o.lo[p] = *reinterpret_cast<const f16x8*>(g.own1 + at + kLo);
+    }
+    if (EPI == kSym && g.own2) {
+      o.hi2[p] = *reinterpret_cast<const f16x8*>(g.own2 + at);
+      o.lo2[p] = *reinterpret_cast<const f16x8*>(g.own2 + at + kLo);
+    }
+  }
 }
 
 // Finish of one 32 x 32 product: its sums go through LDS (32 x kPad floats of
@@ -256,7 +278,7 @@ __device__ inline int run_of_xcd(int id, int all) {
 // C[8 (e / 4) + 4 h + e % 4][r] in lane 32 h + r.
 template <int EPI, bool BF16>
 __device__ inline void finish(const Product& g, const ProductShape& sh, const MuonArgs& m, int64_t c, int64_t row0,
-                              int64_t col0, const f32x16& acc, float* scratch) {
+                              int64_t col0, const f32x16& acc, const Own& own, float* scratch) {
   if (EPI == kSym && col0 < row0) return;   // written by the product above the diagonal
   const bool mirror = EPI == kApply || (EPI == kSym && col0 > row0);
   const int lane = threadIdx.x & 63;
@@ -265,13 +287,6 @@ __device__ inline void finish(const Product& g, const ProductShape& sh, const Mu
     scratch[(8 * (e / 4) + 4 * (lane >> 5) + e % 4) * kPad + (lane & 31)] = acc[e] * g.kp;
   __builtin_amdgcn_wave_barrier();
   const int r = lane & 31, h = lane >> 5;
-  // own values of 8 columns of a row added to v
-  auto add_own = [&](const f16* own, float k, int64_t row, int64_t col, float (&v)[8]) {
-    own += c * sh.c_size + split_at(row, sh.c_rows, col);
-    const f16x8 hi = *reinterpret_cast<const f16x8*>(own), lo = *reinterpret_cast<const f16x8*>(own + kLo);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] += k * ((float)hi[e] + (float)lo[e]);
-  };
   auto take = [&](int row, int col, float (&v)[8]) {
     const f32x4 a = *reinterpret_cast<const f32x4*>(scratch + row * kPad + col);
     const f32x4 b = *reinterpret_cast<const f32x4*>(scratch + row * kPad + col + 4);
@@ -287,7 +302,10 @@ __device__ inline void finish(const Product& g, const ProductShape& sh, const Mu
       const int64_t row = row0 + lr_, col = col0 + lc;
       float v[8];
       take(lr_, lc, v);
-      add_own(g.own1, g.k1, row, col, v);
+      const f16* o1 = g.own1 + c * sh.c_size + split_at(row, sh.c_rows, col);
+      const f16x8 hi = *reinterpret_cast<const f16x8*>(o1), lo = *reinterpret_cast<const f16x8*>(o1 + kLo);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] += g.k1 * ((float)hi[e] + (float)lo[e]);
       if (row >= m.n || col >= m.k) continue;
       const int64_t o = (c * m.n + row) * m.k + col;
       if (wide) {
@@ -311,8 +329,12 @@ __device__ inline void finish(const Product& g, const ProductShape& sh, const Mu
     const int lc = p * 16 + h * 8;
     float v[8];
     take(r, lc, v);
-    if (g.own1) add_own(g.own1, g.k1, row0 + r, col0 + lc, v);
-    if (EPI == kSym && g.own2) add_own(g.own2, g.k2, row0 + r, col0 + lc, v);
+    if (g.own1)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] += g.k1 * ((float)own.hi[p][e] + (float)own.lo[p][e]);
+    if (EPI == kSym && g.own2)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] += g.k2 * ((float)own.hi2[p][e] + (float)own.lo2[p][e]);
     split8(v, g.out + c * sh.c_size + split_at(row0 + r, sh.c_rows, col0 + lc));
     if (mirror) {
       *reinterpret_cast<f32x4*>(scratch + r * kPad + lc) = f32x4{v[0], v[1], v[2], v[3]};
@@ -349,11 +371,10 @@ __global__ __launch_bounds__(64 * T::kWaves) void muon_product(ProductPair pair,
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave / T::WN, wn = wave % T::WN;
-  const int z = blockIdx.z;
+  const int per = sh.tiles * sh.splits, run = run_of_xcd(blockIdx.x, gridDim.x);
+  const int z = run / per, tile = run % per % sh.tiles, split = run % per / sh.tiles;
   const Product& g = pair.g[z >= sh.count];
   const int64_t c = z >= sh.count ? z - sh.count : z;
-  const int run = run_of_xcd(blockIdx.x, sh.tiles * sh.splits);
-  const int tile = run % sh.tiles, split = run / sh.tiles;
   int ti, tj;
   tile_at<EPI, T::kCols / T::kRows>(sh, tile, ti, tj);
   const int64_t i0 = (int64_t)ti * T::kRows, j0 = (int64_t)tj * T::kCols;
@@ -448,8 +469,10 @@ __global__ __launch_bounds__(64 * T::kWaves) void muon_product(ProductPair pair,
   }
   __syncthreads();   // every wave has read its last stage: LDS becomes scratch
   auto end = [&](int i, int j, const f32x16& v, float* scratch) {
-    finish<EPI, BF16>(g, sh, m, c, i0 + (wm * T::TM + i) * 32, j0 + (wn * T::TN + j) * 32, v,
-                      scratch);
+    const int64_t row0 = i0 + (wm * T::TM + i) * 32, col0 = j0 + (wn * T::TN + j) * 32;
+    Own own;
+    load_own<EPI>(g, sh, c, row0, col0, own);
+    finish<EPI, BF16>(g, sh, m, c, row0, col0, v, own, scratch);
   };
   float* scratch = reinterpret_cast<float*>(lds) + wave * (32 * kPad);
 #pragma unroll
@@ -473,6 +496,10 @@ __global__ __launch_bounds__(64) void muon_join(ProductPair pair, ProductShape s
   int ti, tj;
   tile_at<EPI, T::kCols / T::kRows>(sh, tile, ti, tj);
   partial += (((int64_t)z * sh.tiles + tile) * sh.splits * T::kWaves + wave) * (kPer * 4 * 64) + at % kPer * 256 + threadIdx.x;
+  const int64_t row0 = (int64_t)ti * T::kRows + (wave / T::WN * T::TM + i) * 32;
+  const int64_t col0 = (int64_t)tj * T::kCols + (wave % T::WN * T::TN + j) * 32;
+  Own own;
+  load_own<EPI>(g, sh, c, row0, col0, own);
   f32x16 s;
 #pragma unroll
   for (int e = 0; e < 16; ++e) s[e] = 0.f;
@@ -483,8 +510,7 @@ __global__ __launch_bounds__(64) void muon_join(ProductPair pair, ProductShape s
 #pragma unroll
       for (int e = 0; e < 4; ++e) s[4 * e4 + e] += v[e];
     }
-  finish<EPI, BF16>(g, sh, m, c, (int64_t)ti * T::kRows + (wave / T::WN * T::TM + i) * 32,
-                    (int64_t)tj * T::kCols + (wave % T::WN * T::TN + j) * 32, s, scratch);
+  finish<EPI, BF16>(g, sh, m, c, row0, col0, s, own, scratch);
 }
 
 // The same for small matrices, where a launch has few tiles and latency counts:
@@ -493,18 +519,17 @@ __global__ __launch_bounds__(64) void muon_join(ProductPair pair, ProductShape s
 // kAhead steps ahead; the parts are added through LDS in wave order.
 template <int TM, int TN, int W, int EPI, bool BF16>
 __global__ __launch_bounds__(64 * W) void muon_product_small(ProductPair pair, ProductShape sh, MuonArgs m) {
-  constexpr int kAhead = TM * TN == 1 ? 8 : TM * TN == 4 ? 4 : 2;
+  constexpr int kAhead = TM * TN == 1 ? 8 : 4;
   constexpr int kProducts = TM * TN;
-  constexpr int kRound = kProducts <= 4 ? kProducts : TN;   // products added at a time (LDS)
-  __shared__ f32x4 part[W][kRound][4][64];
-  __shared__ __attribute__((aligned(16))) float scratch[kRound][32 * kPad];
+  __shared__ f32x4 part[W][kProducts][4][64];
+  __shared__ __attribute__((aligned(16))) float scratch[kProducts][32 * kPad];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int z = blockIdx.z;
+  const int run = run_of_xcd(blockIdx.x, gridDim.x), z = run / sh.tiles;
   const Product& g = pair.g[z >= sh.count];
   const int64_t c = z >= sh.count ? z - sh.count : z;
   int ti, tj;
-  tile_at<EPI>(sh, run_of_xcd(blockIdx.x, sh.tiles), ti, tj);
+  tile_at<EPI>(sh, run % sh.tiles, ti, tj);
   const int64_t i0 = (int64_t)ti * (32 * TM), j0 = (int64_t)tj * (32 * TN);
   const f16* pp = g.p + c * sh.p_size + i0 * 32 + lane * 8;
   const f16* qp = g.q + c * sh.q_size + j0 * 32 + lane * 8;
@@ -529,6 +554,10 @@ __global__ __launch_bounds__(64 * W) void muon_product_small(ProductPair pair, P
       x.ql[j] = *reinterpret_cast<const f16x8*>(q + j * 1024 + kLo);
     }
   };
+  // wave q finishes product q: its own values are on their way from the start
+  const int64_t row0 = i0 + wave / TN * 32, col0 = j0 + wave % TN * 32;
+  Own own;
+  if (wave < kProducts) load_own<EPI>(g, sh, c, row0, col0, own);
   f32x16 acc[TM][TN];
 #pragma unroll
   for (int i = 0; i < TM; ++i)
@@ -557,31 +586,25 @@ __global__ __launch_bounds__(64 * W) void muon_product_small(ProductPair pair, P
     }
   }
 #pragma unroll
-  for (int q0 = 0; q0 < kProducts; q0 += kRound) {
-    if (q0 > 0) __syncthreads();   // the last round's sums have been read
+  for (int q = 0; q < kProducts; ++q) {
+    const f32x16& v = acc[q / TN][q % TN];
 #pragma unroll
-    for (int q = 0; q < kRound; ++q) {
-      const f32x16& v = acc[(q0 + q) / TN][(q0 + q) % TN];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) part[wave][q][e][lane] = f32x4{v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]};
-    }
-    __syncthreads();
-    const int mine = (wave + W - q0 % W) % W;   // another set of waves each round
-    if (mine >= kRound) continue;
-    f32x16 s;
-#pragma unroll
-    for (int e = 0; e < 16; ++e) s[e] = 0.f;
-#pragma unroll
-    for (int w = 0; w < W; ++w)
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const f32x4 v = part[w][mine][q][lane];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s[4 * q + e] += v[e];
-      }
-    const int at = q0 + mine;
-    finish<EPI, BF16>(g, sh, m, c, i0 + at / TN * 32, j0 + at % TN * 32, s, scratch[mine]);
+    for (int e = 0; e < 4; ++e) part[wave][q][e][lane] = f32x4{v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]};
   }
+  __syncthreads();
+  if (wave >= kProducts) return;
+  f32x16 s;
+#pragma unroll
+  for (int e = 0; e < 16; ++e) s[e] = 0.f;
+#pragma unroll
+  for (int w = 0; w < W; ++w)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const f32x4 v = part[w][wave][q][lane];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[4 * q + e] += v[e];
+    }
+  finish<EPI, BF16>(g, sh, m, c, row0, col0, s, own, scratch[wave]);
 }
 
 template <int EPI>
@@ -596,7 +619,7 @@ template <int TM, int TN, int W, int EPI, bool BF16>
 hipError_t product_small(const ProductPair& g, int pairs, ProductShape sh, const MuonArgs& m, hipStream_t s) {
   sh.tiles = tiles_of<EPI>(sh, 1);
   hipLaunchKernelGGL((muon_product_small<TM, TN, W, EPI, BF16>),
-                     dim3((unsigned)sh.tiles, 1, (unsigned)(pairs * sh.count)), dim3(64 * W), 0, s, g, sh, m);
+                     dim3((unsigned)sh.tiles * (unsigned)(pairs * sh.count)), dim3(64 * W), 0, s, g, sh, m);
   return hipGetLastError();
 }
 
@@ -607,7 +630,7 @@ hipError_t product_t(const ProductPair& g, int pairs, ProductShape sh, const Muo
                      hipStream_t s) {
   sh.tiles = tiles_of<EPI>(sh, T::kCols / T::kRows);
   const unsigned z = (unsigned)(pairs * sh.count);
-  hipLaunchKernelGGL((muon_product<T, EPI, BF16>), dim3((unsigned)(sh.tiles * sh.splits), 1, z),
+  hipLaunchKernelGGL((muon_product<T, EPI, BF16>), dim3((unsigned)(sh.tiles * sh.splits) * z),
                      dim3(64 * T::kWaves), 0, s, g, sh, m, partial);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || sh.splits == 1) return e;
