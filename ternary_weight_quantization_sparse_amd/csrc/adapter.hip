@@ -97,6 +97,11 @@ __global__ __launch_bounds__(64 * kShrinkWaves) void adapter_shrink_mfma(Adapter
   const int id = token < tokens ? ad.ids[token] : -1;
   const uint16_t* xr = x + (token < tokens ? token : tokens - 1) * k + 8 * q;
   const int steps = (int)(k / 32);
+  // the first turn's tokens are on their way while the adapters are looked up
+  u32x4 x0[kShrinkAhead];
+#pragma unroll
+  for (int u = 0; u < kShrinkAhead; ++u)
+    x0[u] = *reinterpret_cast<const u32x4*>(xr + (int64_t)(wave + u * kShrinkWaves < steps ? wave + u * kShrinkWaves : 0) * 32);
   int slot = 0;
   for (int done = -1;; slot = (slot + 1) % kShrinkSlots) {
     int next = id > done && id < ad.count ? id : ad.count;
@@ -106,14 +111,13 @@ __global__ __launch_bounds__(64 * kShrinkWaves) void adapter_shrink_mfma(Adapter
     if (c >= ad.count) break;
     done = c;
     if (slot != (int)blockIdx.z) continue;
-    const int rank = adapter_rank(ad, c);
-    if (r0 >= rank) continue;
-    const float scale = ad.scale[c];
-    // rows past the rank repeat its last: their sums are not used
+    // rows past the stored ones repeat the last; sums of rows past the rank are not used
     const uint16_t* ar[kShrinkRows];
 #pragma unroll
     for (int i = 0; i < kShrinkRows; ++i)
-      ar[i] = ad.a + ((int64_t)c * ad.rank + min(r0 + i * 16 + r, rank - 1)) * k + 8 * q;
+      ar[i] = ad.a + ((int64_t)c * ad.rank + min(r0 + i * 16 + r, ad.rank - 1)) * k + 8 * q;
+    const int rank = adapter_rank(ad, c);
+    const float scale = ad.scale[c];
     f32x4 acc[kShrinkRows];
 #pragma unroll
     for (int i = 0; i < kShrinkRows; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -123,7 +127,7 @@ __global__ __launch_bounds__(64 * kShrinkWaves) void adapter_shrink_mfma(Adapter
       for (int u = 0; u < kShrinkAhead; ++u) {
         // a step past the end repeats this turn's first one; it is not added
         const int64_t at = (int64_t)(s + u * kShrinkWaves < steps ? s + u * kShrinkWaves : s) * 32;
-        xv[u] = *reinterpret_cast<const u32x4*>(xr + at);
+        xv[u] = s == wave ? x0[u] : *reinterpret_cast<const u32x4*>(xr + at);
 #pragma unroll
         for (int i = 0; i < kShrinkRows; ++i) av[u][i] = *reinterpret_cast<const u32x4*>(ar[i] + at);
       }
@@ -135,6 +139,7 @@ __global__ __launch_bounds__(64 * kShrinkWaves) void adapter_shrink_mfma(Adapter
             acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, av[u][i]),
                                                              __builtin_bit_cast(bf16x8, xv[u]), acc[i], 0, 0, 0);
     }
+    if (r0 >= rank) continue;
     __syncthreads();   // the last adapter's sums have been read
 #pragma unroll
     for (int i = 0; i < kShrinkRows; ++i) part[wave][i][lane] = acc[i];

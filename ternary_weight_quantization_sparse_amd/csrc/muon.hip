@@ -114,16 +114,41 @@ __global__ __launch_bounds__(kThreads) void muon_momentum(MuonArgs a, float* __r
   __shared__ double part[kThreads / 64];
   const int64_t size = a.n * a.k, c = blockIdx.y;
   double s = 0.0;
-  for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < size; i += (int64_t)gridDim.x * kThreads) {
-    const int64_t at = c * size + i;
-    float v = get1<BF16>(a.grad, at);
-    if (a.buf) {
-      const float b = a.momentum * get1<BF16>(a.buf, at) + v;
-      put1<BF16>(a.buf_out, at, b);
-      v = a.nesterov ? v + a.momentum * b : b;
+  // eight elements a thread where everything is 16-byte aligned, else one
+  const auto low = [](const void* p) { return reinterpret_cast<uintptr_t>(p); };
+  const bool wide = size % 8 == 0 && ((low(a.grad) | low(a.buf) | low(a.buf_out)) & 15) == 0;
+  const int64_t step = (int64_t)gridDim.x * kThreads, first = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+  if (wide) {
+    for (int64_t i = first * 8; i < size; i += step * 8) {
+      const int64_t at = c * size + i;
+      float v[8];
+      get8<BF16>(a.grad, at, v);
+      if (a.buf) {
+        float b[8];
+        get8<BF16>(a.buf, at, b);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          b[e] = a.momentum * b[e] + v[e];
+          v[e] = a.nesterov ? v[e] + a.momentum * b[e] : b[e];
+        }
+        put8<BF16>(a.buf_out, at, b);
+      }
+      put8<false>(u, at, v);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) s += (double)v[e] * (double)v[e];
     }
-    u[at] = v;
-    s += (double)v * (double)v;
+  } else {
+    for (int64_t i = first; i < size; i += step) {
+      const int64_t at = c * size + i;
+      float v = get1<BF16>(a.grad, at);
+      if (a.buf) {
+        const float b = a.momentum * get1<BF16>(a.buf, at) + v;
+        put1<BF16>(a.buf_out, at, b);
+        v = a.nesterov ? v + a.momentum * b : b;
+      }
+      u[at] = v;
+      s += (double)v * (double)v;
+    }
   }
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) s += __shfl_xor(s, o);
@@ -753,7 +778,7 @@ MuonPlan plan_muon(int count, int64_t n, int64_t k, bool loose) {
   p.rp = (p.r + pad - 1) / pad * pad;
   p.lp = (p.l + pad - 1) / pad * pad;
   p.group = loose && p.l >= 2 * p.r ? 3 : 1;
-  p.parts = std::min<int64_t>(1024, (n * k + 4 * kThreads - 1) / (4 * kThreads));
+  p.parts = std::min<int64_t>(1024, (n * k + 8 * kThreads - 1) / (8 * kThreads));
   const size_t c = (size_t)count;
   size_t at = 0;
   auto take = [&](size_t bytes) {
