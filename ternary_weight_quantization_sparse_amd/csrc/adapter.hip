@@ -73,9 +73,9 @@ __global__ __launch_bounds__(256) void adapter_finish(AdapterArgs ad, const floa
 }
 
 // Prefill: v of 16 tokens and 16 kShrinkRows rows of a on MFMA (A operand: the
-// rows, B operand: the tokens).  The workgroup's waves take every 8th step of
-// 32 k, four steps' loads in flight each, and add their sums through LDS in wave
-// order.  The tile's adapters, in rising order, go to kShrinkSlots workgroups in
+// rows, B operand: the tokens).  The workgroup's waves take every 8th 64 k (a
+// memory line of each row: two steps, lane q with 16 consecutive values), two
+// in flight each, and add their sums through LDS in wave order.  The tile's adapters, in rising order, go to kShrinkSlots workgroups in
 // turn, so a tile in which one request ends and the next begins takes no
 // longer.  v is kept as two bf16 terms, hi + lo (16 bits), as the product's
 // epilogue multiplies it.
@@ -95,13 +95,18 @@ __global__ __launch_bounds__(64 * kShrinkWaves) void adapter_shrink_mfma(Adapter
   const int r0 = blockIdx.y * (16 * kShrinkRows);
   const int64_t token = (int64_t)blockIdx.x * 16 + r;
   const int id = token < tokens ? ad.ids[token] : -1;
-  const uint16_t* xr = x + (token < tokens ? token : tokens - 1) * k + 8 * q;
-  const int steps = (int)(k / 32);
+  const uint16_t* xr = x + (token < tokens ? token : tokens - 1) * k + 16 * q;
+  const int chunks = (int)(k / 64);
   // the first turn's tokens are on their way while the adapters are looked up
+  // (a step past the end repeats the turn's first one; it is not added)
+  auto at = [&](int s, int u) {
+    const int chunk = s + u / 2 * kShrinkWaves;
+    return (int64_t)(chunk < chunks ? chunk : s) * 64 + u % 2 * 8;
+  };
   u32x4 x0[kShrinkAhead];
 #pragma unroll
   for (int u = 0; u < kShrinkAhead; ++u)
-    x0[u] = *reinterpret_cast<const u32x4*>(xr + (int64_t)(wave + u * kShrinkWaves < steps ? wave + u * kShrinkWaves : 0) * 32);
+    x0[u] = wave < chunks ? *reinterpret_cast<const u32x4*>(xr + at(wave, u)) : u32x4{0u, 0u, 0u, 0u};
   int slot = 0;
   for (int done = -1;; slot = (slot + 1) % kShrinkSlots) {
     int next = id > done && id < ad.count ? id : ad.count;
@@ -115,25 +120,23 @@ __global__ __launch_bounds__(64 * kShrinkWaves) void adapter_shrink_mfma(Adapter
     const uint16_t* ar[kShrinkRows];
 #pragma unroll
     for (int i = 0; i < kShrinkRows; ++i)
-      ar[i] = ad.a + ((int64_t)c * ad.rank + min(r0 + i * 16 + r, ad.rank - 1)) * k + 8 * q;
+      ar[i] = ad.a + ((int64_t)c * ad.rank + min(r0 + i * 16 + r, ad.rank - 1)) * k + 16 * q;
     const int rank = adapter_rank(ad, c);
     const float scale = ad.scale[c];
     f32x4 acc[kShrinkRows];
 #pragma unroll
     for (int i = 0; i < kShrinkRows; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-    for (int s = wave; s < steps; s += kShrinkAhead * kShrinkWaves) {
+    for (int s = wave; s < chunks; s += kShrinkAhead / 2 * kShrinkWaves) {
       u32x4 xv[kShrinkAhead], av[kShrinkAhead][kShrinkRows];
 #pragma unroll
       for (int u = 0; u < kShrinkAhead; ++u) {
-        // a step past the end repeats this turn's first one; it is not added
-        const int64_t at = (int64_t)(s + u * kShrinkWaves < steps ? s + u * kShrinkWaves : s) * 32;
-        xv[u] = s == wave ? x0[u] : *reinterpret_cast<const u32x4*>(xr + at);
+        xv[u] = s == wave ? x0[u] : *reinterpret_cast<const u32x4*>(xr + at(s, u));
 #pragma unroll
-        for (int i = 0; i < kShrinkRows; ++i) av[u][i] = *reinterpret_cast<const u32x4*>(ar[i] + at);
+        for (int i = 0; i < kShrinkRows; ++i) av[u][i] = *reinterpret_cast<const u32x4*>(ar[i] + at(s, u));
       }
 #pragma unroll
       for (int u = 0; u < kShrinkAhead; ++u)
-        if (s + u * kShrinkWaves < steps)
+        if (s + u / 2 * kShrinkWaves < chunks)
 #pragma unroll
           for (int i = 0; i < kShrinkRows; ++i)
             acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, av[u][i]),
