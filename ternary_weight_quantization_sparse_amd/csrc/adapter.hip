@@ -5,6 +5,13 @@
 // Two low-rank products around the packed one: v[m] = scale_c A_c x[m] (rank
 // values a token), then B_c v[m] added to the packed product's fp32 result
 // before y is rounded.
+//
+// Decode is two launches: the packed product's K ranges with v beside them (the
+// same launch), and adapter_finish.  Latency and the call's host side bound it: 16 tokens x 16384 x
+// 2048 with rank 64, 8.1 us and 8.6 us (34 MB of b), 18 us a call; by itself
+// the packed product's call takes 17.  Prefill is v, then the packed product's GEMM
+// with B_c v in its epilogue: 2048 tokens x 16384 x 2048, rank 64, 13 us and 163
+// us; without adapters that GEMM takes 124.
 #include <algorithm>
 
 #include "ops_internal.h"

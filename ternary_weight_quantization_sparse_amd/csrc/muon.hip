@@ -27,8 +27,10 @@
 // weights do not see it.
 //
 // The matrix cores bound the large sizes, at the clock that their power leaves:
-// 2048 x 8192 (fp32) runs its products over X at 1.1 PFLOP/s of float16, the matrix cores 79%
-// busy at 1.7 GHz.  Small ones are bound by 17 launches of about 5 us.
+// 2048 x 8192 runs its products with X at 1.1 PFLOP/s of float16 (185 us each),
+// the matrix cores 70% busy at 1.8 GHz; a step of an 8192 x 2048 fp32 weight takes 1.18 ms, 1.68
+// PFLOP of float16 if every step went over X.  Small ones are bound by their 15 to 17
+// launches of about 5 us (256 x 512: 85 us).
 #include <algorithm>
 
 #include "ops_internal.h"
@@ -777,7 +779,8 @@ MuonPlan plan_muon(int count, int64_t n, int64_t k, bool loose) {
   for (const MuonCut& c : {p.gram, p.sym, p.pair, p.apply, p.last}) pad = std::max<int64_t>(pad, c.cols);
   p.rp = (p.r + pad - 1) / pad * pad;
   p.lp = (p.l + pad - 1) / pad * pad;
-  p.group = loose && p.l >= 2 * p.r ? 3 : 1;
+  // two launches more, less work: not where launches are all there is (256 x 512)
+  p.group = loose && p.l >= 2 * p.r && p.apply.rows > 32 ? 3 : 1;
   p.parts = std::min<int64_t>(1024, (n * k + 8 * kThreads - 1) / (8 * kThreads));
   const size_t c = (size_t)count;
   size_t at = 0;
