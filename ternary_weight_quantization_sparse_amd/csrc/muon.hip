@@ -30,7 +30,7 @@
 // 2048 x 8192 runs its products with X at 1.1 PFLOP/s of float16 (185 us each),
 // the matrix cores 70% busy at 1.8 GHz; a step of an 8192 x 2048 fp32 weight takes 1.18 ms, 1.68
 // PFLOP of float16 if every step went over X.  Small ones are bound by their 15 to 17
-// launches of about 5 us (256 x 512: 85 us).
+// launches of about 5 us (256 x 512: 82 us).
 #include <algorithm>
 
 #include "ops_internal.h"
