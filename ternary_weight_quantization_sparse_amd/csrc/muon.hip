@@ -94,6 +94,15 @@ template <bool BF16> __device__ inline void get8(const void* p, int64_t i, float
     for (int e = 0; e < 4; ++e) { v[e] = a[e]; v[4 + e] = b[e]; }
   }
 }
+template <bool BF16> __device__ inline f32x4 get4(const void* p, int64_t i) {
+  if constexpr (BF16) {
+    const uint2 r = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + i);
+    return f32x4{__uint_as_float(r.x << 16), __uint_as_float(r.x & 0xFFFF0000u), __uint_as_float(r.y << 16),
+                 __uint_as_float(r.y & 0xFFFF0000u)};
+  } else {
+    return *reinterpret_cast<const f32x4*>(static_cast<const float*>(p) + i);
+  }
+}
 template <bool BF16> __device__ inline void put8(void* p, int64_t i, const float (&v)[8]) {
   if constexpr (BF16) {
     uint32_t d[4];
@@ -109,7 +118,8 @@ template <bool BF16> __device__ inline void put8(void* p, int64_t i, const float
 }
 
 // Momentum, and the sum of squares of u in doubles (no overflow or underflow
-// for any fp32 gradient), one partial a workgroup.
+// for any fp32 gradient), one partial a workgroup.  Without momentum u is the
+// gradient itself and is not written (u null).
 template <bool BF16>
 __global__ __launch_bounds__(kThreads) void muon_momentum(MuonArgs a, float* __restrict__ u,
                                                           double* __restrict__ sums) {
@@ -135,7 +145,7 @@ __global__ __launch_bounds__(kThreads) void muon_momentum(MuonArgs a, float* __r
         }
         put8<BF16>(a.buf_out, at, b);
       }
-      put8<false>(u, at, v);
+      if (u) put8<false>(u, at, v);
 #pragma unroll
       for (int e = 0; e < 8; ++e) s += (double)v[e] * (double)v[e];
     }
@@ -148,7 +158,7 @@ __global__ __launch_bounds__(kThreads) void muon_momentum(MuonArgs a, float* __r
         put1<BF16>(a.buf_out, at, b);
         v = a.nesterov ? v + a.momentum * b : b;
       }
-      u[at] = v;
+      if (u) u[at] = v;
       s += (double)v * (double)v;
     }
   }
@@ -167,47 +177,58 @@ struct SplitOut {
 };
 
 // u / (|u| + eps) as split rows and as split columns, zeros in the padding: a
-// wave per 32 x 32 tile, transposed through LDS.
-__global__ __launch_bounds__(kThreads) void muon_split(const float* __restrict__ u, const double* __restrict__ sums,
+// wave per 32 x 32 tile, transposed through LDS.  The first tile's values are
+// on their way while the norm's partials are added.
+template <bool BF16>
+__global__ __launch_bounds__(kThreads) void muon_split(const void* __restrict__ u, const double* __restrict__ sums,
                                                        int parts, float eps, int64_t n, int64_t k, int64_t np,
                                                        int64_t kp, SplitOut rows, SplitOut cols) {
   __shared__ double part[kThreads / 64];
   __shared__ __attribute__((aligned(16))) float scratch[4][32 * kPad];
   const int64_t c = blockIdx.y;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  float* mine = scratch[wave];
+  const int64_t base = c * n * k;
+  const bool vec = k % 4 == 0 && (reinterpret_cast<uintptr_t>(u) & (BF16 ? 7 : 15)) == 0;
+  const int64_t tiles_k = kp / 32, tiles = np / 32 * tiles_k, step = (int64_t)gridDim.x * 4;
+  int64_t t = (int64_t)blockIdx.x * 4 + wave;
+  f32x4 in[4];
+  auto load = [&](int64_t tile) {
+    const int64_t n0 = tile / tiles_k * 32, k0 = tile % tiles_k * 32;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = i * 8 + (lane >> 3), q = (lane & 7) * 4;
+      in[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+      if (n0 + r < n) {
+        const int64_t src = base + (n0 + r) * k + k0 + q;
+        if (vec) {
+          if (k0 + q < k) in[i] = get4<BF16>(u, src);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (k0 + q + e < k) in[i][e] = get1<BF16>(u, src + e);
+        }
+      }
+    }
+  };
+  if (t < tiles) load(t);
   double s = 0.0;
   for (int i = threadIdx.x; i < parts; i += kThreads) s += sums[c * parts + i];
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) s += __shfl_xor(s, o);
-  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = s;
+  if (lane == 0) part[wave] = s;
   __syncthreads();
   s = (part[0] + part[1]) + (part[2] + part[3]);
   const float mul = (float)((double)kScale / (sqrt(s) + (double)eps));
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  float* mine = scratch[wave];
-  u += c * n * k;
   rows.m += c * rows.size;
   cols.m += c * cols.size;
-  const bool vec = k % 4 == 0;   // u is 256-byte aligned
-  const int64_t tiles_k = kp / 32, tiles = np / 32 * tiles_k;
-  for (int64_t t = (int64_t)blockIdx.x * 4 + wave; t < tiles; t += (int64_t)gridDim.x * 4) {
+  for (; t < tiles; t += step) {
     const int64_t n0 = t / tiles_k * 32, k0 = t % tiles_k * 32;
     __builtin_amdgcn_wave_barrier();
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = i * 8 + (lane >> 3), q = (lane & 7) * 4;
-      f32x4 v{0.f, 0.f, 0.f, 0.f};
-      if (n0 + r < n) {
-        const float* src = u + (n0 + r) * k + k0 + q;
-        if (vec) {
-          if (k0 + q < k) v = *reinterpret_cast<const f32x4*>(src);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (k0 + q + e < k) v[e] = src[e];
-        }
-      }
-      *reinterpret_cast<f32x4*>(mine + r * kPad + q) = v * mul;
-    }
+    for (int i = 0; i < 4; ++i)
+      *reinterpret_cast<f32x4*>(mine + (i * 8 + (lane >> 3)) * kPad + (lane & 7) * 4) = in[i] * mul;
+    if (t + step < tiles) load(t + step);
     __builtin_amdgcn_wave_barrier();
     const int r = lane & 31, h = lane >> 5;
 #pragma unroll
@@ -817,7 +838,7 @@ MuonPlan plan_muon(int count, int64_t n, int64_t k, bool loose) {
 }
 
 hipError_t launch_muon(const MuonPlan& p, const MuonArgs& a, bool bf16, char* ws, hipStream_t s) {
-  float* u = reinterpret_cast<float*>(ws + p.u);
+  float* u = a.buf ? reinterpret_cast<float*>(ws + p.u) : nullptr;
   double* sums = reinterpret_cast<double*>(ws + p.sums);
   const dim3 g1((unsigned)p.parts, (unsigned)a.count);
   if (bf16) hipLaunchKernelGGL((muon_momentum<true>), g1, dim3(kThreads), 0, s, a, u, sums);
@@ -828,8 +849,13 @@ hipError_t launch_muon(const MuonPlan& p, const MuonArgs& a, bool bf16, char* ws
   const int64_t np = wide ? p.rp : p.lp, kp = wide ? p.lp : p.rp;
   const SplitOut x{reinterpret_cast<f16*>(ws + p.x), p.rp, p.rp * p.lp * 2};
   const SplitOut xt{reinterpret_cast<f16*>(ws + p.xt0), p.lp, p.lp * p.rp * 2};
-  hipLaunchKernelGGL(muon_split, dim3((unsigned)std::min<int64_t>(2048, (np / 32 * (kp / 32) + 3) / 4), (unsigned)a.count),
-                     dim3(kThreads), 0, s, u, sums, (int)p.parts, a.eps, a.n, a.k, np, kp, wide ? x : xt, wide ? xt : x);
+  const dim3 g2((unsigned)std::min<int64_t>(2048, (np / 32 * (kp / 32) + 3) / 4), (unsigned)a.count);
+  if (!u && bf16)
+    hipLaunchKernelGGL((muon_split<true>), g2, dim3(kThreads), 0, s, a.grad, sums, (int)p.parts, a.eps, a.n, a.k, np, kp,
+                       wide ? x : xt, wide ? xt : x);
+  else
+    hipLaunchKernelGGL((muon_split<false>), g2, dim3(kThreads), 0, s, u ? u : a.grad, sums, (int)p.parts, a.eps, a.n, a.k,
+                       np, kp, wide ? x : xt, wide ? xt : x);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
   return steps(p, a, bf16, ws, s);
