@@ -165,7 +165,8 @@ __global__ __launch_bounds__(64 * kShrinkWaves) void adapter_shrink_mfma(Adapter
         const float v = s[e] * scale;
         const __bf16 h = (__bf16)v;
         hi[e] = __builtin_bit_cast(uint16_t, h);
-        lo[e] = __builtin_bit_cast(uint16_t, (__bf16)(v - (float)h));
+        const float rest = v - (float)h;   // an infinity has none: inf - inf would make y NaN
+        lo[e] = __builtin_bit_cast(uint16_t, (__bf16)(rest == rest ? rest : 0.f));
       }
       *reinterpret_cast<uint2*>(vh + token * ad.rank + row) = make_uint2(hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16));
       *reinterpret_cast<uint2*>(vl + token * ad.rank + row) = make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));

@@ -143,6 +143,18 @@ def test_bad_values_stay_with_their_tokens(tokens):
     assert bool(torch.isnan(got[3]).all()) and not bool(torch.isfinite(got[2]).all())
 
 
+@pytest.mark.parametrize("tokens", [4, 16, 40, 150])
+def test_an_infinite_scale_keeps_its_signs(tokens):
+    """One adapter of rank 1 and infinite scale: its tokens' outputs are the signed infinities of b."""
+    pw, _, x, ad, ids = make(256, 512, "per_group", tokens, 3, 8)
+    ids.fill_(1)
+    ad.rank = torch.tensor([8, 1, 8], dtype=torch.int32, device=DEV)
+    ad.scale[1] = float("inf")
+    want = torch.sign(x.double() @ ad.a[1, 0].double())[:, None] * ad.b[1, :, 0].double() * float("inf")
+    f = S.adapter_gemv if tokens <= 16 else S.adapter_gemm
+    assert torch.equal(f(pw, x, ad, ids).double(), want)
+
+
 def test_one_token_alike_in_both_forms():
     pw, wq, x, ad, ids = make(256, 256, "per_channel", 1, 2, 8)
     ids[0] = 1
