@@ -158,6 +158,19 @@ def block_norm_backward(dh_out, dn, h, w_pre=None, y=None, w_post=None, gate=Non
 def _make_ad():
     torch = _torch()
 
+    class Gradients(torch.autograd.Function):
+        """The gradients in a graph of their own, which cannot be differentiated:
+        they depend on h, y, w_post, w_pre and gate, so without it a second
+        derivative would be wrong in silence."""
+
+        @staticmethod
+        def forward(ctx, *args):
+            return _backward(*args)
+
+        @staticmethod
+        def backward(ctx, *grads):
+            raise RuntimeError("block_norm_ad has first derivatives only")
+
     class BlockNorm(torch.autograd.Function):
         """`block_norm` with `block_norm_backward` as its gradient."""
 
@@ -175,7 +188,8 @@ def _make_ad():
             if dh_out is None and dn is None:
                 return (None,) * 7
             layout, res_scale, eps = ctx.args
-            dh, dw_pre, dy, dw_post, dgate = _backward(layout, dh_out, dn, *ctx.saved_tensors, res_scale, eps, None)
+            grads = Gradients.apply if torch.is_grad_enabled() else _backward   # create_graph, or not
+            dh, dw_pre, dy, dw_post, dgate = grads(layout, dh_out, dn, *ctx.saved_tensors, res_scale, eps, None)
             return dh, dw_pre, dy, dw_post, dgate, None, None
 
     return BlockNorm

@@ -272,6 +272,15 @@ def test_autograd_partial_graphs():
     assert torch.equal(g, ref)
 
 
+def test_second_derivatives_are_refused():
+    """The gradients have no gradient of their own: asking for one raises."""
+    h = torch.randn(3, 64, device=DEV, requires_grad=True)
+    _, n = S.block_norm_ad(h, torch.ones(64, device=DEV))
+    (g,) = torch.autograd.grad(n.sum(), h, create_graph=True)
+    with pytest.raises(RuntimeError):
+        torch.autograd.grad((g + h).sum(), h)
+
+
 def test_refusals():
     h, w = torch.zeros(4, 64, device=DEV), torch.ones(64, device=DEV)
     for kw in (dict(), dict(w_pre=w[:32]), dict(w_pre=w, w_post=w), dict(w_pre=w, res_scale=0.5),
