@@ -153,6 +153,9 @@ __device__ inline void group_sum3(float& a, float& b, float& c, float (*slot)[12
 }
 
 __device__ inline float rnorm(float sum, float rdim, float eps) { return 1.0f / sqrtf(sum * rdim + eps); }
+// r^3 m for a mean m of products with a row of norm 1 / r: r m is of the
+// order of the other factor, r^3 alone would leave fp32's range at 2^43.
+__device__ inline float cubed(float r, float m) { return r * (r * (r * m)); }
 
 // Gate of (row, col): the address of its first element and whether it varies
 // with the column.
@@ -418,7 +421,7 @@ __global__ __launch_bounds__(kThreads) void norm_backward(NormArgs a, NormGrads 
       if (pre) {
         group_sum2<TPR>(s_hh, s_uh, &red2[odd]);
         r_h = rnorm(s_hh, rdim, a.eps);
-        c_h = r_h * r_h * r_h * s_uh * rdim;
+        c_h = cubed(r_h, s_uh * rdim);
       }
       // t and what follows from it
       float v[NPT][V];
@@ -471,7 +474,7 @@ __global__ __launch_bounds__(kThreads) void norm_backward(NormArgs a, NormGrads 
           const float g1[1] = {s_tp};
           store_vec(static_cast<T*>(d.dgate) + row, g1);
         }
-        const float c_y = post ? r_y * r_y * r_y * s_vy * rdim : 0.f;
+        const float c_y = post ? cubed(r_y, s_vy * rdim) : 0.f;
 #pragma unroll
         for (int j = 0; j < NPT; ++j) {
           const int col = (j * TPR + t) * V;
@@ -620,7 +623,7 @@ __global__ __launch_bounds__(kThreads) void norm_backward_long(NormArgs a, NormG
     }
     group_sum2<256>(s_hh, s_uh, &red2[0]);
     r_h = rnorm(s_hh, rdim, a.eps);
-    c_h = r_h * r_h * r_h * s_uh * rdim;
+    c_h = cubed(r_h, s_uh * rdim);
   }
   float s_vy = 0.f, s_tp = 0.f;
   for (int64_t c = threadIdx.x; c < a.dim; c += kThreads) {
@@ -636,7 +639,7 @@ __global__ __launch_bounds__(kThreads) void norm_backward_long(NormArgs a, NormG
   if (a.y) {
     group_sum2<256>(s_vy, s_tp, &red2[1]);
     if (a.gate_kind == SHERRY_GATE_TOKEN && threadIdx.x == 0) put1<T>(d.dgate, row, s_tp);
-    const float c_y = a.w_post ? r_y * r_y * r_y * s_vy * rdim : 0.f;
+    const float c_y = a.w_post ? cubed(r_y, s_vy * rdim) : 0.f;
     for (int64_t c = threadIdx.x; c < a.dim; c += kThreads) {
       const float t = t_at<T, W>(a, d, row, c, h2_at<T, W>(a, row, c, r_y), r_h, c_h);
       const float w = a.w_post ? at1<W>(a.w_post, c) : 1.f;

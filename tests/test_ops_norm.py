@@ -216,6 +216,21 @@ def test_large_and_small_values():
         check(a, dh, dn, eps=0.0)
 
 
+@pytest.mark.parametrize("power", [-45, 45])
+@pytest.mark.parametrize("dim", [100, 512, 2048, 9001])
+def test_gradients_scale_back(dim, power):
+    """Norms do not see a power of two: rows 2^45 times as large or small have gradients as much
+    smaller or larger, to the bit (every product is exact but for its rounding)."""
+    a, (_, dn) = inputs(8, dim, F32, F32, None)
+    by = 2.0 ** power
+    want = S.block_norm_backward(None, dn, a["h"], a["w_pre"], eps=0.0)
+    got = S.block_norm_backward(None, dn, a["h"] * by, a["w_pre"], eps=0.0)
+    assert torch.equal(got[0] * by, want[0]) and torch.equal(got[1], want[1])
+    want = S.block_norm_backward(dn, None, a["h"], y=a["y"], w_post=a["w_post"], eps=0.0)
+    got = S.block_norm_backward(dn, None, a["h"], y=a["y"] * by, w_post=a["w_post"], eps=0.0)
+    assert torch.equal(got[2] * by, want[2]) and torch.equal(got[3], want[3])
+
+
 def test_another_stream():
     a, (dh, dn) = inputs(300, 2048, BF16, F32, "channel")
     s = torch.cuda.Stream()
