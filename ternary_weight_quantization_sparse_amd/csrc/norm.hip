@@ -19,7 +19,7 @@
 // dh', dn -> dy, dh).  A row stays in the registers of one group of threads
 // from its loads to its stores, so every byte moves once.  8192 x 2048 bf16
 // (fp32 norm weights): forward 134 MB in 25.6 us (5.2 TB/s; a copy of 1 GB
-// reaches 5.1), backward 201 MB in 47 us (4.3 TB/s) and 5 us for the column
+// reaches 5.1), backward 201 MB in 47.5 us (4.2 TB/s) and 5 us for the column
 // sums; one row 2.6 us.
 #include <algorithm>
 #include <type_traits>
@@ -752,8 +752,8 @@ bool aligned(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0
 
 // Shares of rows for the column sums.  About 512 workgroups of 256 threads:
 // two a CU, each holding its columns' sums over all its rows, so the partials
-// stay small against the rows themselves (8192 x 2048: 55 us and 5 us of
-// joining; with 1024 workgroups 60 and 8).
+// stay small against the rows themselves (8192 x 2048: 47.5 us and 5 us of
+// joining; with 1024 workgroups 51 and 8.5).
 NormSplit plan_norm_backward(int64_t rows, int64_t dim, int gate_kind, int64_t gate_rows) {
   constexpr int64_t kBlocks = 512;
   NormSplit s{};
