@@ -103,6 +103,20 @@ def test_prefill_wide_tiles(gran):
     check(S.adapter_gemm(pw, x, ad, ids), want, tol, BF16)
 
 
+def test_prefill_past_the_copy_range():
+    """More activations than one launch addresses (2^31 bytes): the next
+    launch's tokens keep their ids and low-rank products."""
+    tokens, k = 131100, 8192
+    pw, wq, _, ad, _ = make(64, k, "per_group", 1, 5, 16)
+    g = torch.Generator(device=DEV).manual_seed(3)
+    x = torch.randn(tokens, k, generator=g, device=DEV, dtype=BF16)
+    ids = (torch.arange(tokens, device=DEV) // 7 % 6).to(torch.int32)
+    y = S.adapter_gemm(pw, x, ad, ids)
+    at = torch.cat([torch.arange(0, 10), torch.arange(130930, 130960), torch.arange(131060, 131100)]).to(DEV)
+    want, tol = reference(wq, x[at], ad, ids[at])
+    check(y[at], want, tol, BF16)
+
+
 @pytest.mark.parametrize("tokens", [3, 16, 33, 300])
 def test_ids(tokens):
     """No adapter, ids out of range, every token its own, one for all; ids in any order."""

@@ -155,6 +155,35 @@ def test_strided_unaligned_and_streams():
     assert torch.equal(got, want)
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("shift", [1, 2, 4])
+def test_even_rows_at_any_element(dtype, shift):
+    """Rows of a multiple of 8 elements that begin at any element, read there as aligned ones are."""
+    base = rand(72 * 80 + shift, seed=shift).to(dtype)
+    g = base[shift:].reshape(72, 80)
+    w, b = g + 1, g * 2
+    assert torch.equal(S.orthogonalize(g), S.orthogonalize(g.clone()))
+    assert all(torch.equal(x, y) for x, y in zip(S.muon_step(w, g, b, 0.1), S.muon_step(w, g.clone(), b, 0.1)))
+
+
+@pytest.mark.parametrize("n,k", [(16384, 16384), (16384, 8)])
+def test_longest_sides(n, k):
+    """One step at the largest side (1 GB a matrix): some rows against 64 bits."""
+    g = rand(n, k, seed=13)
+    got = S.orthogonalize(g, steps=1)
+    a, b, c = S.NEWTON_SCHULZ
+    x = g.double() / (g.double().norm() + 1e-7)
+    at = torch.tensor([0, 1, 4097, 9000, 16382, 16383], device=DEV)
+    if n <= k:
+        m = x @ x.t()
+        rows = b * m[at] + c * (m[at] @ m)
+        want = a * x[at] + rows @ x
+    else:
+        m = x.t() @ x
+        want = a * x[at] + x[at] @ (b * m + c * (m @ m))
+    assert off(got[at], want) < 2e-5
+
+
 def test_transpose_agrees():
     g = rand(150, 333, seed=11)
     assert off(S.orthogonalize(g.t().contiguous()).t(), S.orthogonalize(g).double()) < 1e-4
