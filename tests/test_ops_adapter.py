@@ -117,6 +117,20 @@ def test_prefill_past_the_copy_range():
     check(y[at], want, tol, BF16)
 
 
+@pytest.mark.parametrize("tokens", [1, 5, 16, 40])
+def test_adapters_past_32_bit_offsets(tokens):
+    """2.2e9 elements of b: the last adapters are found."""
+    pw, wq, x, _, _ = make(16384, 256, "per_group", tokens, 1, 8)
+    g = torch.Generator(device=DEV).manual_seed(9)
+    b = torch.randn(2100, 16384, 64, generator=g, device=DEV, dtype=BF16)
+    a = torch.randn(2100, 64, 256, generator=g, device=DEV, dtype=BF16) * 0.1
+    ad = S.AdapterSet(a, b, torch.rand(2100, generator=g, device=DEV))
+    ids = (2099 - torch.arange(tokens, device=DEV) // 3).to(torch.int32)
+    want, tol = reference(wq, x, ad, ids)
+    f = S.adapter_gemv if tokens <= 16 else S.adapter_gemm
+    check(f(pw, x, ad, ids), want, tol, BF16)
+
+
 @pytest.mark.parametrize("tokens", [3, 16, 33, 300])
 def test_ids(tokens):
     """No adapter, ids out of range, every token its own, one for all; ids in any order."""

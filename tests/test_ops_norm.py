@@ -238,6 +238,20 @@ def test_another_stream():
     check(a, dh, dn, stream=s)
 
 
+def test_rows_past_32_bit_offsets():
+    """2.3e9 elements: the last rows are what the same rows by themselves are."""
+    dim, w = 2048, torch.rand(2048, device=DEV) + 0.5
+    h = torch.randn(1100003, dim, device=DEV, dtype=BF16)
+    end = h[-9:].clone()
+    out = S.block_norm(h, w, y=h, w_post=w, res_scale=0.5)
+    for got, want in zip(out, S.block_norm(end, w, y=end, w_post=w, res_scale=0.5)):
+        assert torch.equal(got[-9:], want)
+    del out
+    grads = S.block_norm_backward(h, h, h, w, y=h, w_post=w)
+    want = S.block_norm_backward(end, end, end, w, y=end, w_post=w)
+    assert torch.equal(grads[0][-9:], want[0]) and torch.equal(grads[2][-9:], want[2])
+
+
 def test_repeats_bit_for_bit():
     a, (dh, dn) = inputs(3000, 1024, BF16, F32, "rows", 3)
     kw = {k: v for k, v in a.items() if k != "h"}
