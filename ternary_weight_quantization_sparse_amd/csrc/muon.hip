@@ -796,12 +796,17 @@ MuonPlan plan_muon(int count, int64_t n, int64_t k, bool loose) {
   p.pair = cut_of(p.r, p.r, p.r, 2 * (int64_t)count, true);
   p.apply = cut_of(p.r, p.l, p.r, count, false);
   p.last = n > k ? cut_of(p.l, p.r, p.r, count, false) : p.apply;
-  int64_t pad = 32;   // both sides, so that the tiles of every product are whole
-  for (const MuonCut& c : {p.gram, p.sym, p.pair, p.apply, p.last}) pad = std::max<int64_t>(pad, c.cols);
-  p.rp = (p.r + pad - 1) / pad * pad;
-  p.lp = (p.l + pad - 1) / pad * pad;
   // two launches more, less work: not where launches are all there is (256 x 512)
-  p.group = loose && p.l >= 2 * p.r && p.apply.rows > 32 ? 3 : 1;
+  const bool grouped = p.l >= 2 * p.r && p.apply.rows > 32;
+  p.group = loose && grouped ? 3 : 1;
+  // sides padded so that the tiles of every product are whole (the same for
+  // either `loose`: the workspace is asked for before the steps' form is known)
+  int64_t pr = std::max(p.apply.rows, std::max(p.gram.cols, p.sym.cols)), pl = p.apply.cols;
+  if (grouped) pr = std::max<int64_t>(pr, p.pair.cols);
+  pr = std::max<int64_t>(pr, n > k ? p.last.cols : p.last.rows);
+  pl = std::max<int64_t>(pl, n > k ? p.last.rows : p.last.cols);
+  p.rp = (p.r + pr - 1) / pr * pr;
+  p.lp = (p.l + pl - 1) / pl * pl;
   p.parts = std::min<int64_t>(1024, (n * k + 8 * kThreads - 1) / (8 * kThreads));
   const size_t c = (size_t)count;
   size_t at = 0;
@@ -829,7 +834,7 @@ MuonPlan plan_muon(int count, int64_t n, int64_t k, bool loose) {
   };
   size_t most = part(p.gram, p.rp, p.rp, true, 1);
   most = std::max(most, part(p.sym, p.rp, p.rp, true, 1));
-  most = std::max(most, part(p.pair, p.rp, p.rp, true, 2));
+  if (grouped) most = std::max(most, part(p.pair, p.rp, p.rp, true, 2));
   most = std::max(most, part(p.apply, p.rp, p.lp, false, 1));
   most = std::max(most, part(p.last, p.lp, p.rp, false, 1));
   p.partial = take(most);
