@@ -32,6 +32,7 @@
 // PFLOP of float16 if every step went over X.  Small ones are bound by their 15 to 17
 // launches of about 5 us (256 x 512: 82 us).
 #include <algorithm>
+#include <utility>
 
 #include "ops_internal.h"
 
@@ -671,7 +672,8 @@ hipError_t product_small(const ProductPair& g, int pairs, ProductShape sh, const
   return hipGetLastError();
 }
 
-typedef Tile<2, 2, 2, 4> TileBig;   // 128 x 256
+typedef Tile<2, 2, 2, 4> TileBig;    // 128 x 256
+typedef Tile<2, 2, 4, 2> TileTall;   // 256 x 128
 
 template <class T, int EPI, bool BF16>
 hipError_t product_t(const ProductPair& g, int pairs, ProductShape sh, const MuonArgs& m, f32x4* partial,
@@ -693,6 +695,8 @@ hipError_t product(const ProductPair& g, int pairs, ProductShape sh, MuonCut cut
   sh.tiles_m = (int)(sh.c_high / cut.rows);
   sh.tiles_n = (int)(sh.c_wide / cut.cols);
   sh.splits = cut.splits;
+  if constexpr (EPI == kLast)
+    if (cut.rows == 256) return product_t<TileTall, EPI, BF16>(g, pairs, sh, m, partial, s);
   if (cut.rows == 128) return product_t<TileBig, EPI, BF16>(g, pairs, sh, m, partial, s);
   if (cut.rows == 64) return product_small<2, 2, 4, EPI, BF16>(g, pairs, sh, m, s);
   return product_small<1, 1, 4, EPI, BF16>(g, pairs, sh, m, s);
@@ -795,7 +799,10 @@ MuonPlan plan_muon(int count, int64_t n, int64_t k, bool loose) {
   p.sym = cut_of(p.r, p.r, p.r, count, true);
   p.pair = cut_of(p.r, p.r, p.r, 2 * (int64_t)count, true);
   p.apply = cut_of(p.r, p.l, p.r, count, false);
-  p.last = n > k ? cut_of(p.l, p.r, p.r, count, false) : p.apply;
+  // the result of n > k has X's columns as its rows, so its tile stands upright: the shorter side is
+  // padded to 128 either way (8000 x 600 update: 225 us against 298 with the 128 x 256 tile and 256)
+  p.last = p.apply;
+  if (n > k) std::swap(p.last.rows, p.last.cols);
   // two launches more, less work: not where launches are all there is (256 x 512)
   const bool grouped = p.l >= 2 * p.r && p.apply.rows > 32;
   p.group = loose && grouped ? 3 : 1;

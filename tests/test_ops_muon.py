@@ -60,6 +60,16 @@ def test_shapes(n, k, dtype):
     assert off(got, steps64(g)) < (1e-4 if dtype == F32 else 1e-4 + 2.0 ** -8)
 
 
+@pytest.mark.parametrize("n,k", [(1300, 1300), (600, 5500), (5500, 600), (1420, 1600), (1090, 4100), (4100, 1090)])
+def test_large_tiles_on_ragged_sides(n, k):
+    """Sides that no tile divides, padded to 128 and 256; whole steps and steps in groups."""
+    g = rand(n, k, seed=n)
+    want = steps64(g)
+    assert off(S.orthogonalize(g), want) < 1e-4
+    w, _ = S.muon_step(torch.zeros_like(g), g, torch.zeros_like(g), 1.0, momentum=0.0, scale=1.0)
+    assert off(-w, want) < 1e-4
+
+
 def spectra(n, k):
     yield rand(n, 8, seed=1) @ rand(8, k, seed=2) + 0.01 * rand(n, k, seed=3)
     yield 0.02 * rand(n, k, seed=4) + rand(n, 1, seed=5) @ rand(1, k, seed=6)
