@@ -173,7 +173,7 @@ __global__ __launch_bounds__(kThreads) void norm_forward(NormArgs a) {
   typedef typename Raw<T, V>::type R;
   __shared__ float red[2][4];
   const int t = threadIdx.x % TPR;
-  const int64_t row = (int64_t)blockIdx.x * (kThreads / TPR) + threadIdx.x / TPR;
+  const int64_t row = a.row0 + (int64_t)blockIdx.x * (kThreads / TPR) + threadIdx.x / TPR;
   if (row >= a.rows) return;   // whole waves; a 256-thread group always has its row
   const int dim = a.dim;
   const T* h = static_cast<const T*>(a.h) + row * dim;
@@ -568,7 +568,7 @@ __device__ inline float h2_at(const NormArgs& a, int64_t row, int64_t col, float
 template <typename T, typename W>
 __global__ __launch_bounds__(kThreads) void norm_forward_long(NormArgs a) {
   __shared__ float red[2][4];
-  const int64_t row = blockIdx.x;
+  const int64_t row = a.row0 + blockIdx.x;
   const float rdim = 1.0f / (float)a.dim;
   float r_y = 1.f;
   if (a.w_post) {
@@ -603,7 +603,7 @@ __device__ inline float t_at(const NormArgs& a, const NormGrads& d, int64_t row,
 template <typename T, typename W>
 __global__ __launch_bounds__(kThreads) void norm_backward_long(NormArgs a, NormGrads d) {
   __shared__ float red1[1][4], red2[2][8];
-  const int64_t row = blockIdx.x;
+  const int64_t row = a.row0 + blockIdx.x;
   const float rdim = 1.0f / (float)a.dim;
   float r_y = 1.f, r_h = 0.f, c_h = 0.f;
   if (a.w_post) {
@@ -706,15 +706,32 @@ bool with_shape(int64_t dim, F&& f) {
   return true;
 }
 
+// Kernels with a workgroup for every `per` rows: launches of at most 2^22
+// workgroups each, since a launch holds fewer than 2^32 threads.
+template <typename F>
+hipError_t over_rows(NormArgs a, int64_t per, F&& launch) {
+  constexpr int64_t kMost = (int64_t)1 << 22;
+  for (; a.row0 < a.rows; a.row0 += kMost * per) {
+    launch(a, dim3((unsigned)std::min(kMost, (a.rows - a.row0 + per - 1) / per)));
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
 template <typename T, typename W, int V>
 hipError_t forward_v(const NormArgs& a, hipStream_t s) {
+  hipError_t e = hipSuccess;
   const bool ok = with_shape<T, W, V>(a.dim, [&](auto npt, auto tpr) {
-    constexpr int kRows = kThreads / decltype(tpr)::value;
-    hipLaunchKernelGGL((norm_forward<T, W, V, decltype(npt)::value, decltype(tpr)::value>),
-                       dim3((unsigned)((a.rows + kRows - 1) / kRows)), dim3(kThreads), 0, s, a);
+    e = over_rows(a, kThreads / decltype(tpr)::value, [&](const NormArgs& part, dim3 grid) {
+      hipLaunchKernelGGL((norm_forward<T, W, V, decltype(npt)::value, decltype(tpr)::value>), grid, dim3(kThreads), 0,
+                         s, part);
+    });
   });
-  if (!ok) hipLaunchKernelGGL((norm_forward_long<T, W>), dim3((unsigned)a.rows), dim3(kThreads), 0, s, a);
-  return hipGetLastError();
+  if (ok) return e;
+  return over_rows(a, 1, [&](const NormArgs& part, dim3 grid) {
+    hipLaunchKernelGGL((norm_forward_long<T, W>), grid, dim3(kThreads), 0, s, part);
+  });
 }
 
 template <typename T, typename W, int V>
@@ -725,8 +742,9 @@ hipError_t backward_v(const NormArgs& a, const NormGrads& d, const NormSplit& sp
                          dim3((unsigned)sp.blocks), dim3(kThreads), 0, s, a, d, sp);
     });
     if (!ok) {
-      hipLaunchKernelGGL((norm_backward_long<T, W>), dim3((unsigned)a.rows), dim3(kThreads), 0, s, a, d);
-      hipError_t e = hipGetLastError();
+      const hipError_t e = over_rows(a, 1, [&](const NormArgs& part, dim3 grid) {
+        hipLaunchKernelGGL((norm_backward_long<T, W>), grid, dim3(kThreads), 0, s, part, d);
+      });
       if (e != hipSuccess) return e;
       hipLaunchKernelGGL((norm_columns_long<T, W>),
                          dim3((unsigned)((a.dim + kThreads - 1) / kThreads), (unsigned)sp.blocks), dim3(kThreads), 0,

@@ -100,7 +100,7 @@ int32_t sherry_block_norm(int64_t rows, int64_t dim, const void* h, const void* 
   if ((y && !h_out) || (w_pre && !n_out)) return SHERRY_ERR_NULL;
   const uintptr_t item = dtype == SHERRY_F32 ? 4 : 2;
   if (!multiple_of(h_out, item) || !multiple_of(n_out, item)) return SHERRY_ERR_ALIGN;
-  const NormArgs a{rows, (int)dim, h, y, w_post, w_pre, gate, gate_kind, gate_rows, res_scale, eps, h_out, n_out};
+  const NormArgs a{rows, (int)dim, h, y, w_post, w_pre, gate, gate_kind, gate_rows, res_scale, eps, h_out, n_out, 0};
   return hip_status(launch_norm_forward(a, dtype == SHERRY_BF16, w_dtype == SHERRY_BF16,
                                         static_cast<hipStream_t>(stream)));
 }
@@ -129,7 +129,7 @@ int32_t sherry_block_norm_backward(int64_t rows, int64_t dim, const void* h, con
   if (!aligned16(workspace)) return SHERRY_ERR_ALIGN;
   char* ws = static_cast<char*>(workspace);
   const NormArgs a{rows,      (int)dim, h,       y,       w_post, w_pre, gate, gate_kind,
-                   gate_rows, res_scale, eps, nullptr, nullptr};
+                   gate_rows, res_scale, eps, nullptr, nullptr, 0};
   const NormGrads d{dh_out,
                     w_pre ? dn_out : nullptr,
                     dh,

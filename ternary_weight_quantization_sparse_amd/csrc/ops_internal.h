@@ -16,6 +16,7 @@ struct NormArgs {
   int64_t gate_rows;
   float res_scale, eps;
   void *h_out, *n_out;
+  int64_t row0;              // a launch's first row, where rows take several launches
 };
 struct NormGrads {
   const void *dh_out, *dn_out;

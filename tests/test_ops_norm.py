@@ -322,3 +322,25 @@ def test_refusals():
         S.block_norm(h.half(), w)
     with pytest.raises(ValueError):
         S.block_norm_backward(h[:2], None, h, w)
+
+
+@pytest.mark.parametrize("rows,dim,gate", [((1 << 26) + 8, 8, "token"), ((1 << 26) + 8, 8, "rows"), ((1 << 24) + 3, 129, None)])
+def test_rows_of_more_than_one_launch(rows, dim, gate):
+    """More rows than the 2^32 threads of a launch hold: every row is what it is in a call of its own part."""
+    g = torch.Generator(device=DEV).manual_seed(2)
+    h = torch.randn(rows, dim, generator=g, device=DEV, dtype=BF16)
+    w = torch.rand(dim, generator=g, device=DEV) + 0.5
+    gates = {None: None, "token": torch.randn(rows, 1, generator=g, device=DEV, dtype=BF16),
+             "rows": torch.randn(rows // 8, dim, generator=g, device=DEV, dtype=BF16)}[gate]
+
+    def call(part):
+        if gate is None:
+            return S.block_norm(h[part], w)[1:]
+        per = 8 if gate == "rows" else 1
+        return S.block_norm(h[part], w, y=h[part], w_post=w, gate=gates[part.start // per:part.stop // per])
+
+    out = call(slice(0, rows))
+    step = 1 << 22
+    for at in range(0, rows, step):
+        part = slice(at, min(at + step, rows))
+        assert all(torch.equal(a[part], b) for a, b in zip(out, call(part))), at
