@@ -772,19 +772,14 @@ hipError_t launch_lut(const GemvPlan& p, dim3 grid, hipStream_t s, const uint8_t
     else SHERRY_LUT(1, M_, RW_, KW_);                \
   } while (0)
   const int cfg = p.rw * 100 + p.kw;
-  if constexpr (sizeof...(AD) == 0) {   // launches over many matrices
+  if constexpr (SHERRY_LUT_ROWS > 1) {
     if (cfg == 401 && p.rows_per_thread == 4) {
       SHERRY_LUT_WIN(4, 4, 1);
       return hipSuccess;
     }
-    if (cfg == 801) {
-      SHERRY_LUT_WIN(1, 8, 1);
-      return hipSuccess;
-    }
-  } else if (p.rows_per_thread != 1) {
-    return hipErrorInvalidValue;
   }
   if (cfg == 401) SHERRY_LUT_WIN(1, 4, 1);
+  else if (cfg == 801) SHERRY_LUT_WIN(1, 8, 1);
   else if (cfg == 402) SHERRY_LUT_WIN(1, 4, 2);
   else if (cfg == 404) SHERRY_LUT_WIN(1, 4, 4);
   else if (cfg == 208) {

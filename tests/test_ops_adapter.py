@@ -234,3 +234,15 @@ def test_refusals():
         S.adapter_gemv(pw, x.repeat(5, 1), ad, ids.repeat(5))
     with pytest.raises(ValueError):
         S.adapter_gemm(pw, x[:0], ad, ids[:0])
+
+
+@pytest.mark.parametrize("n", [1048064, 1048065, 1 << 20])
+@pytest.mark.parametrize("gran", ["per_group", "per_channel"])
+def test_one_token_on_the_widest_weights(n, gran):
+    """From N = 1048065 a single call takes workgroups of 512 rows, with adapters as without."""
+    pw, wq, x, ad, ids = make(n, 128, gran, 1, 2, 8)
+    for c in (-1, 1):
+        ids[0] = c
+        want, tol = reference(wq, x, ad, ids)
+        check(S.adapter_gemv(pw, x, ad, ids), want, tol, BF16)
+        check(S.adapter_gemv(pw, x, ad, ids, "float32"), want, tol, F32)
