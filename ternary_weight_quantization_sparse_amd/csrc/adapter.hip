@@ -163,10 +163,11 @@ __global__ __launch_bounds__(64 * kShrinkWaves) void adapter_shrink_mfma(Adapter
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const float v = s[e] * scale;
-        const __bf16 h = (__bf16)v;
-        hi[e] = __builtin_bit_cast(uint16_t, h);
-        const float rest = v - (float)h;   // an infinity has none: inf - inf would make y NaN
-        lo[e] = __builtin_bit_cast(uint16_t, (__bf16)(rest == rest ? rest : 0.f));
+        hi[e] = __builtin_bit_cast(uint16_t, (__bf16)v);
+        // what lies beyond the largest bf16 stays finite; infinities and NaN have no second term
+        if ((hi[e] & 0x7FFFu) == 0x7F80u && __builtin_isfinite(v)) hi[e] -= 1;
+        const float rest = v - __uint_as_float(hi[e] << 16);
+        lo[e] = __builtin_isfinite(v) ? __builtin_bit_cast(uint16_t, (__bf16)rest) : 0u;
       }
       *reinterpret_cast<uint2*>(vh + token * ad.rank + row) = make_uint2(hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16));
       *reinterpret_cast<uint2*>(vl + token * ad.rank + row) = make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));

@@ -488,13 +488,14 @@ __global__ __launch_bounds__(kThreads, AR ? (GRAN != SHERRY_PER_GROUP || MERGE ?
         find_adapter(c);                        // the next one, its rank on the way
         for (int k0 = 0; k0 < rank; k0 += 32) {
           const int kr = k0 + 8 * q;            // this lane's 8 columns of b
+          auto load_b = [&](int i) {
+            const int64_t gn = n0 + wave * kWN + i * 16 + r;
+            return kr < rank && gn < n ? *reinterpret_cast<const u32x4*>(ad.a.b + ((int64_t)c * n + gn) * ad.a.rank + kr)
+                                       : u32x4{0u, 0u, 0u, 0u};
+          };
           u32x4 bw[kTN], vh[kTM], vl[kTM];
 #pragma unroll
-          for (int i = 0; i < kTN; ++i) {
-            const int64_t gn = n0 + wave * kWN + i * 16 + r;
-            bw[i] = kr < rank && gn < n ? *reinterpret_cast<const u32x4*>(ad.a.b + ((int64_t)c * n + gn) * ad.a.rank + kr)
-                                        : u32x4{0u, 0u, 0u, 0u};
-          }
+          for (int i = 0; i < kTN; ++i) bw[i] = load_b(i);
 #pragma unroll
           for (int jj = 0; jj < kTM; ++jj) {
             const bool mine = id[jj] == c && kr < rank;
@@ -502,9 +503,10 @@ __global__ __launch_bounds__(kThreads, AR ? (GRAN != SHERRY_PER_GROUP || MERGE ?
             vh[jj] = mine ? *reinterpret_cast<const u32x4*>(ad.vh + at) : u32x4{0u, 0u, 0u, 0u};
             vl[jj] = mine ? *reinterpret_cast<const u32x4*>(ad.vl + at) : u32x4{0u, 0u, 0u, 0u};
           }
-          // columns past the rank, in b and in v, are zero whatever they hold
+          // columns past the rank, in b and in v, are zero whatever they hold (a
+          // mask at the loads would wait for each in turn)
+          u32x4 keep{~0u, ~0u, ~0u, ~0u};
           if (k0 + 32 > rank) {
-            u32x4 keep;
 #pragma unroll
             for (int e = 0; e < 4; ++e)
               keep[e] = (kr + 2 * e < rank ? 0xFFFFu : 0u) | (kr + 2 * e + 1 < rank ? 0xFFFF0000u : 0u);
@@ -516,18 +518,46 @@ __global__ __launch_bounds__(kThreads, AR ? (GRAN != SHERRY_PER_GROUP || MERGE ?
               vl[jj] &= keep;
             }
           }
-          // added by selection: an infinity or NaN in this adapter's b stays
-          // with its own tokens
+          // Tokens of other adapters have zeros in v, so the sums go straight into
+          // the accumulators.  Infinities and NaN of b (times zero: NaN) count as ones of
+          // their sign here; the sums that they make are added below.
+          uint32_t full = 0;   // bits 15 and 31: an exponent of ones
 #pragma unroll
-          for (int jj = 0; jj < kTM; ++jj)
+          for (int i = 0; i < kTN; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) full |= (bw[i][e] & 0x7F807F80u) + 0x00800080u;
+          const bool bad = __any((full & 0x80008000u) != 0);
+          if (bad)
+#pragma unroll
+            for (int i = 0; i < kTN; ++i)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                if ((bw[i][e] & 0x7F80u) == 0x7F80u) bw[i][e] = (bw[i][e] & 0xFFFF8000u) | 0x3F80u;
+                if ((bw[i][e] & 0x7F800000u) == 0x7F800000u) bw[i][e] = (bw[i][e] & 0x8000FFFFu) | 0x3F800000u;
+              }
+          auto multiply = [&](const u32x4 (&v)[kTM]) {
+#pragma unroll
+            for (int jj = 0; jj < kTM; ++jj)
+#pragma unroll
+              for (int i = 0; i < kTN; ++i)
+                acc[i][jj] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, bw[i]),
+                                                                     __builtin_bit_cast(bf16x8, v[jj]), acc[i][jj], 0, 0, 0);
+          };
+          multiply(vl);
+          multiply(vh);
+          // A sum that b's own infinities and NaN make one is added to its token by
+          // selection, from the first term of v (zero or of its sign; the second need not be).
+          if (bad)
 #pragma unroll
             for (int i = 0; i < kTN; ++i) {
-              const bf16x8 w = __builtin_bit_cast(bf16x8, bw[i]);
-              f32x4 d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, __builtin_bit_cast(bf16x8, vl[jj]),
-                                                                f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
-              d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, __builtin_bit_cast(bf16x8, vh[jj]), d, 0, 0, 0);
+              const bf16x8 w = __builtin_bit_cast(bf16x8, load_b(i) & keep);
 #pragma unroll
-              for (int e = 0; e < 4; ++e) acc[i][jj][e] += id[jj] == c ? d[e] : 0.f;
+              for (int jj = 0; jj < kTM; ++jj) {
+                const f32x4 d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, __builtin_bit_cast(bf16x8, vh[jj]),
+                                                                        f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[i][jj][e] += id[jj] == c && !__builtin_isfinite(d[e]) ? d[e] : 0.f;
+              }
             }
         }
       }

@@ -246,3 +246,60 @@ def test_one_token_on_the_widest_weights(n, gran):
         want, tol = reference(wq, x, ad, ids)
         check(S.adapter_gemv(pw, x, ad, ids), want, tol, BF16)
         check(S.adapter_gemv(pw, x, ad, ids, "float32"), want, tol, F32)
+
+
+def same_as_defined(got, want, tol):
+    """Infinities and NaN where the 64-bit product has them, the rest within bounds."""
+    fine = torch.isfinite(want)
+    assert torch.equal(torch.isnan(got), torch.isnan(want))
+    inf = torch.isinf(want)
+    assert torch.equal(got[inf].double(), want[inf])
+    check(got[fine], want[fine], tol[fine], BF16)
+
+
+@pytest.mark.parametrize("tokens", [3, 16, 40, 150])
+@pytest.mark.parametrize("n,gran", [(256, "per_group"), (256, "per_tensor"), (16384, "per_channel")])
+def test_infinities_in_b_keep_their_signs(tokens, n, gran):
+    """b times its token's a x: signed infinities, whether a x is a bf16 number or not, and NaN where it is zero."""
+    pw, wq, x, ad, ids = make(n, 256, gran, tokens, 3, 16)
+    ids.copy_(torch.arange(tokens, device=DEV) // 2 % 3)
+    ad.scale.fill_(1.0)
+    ad.a[0, 0], ad.a[0, 1] = 0, 0
+    ad.a[0, 0, 5] = 1.0                        # a x is the token's value itself: no second term
+    ad.a[0, 1, 5], ad.a[0, 1, 6] = 1.0, 2 ** -9   # and one that has a second term of either sign
+    x[1, 5] = 0
+    inf = float("inf")
+    ad.b[0, 7, 0], ad.b[0, 60, 1], ad.b[0, 61, 1] = inf, inf, -inf
+    ad.b[1, 100, 15] = -inf
+    ad.b[2, 9, 2] = float("nan")
+    want, tol = reference(wq, x, ad, ids)
+    f = S.adapter_gemv if tokens <= 16 else S.adapter_gemm
+    same_as_defined(f(pw, x, ad, ids), want, tol)
+
+
+@pytest.mark.parametrize("tokens", [3, 40, 150])
+def test_low_rank_sums_past_the_largest_bf16(tokens):
+    """a x between the largest bf16 and the largest fp32 number: finite, as b x it is."""
+    pw, wq, x, ad, ids = make(256, 256, "per_group", tokens, 2, 8)
+    ids.fill_(1)
+    ad.a[1] = 0
+    ad.a[1, 0, 0] = 1.0
+    x[:, 0] = torch.where(torch.arange(tokens, device=DEV) % 2 == 0, 1.0, -1.0).to(BF16)
+    ad.scale[1] = 3.399e38
+    ad.b[1, :, 0] = (ad.b[1, :, 0].double() * 2.0 ** -120).to(BF16)
+    want, tol = reference(wq, x, ad, ids)
+    f = S.adapter_gemv if tokens <= 16 else S.adapter_gemm
+    same_as_defined(f(pw, x, ad, ids), want, tol)
+
+
+@pytest.mark.parametrize("tokens", [3, 40, 150])
+def test_infinities_in_both_factors(tokens):
+    """b and a x infinite at once: their product's sign."""
+    pw, wq, x, ad, ids = make(256, 256, "per_group", tokens, 2, 8)
+    ids.fill_(1)
+    ad.rank = torch.tensor([8, 1], dtype=torch.int32, device=DEV)
+    ad.scale[1] = float("inf")
+    ad.b[1, 9, 0], ad.b[1, 77, 0] = float("inf"), -float("inf")
+    want, tol = reference(wq, x, ad, ids)
+    f = S.adapter_gemv if tokens <= 16 else S.adapter_gemm
+    same_as_defined(f(pw, x, ad, ids), want, tol)
