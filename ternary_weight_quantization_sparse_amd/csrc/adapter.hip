@@ -84,8 +84,7 @@ __global__ __launch_bounds__(256) void adapter_finish(AdapterArgs ad, const floa
 // memory line of each row: two steps, lane q with 16 consecutive values), two
 // in flight each, and add their sums through LDS in wave order.  The tile's adapters, in rising order, go to kShrinkSlots workgroups in
 // turn, so a tile in which one request ends and the next begins takes no
-// longer.  v is kept as two bf16 terms, hi + lo (16 bits), as the product's
-// epilogue multiplies it.
+// longer.  v is kept as the bf16 terms that the product's epilogue multiplies.
 // Latency bounds it (look up the adapter, its rank, the rows): 2048 tokens x
 // 64 rows x 2048 k in 13.9 us with four row tiles a workgroup, 17.6 with one; 517
 // tokens x 16 rows in 7.1 with one, so ranks up to 16 take one.
@@ -93,8 +92,7 @@ constexpr int kShrinkWaves = 8, kShrinkAhead = 4, kShrinkSlots = 2;
 template <int kShrinkRows>
 __global__ __launch_bounds__(64 * kShrinkWaves) void adapter_shrink_mfma(AdapterArgs ad, const uint16_t* __restrict__ x,
                                                                          int64_t k, int64_t tokens,
-                                                                         uint16_t* __restrict__ vh,
-                                                                         uint16_t* __restrict__ vl) {
+                                                                         uint16_t* __restrict__ v) {
   __shared__ f32x4 part[kShrinkWaves][kShrinkRows][64];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -159,18 +157,24 @@ __global__ __launch_bounds__(64 * kShrinkWaves) void adapter_shrink_mfma(Adapter
       f32x4 s = part[0][wave][lane];
 #pragma unroll
       for (int w = 1; w < kShrinkWaves; ++w) s += part[w][wave][lane];
-      uint32_t hi[4], lo[4];
+      uint32_t term[kAdapterTerms][4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const float v = s[e] * scale;
-        hi[e] = __builtin_bit_cast(uint16_t, (__bf16)v);
-        // what lies beyond the largest bf16 stays finite; infinities and NaN have no second term
-        if ((hi[e] & 0x7FFFu) == 0x7F80u && __builtin_isfinite(v)) hi[e] -= 1;
-        const float rest = v - __uint_as_float(hi[e] << 16);
-        lo[e] = __builtin_isfinite(v) ? __builtin_bit_cast(uint16_t, (__bf16)rest) : 0u;
+        float rest = s[e] * scale;
+        const bool finite = __builtin_isfinite(rest);
+#pragma unroll
+        for (int t = 0; t < kAdapterTerms; ++t) {
+          uint32_t h = __builtin_bit_cast(uint16_t, (__bf16)rest);
+          // what lies beyond the largest bf16 stays finite; infinities and NaN have no further terms
+          if ((h & 0x7FFFu) == 0x7F80u && finite) h -= 1;
+          term[t][e] = t == 0 || finite ? h : 0u;
+          rest -= __uint_as_float(h << 16);
+        }
       }
-      *reinterpret_cast<uint2*>(vh + token * ad.rank + row) = make_uint2(hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16));
-      *reinterpret_cast<uint2*>(vl + token * ad.rank + row) = make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
+#pragma unroll
+      for (int t = 0; t < kAdapterTerms; ++t)
+        *reinterpret_cast<uint2*>(v + (t * tokens + token) * ad.rank + row) =
+            make_uint2(term[t][0] | (term[t][1] << 16), term[t][2] | (term[t][3] << 16));
     }
   }
 }
@@ -184,9 +188,9 @@ AdapterPlan plan_adapter(int64_t n, int64_t k, int gran, int group_size, int64_t
     const int splits = plan_gemv(n, k, gran, group_size, (int)tokens, 1).ksplit;
     p.v_offset = up((size_t)splits * (size_t)tokens * (size_t)n * 4);
   } else {
-    p.v_offset = up(plan_gemm(n, k, gran, group_size, tokens, true).workspace_bytes);   // hi, then lo
+    p.v_offset = up(plan_gemm(n, k, gran, group_size, tokens, true).workspace_bytes);
   }
-  p.workspace_bytes = p.v_offset + up((size_t)tokens * (size_t)rank * 4);
+  p.workspace_bytes = p.v_offset + up((size_t)tokens * (size_t)rank * (decode ? 4 : 2 * kAdapterTerms));
   return p;
 }
 
@@ -222,19 +226,18 @@ hipError_t launch_adapter_gemv(const AdapterPlan& p, int64_t n, int64_t k, int g
 hipError_t launch_adapter_gemm(const AdapterPlan& p, int64_t n, int64_t k, int gran, int group_size,
                                const uint8_t* packed, const float* alpha, const uint16_t* x, int64_t m, uint16_t* y,
                                const AdapterArgs& ad, char* ws, hipStream_t s) {
-  uint16_t* vh = reinterpret_cast<uint16_t*>(ws + p.v_offset);
-  uint16_t* vl = vh + m * ad.rank;
+  uint16_t* v = reinterpret_cast<uint16_t*>(ws + p.v_offset);
   const unsigned tiles = (unsigned)((m + 15) / 16);
   if (ad.rank <= 16)
     hipLaunchKernelGGL(adapter_shrink_mfma<1>, dim3(tiles, 1, kShrinkSlots), dim3(64 * kShrinkWaves), 0, s, ad, x, k, m,
-                       vh, vl);
+                       v);
   else
     hipLaunchKernelGGL(adapter_shrink_mfma<4>, dim3(tiles, (unsigned)((ad.rank + 63) / 64), kShrinkSlots),
-                       dim3(64 * kShrinkWaves), 0, s, ad, x, k, m, vh, vl);
+                       dim3(64 * kShrinkWaves), 0, s, ad, x, k, m, v);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const GemmPlan g = plan_gemm(n, k, gran, group_size, m, true);
-  const AdapterTerm term{ad, vh, vl};
+  const AdapterTerm term{ad, v, m * ad.rank};
   return launch_gemm_adapted(g, n, k, gran, group_size, packed, alpha, x, m, y,
                              reinterpret_cast<float*>(ws + p.partial_offset), term, s);
 }

@@ -42,9 +42,9 @@
 // Adapters (AD): the epilogue adds each token's low-rank product to the fp32
 // accumulators before their one rounding, on MFMA: for every adapter in use by
 // the tile's tokens, its b rows as the A operand and the tokens' scaled a x as
-// the B operand, added to the tokens of that adapter only.  The fp32 a x go in as two
-// bf16 terms (hi + lo, 16 bits), so the delta loses nothing that y's rounding
-// would keep.
+// the B operand, added to the tokens of that adapter only.  The fp32 a x go in as
+// three bf16 terms, which together are the fp32 value (24 bits): two would lose
+// 2^-18 of the low-rank sum, which shows where y is much smaller than it.
 #include <cmath>
 #include <type_traits>
 
@@ -483,25 +483,28 @@ __global__ __launch_bounds__(kThreads, AR ? (GRAN != SHERRY_PER_GROUP || MERGE ?
       int id[kTM];
 #pragma unroll
       for (int jj = 0; jj < kTM; ++jj) id[jj] = tile_ids[jj * 16 + r];
+      const uint16_t* vt = ad.v + m0 * ad.a.rank;   // the tile's tokens
       while (ad_next < ad.a.count) {
         const int c = ad_next, rank = ad_rank;
+        const uint16_t* bt = ad.a.b + ((int64_t)c * n + n0) * ad.a.rank;   // the tile's rows of b
         find_adapter(c);                        // the next one, its rank on the way
         for (int k0 = 0; k0 < rank; k0 += 32) {
           const int kr = k0 + 8 * q;            // this lane's 8 columns of b
           auto load_b = [&](int i) {
-            const int64_t gn = n0 + wave * kWN + i * 16 + r;
-            return kr < rank && gn < n ? *reinterpret_cast<const u32x4*>(ad.a.b + ((int64_t)c * n + gn) * ad.a.rank + kr)
-                                       : u32x4{0u, 0u, 0u, 0u};
+            const uint32_t at = (uint32_t)(wave * kWN + i * 16 + r);
+            return kr < rank && n0 + at < n ? *reinterpret_cast<const u32x4*>(bt + (at * (uint32_t)ad.a.rank + kr))
+                                            : u32x4{0u, 0u, 0u, 0u};
           };
-          u32x4 bw[kTN], vh[kTM], vl[kTM];
+          u32x4 bw[kTN], v[kAdapterTerms][kTM];
 #pragma unroll
           for (int i = 0; i < kTN; ++i) bw[i] = load_b(i);
 #pragma unroll
           for (int jj = 0; jj < kTM; ++jj) {
             const bool mine = id[jj] == c && kr < rank;
-            const int64_t at = (m0 + jj * 16 + r) * ad.a.rank + kr;
-            vh[jj] = mine ? *reinterpret_cast<const u32x4*>(ad.vh + at) : u32x4{0u, 0u, 0u, 0u};
-            vl[jj] = mine ? *reinterpret_cast<const u32x4*>(ad.vl + at) : u32x4{0u, 0u, 0u, 0u};
+            const uint32_t at = (uint32_t)((jj * 16 + r) * ad.a.rank + kr);
+#pragma unroll
+            for (int t = 0; t < kAdapterTerms; ++t)
+              v[t][jj] = mine ? *reinterpret_cast<const u32x4*>(vt + t * ad.plane + at) : u32x4{0u, 0u, 0u, 0u};
           }
           // columns past the rank, in b and in v, are zero whatever they hold (a
           // mask at the loads would wait for each in turn)
@@ -513,10 +516,9 @@ __global__ __launch_bounds__(kThreads, AR ? (GRAN != SHERRY_PER_GROUP || MERGE ?
 #pragma unroll
             for (int i = 0; i < kTN; ++i) bw[i] &= keep;
 #pragma unroll
-            for (int jj = 0; jj < kTM; ++jj) {
-              vh[jj] &= keep;
-              vl[jj] &= keep;
-            }
+            for (int t = 0; t < kAdapterTerms; ++t)
+#pragma unroll
+              for (int jj = 0; jj < kTM; ++jj) v[t][jj] &= keep;
           }
           // Tokens of other adapters have zeros in v, so the sums go straight into
           // the accumulators.  Infinities and NaN of b (times zero: NaN) count as ones of
@@ -535,25 +537,23 @@ __global__ __launch_bounds__(kThreads, AR ? (GRAN != SHERRY_PER_GROUP || MERGE ?
                 if ((bw[i][e] & 0x7F80u) == 0x7F80u) bw[i][e] = (bw[i][e] & 0xFFFF8000u) | 0x3F80u;
                 if ((bw[i][e] & 0x7F800000u) == 0x7F800000u) bw[i][e] = (bw[i][e] & 0x8000FFFFu) | 0x3F800000u;
               }
-          auto multiply = [&](const u32x4 (&v)[kTM]) {
+#pragma unroll
+          for (int t = kAdapterTerms - 1; t >= 0; --t)
 #pragma unroll
             for (int jj = 0; jj < kTM; ++jj)
 #pragma unroll
               for (int i = 0; i < kTN; ++i)
                 acc[i][jj] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, bw[i]),
-                                                                     __builtin_bit_cast(bf16x8, v[jj]), acc[i][jj], 0, 0, 0);
-          };
-          multiply(vl);
-          multiply(vh);
+                                                                     __builtin_bit_cast(bf16x8, v[t][jj]), acc[i][jj], 0, 0, 0);
           // A sum that b's own infinities and NaN make one is added to its token by
-          // selection, from the first term of v (zero or of its sign; the second need not be).
+          // selection, from the first term of v (zero or of its sign; the others need not be).
           if (bad)
 #pragma unroll
             for (int i = 0; i < kTN; ++i) {
               const bf16x8 w = __builtin_bit_cast(bf16x8, load_b(i) & keep);
 #pragma unroll
               for (int jj = 0; jj < kTM; ++jj) {
-                const f32x4 d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, __builtin_bit_cast(bf16x8, vh[jj]),
+                const f32x4 d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, __builtin_bit_cast(bf16x8, v[0][jj]),
                                                                         f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) acc[i][jj][e] += id[jj] == c && !__builtin_isfinite(d[e]) ? d[e] : 0.f;
@@ -682,8 +682,7 @@ hipError_t launch_g(const GemmPlan& p, int64_t n, int64_t k, int group_sbs, cons
                        mc, group_sbs, tiles_m, tiles_n, sb_per_split, wd, lam, ad);
     if constexpr (AD) {   // the next chunk's tokens
       ad.a.ids += mc;
-      ad.vh += mc * ad.a.rank;
-      ad.vl += mc * ad.a.rank;
+      ad.v += mc * ad.a.rank;
     }
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;

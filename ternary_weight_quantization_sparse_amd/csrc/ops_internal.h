@@ -55,18 +55,20 @@ struct AdapterArgs {
 __device__ inline int adapter_rank(const AdapterArgs& a, int c) {
   return a.ranks ? min(max(a.ranks[c], 0), a.rank) : a.rank;
 }
-// The adapters' term of a product: scale * a x of each token, [tokens, rank],
-// as two bf16 terms.
+// The adapters' term of a product: scale * a x of each token, [tokens, rank], as
+// a sum of bf16 terms, each in a plane of its own, the largest first.
+constexpr int kAdapterTerms = 3;
 struct AdapterTerm {
   AdapterArgs a;
-  const uint16_t *vh, *vl;
+  const uint16_t* v;
+  int64_t plane;
 };
 hipError_t launch_gemm_adapted(const GemmPlan& p, int64_t n, int64_t k, int gran, int group_size,
                                const uint8_t* packed, const float* alpha, const uint16_t* x, int64_t m,
                                uint16_t* y, float* ws, const AdapterTerm& ad, hipStream_t s);
 struct AdapterPlan {
   size_t partial_offset;    // the packed product's workspace: decode, fp32 partials [splits, tokens, N]
-  size_t v_offset;          // low-rank products [tokens, rank]: fp32 (decode), or bf16 hi and lo
+  size_t v_offset;          // low-rank products [tokens, rank]: fp32 (decode), or bf16 terms
   size_t workspace_bytes;
 };
 AdapterPlan plan_adapter(int64_t n, int64_t k, int gran, int group_size, int64_t tokens, int rank, bool decode);

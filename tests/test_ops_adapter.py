@@ -303,3 +303,23 @@ def test_infinities_in_both_factors(tokens):
     want, tol = reference(wq, x, ad, ids)
     f = S.adapter_gemv if tokens <= 16 else S.adapter_gemm
     same_as_defined(f(pw, x, ad, ids), want, tol)
+
+
+@pytest.mark.parametrize("tokens", [3, 40, 700])
+@pytest.mark.parametrize("n", [200, 16384])
+def test_cancelling_low_rank_sums(tokens, n):
+    """Two terms that leave 2^-14 of themselves: a x of fp32's 24 bits (three half-ulps of each term), y rounded
+    once.  16 bits of a x would be off by up to 2^-18 of each."""
+    pw, wq, x, ad, ids = make(n, 128, "per_group", tokens, 3, 8)
+    pw.alpha.mul_(2.0 ** -40)
+    ids.copy_(torch.arange(tokens, device=DEV) % 3)
+    for t in (x, ad.a, ad.b):
+        t.zero_()
+    x[:, 0], x[:, 1] = 1.0, -(1 - 2.0 ** -7)
+    ad.a[:, 0, 0], ad.a[:, 1, 1] = 1.0, 1.0
+    ad.b[:, :, 0], ad.b[:, :, 1] = 1.0, 1 + 2.0 ** -7
+    ad.scale.copy_(torch.tensor([1.2345678, 0.7654321, 1.9996643], device=DEV))
+    want, _ = reference(wq * 2.0 ** -40, x, ad, ids)
+    size = 2.0 * ad.scale[ids.long()].double()[:, None].expand_as(want)
+    f = S.adapter_gemv if tokens <= 16 else S.adapter_gemm
+    check(f(pw, x, ad, ids), want, 3 * 2.0 ** -24 * size, BF16)
