@@ -108,7 +108,10 @@ size_t sherry_muon_workspace_bytes(int32_t count, int64_t n, int64_t k);
  * quintic coefficients five steps bring every singular value that is not far below the
  * norm near 1.  The products keep 22 bits of each factor and fp32 sums.
  *   g, out   [count, N, K] contiguous, dtype SHERRY_F32 or SHERRY_BF16; out may be g.
- *   steps 1..16; coefficients whose iterates stay below 4 and |bA + cAA| below 7.
+ *   steps 1..16.  Coefficients: with m_0 = 1 and m_i+1 the largest |a s + b s^3 + c s^5| of s in [0, m_i]
+ *   (the largest singular value that a step can give), every step has to begin below m_i = 2.82 with
+ *   |b t + c t^2| below 7.98 for t in [0, m_i^2], the range in which the products are kept; others return
+ *   SHERRY_ERR_ARG.
  *   N, K 1 .. 16384, count 1 .. 65535.
  */
 int32_t sherry_orthogonalize(int32_t count, int64_t n, int64_t k, const void* g, int32_t dtype, void* out,

@@ -14,7 +14,8 @@
 // hi hi + hi lo + lo hi, summed in fp32: the result then differs from one in
 // fp32 arithmetic by no more than that differs from 64 bits.  The power of two
 // puts entries down to 1 / sqrt(L) well inside float16's range (lo parts stay
-// normal numbers to 2^-27) and leaves room to 4 for iterates and 7 for b A + c A A.
+// normal numbers to 2^-27) and leaves room below 8 for X, A and b A + c A A, so
+// singular values of an iterate below 2.82; muon_range refuses coefficients that can leave it.
 //
 // Steps in groups.  All factors of X are polynomials of one matrix and commute,
 // so three steps need X only at their start and end: with A = X X^T, B = b A +
@@ -32,6 +33,7 @@
 // PFLOP of float16 if every step went over X.  Small ones are bound by their 15 to 17
 // launches of about 5 us (256 x 512: 82 us).
 #include <algorithm>
+#include <cmath>
 #include <utility>
 
 #include "ops_internal.h"
@@ -49,6 +51,7 @@ constexpr float kScale = 8192.f, kRScale = 1.f / 8192.f, kScaleD = 512.f;
 constexpr int kBK = 16;                 // k of an LDS stage: one 64-byte piece (hi, lo) of a row
 constexpr int kRowB = kBK * 4;
 constexpr int kSlots = 4;               // LDS stages: one read, up to three in flight
+constexpr int kGroupSteps = 3;          // steps between two looks at X, where they are taken in groups
 
 // A split matrix of `rows` rows is kept in the order of the MFMA's operands:
 // for each 16 columns and 32 rows 2 KB, 1 KB of hi values and 1 KB of lo ones,
@@ -768,7 +771,51 @@ hipError_t steps(const MuonPlan& p, const MuonArgs& m, bool bf16, char* ws, hipS
   return hipSuccess;
 }
 
+// The largest |u0 + u1 x + u2 x^2 + u3 x^3| of x in [0, top], at the ends or
+// where the derivative is zero; `odd`: of s times that for x = s^2.
+double largest(const double (&u)[4], double top, bool odd) {
+  auto value = [&](double x) {
+    const double v = u[0] + x * (u[1] + x * (u[2] + x * u[3]));
+    return std::fabs(odd ? std::sqrt(x) * v : v);
+  };
+  double most = std::max(value(0.0), value(top));
+  // (s v(s^2))' = u0 + 3 u1 x + 5 u2 x^2 (u3 = 0); v' = u1 + 2 u2 x + 3 u3 x^2
+  const double p = odd ? u[0] : u[1], q = odd ? 3 * u[1] : 2 * u[2], r = odd ? 5 * u[2] : 3 * u[3];
+  double at[2] = {-1.0, -1.0};
+  if (r == 0.0) {
+    if (q != 0.0) at[0] = -p / q;
+  } else if (q * q >= 4 * p * r) {
+    const double w = -0.5 * (q + std::copysign(std::sqrt(q * q - 4 * p * r), q));
+    at[0] = w / r;
+    if (w != 0.0) at[1] = p / w;
+  }
+  for (double x : at)
+    if (x > 0.0 && x < top) most = std::max(most, value(x));
+  return most;
+}
+
 }  // namespace
+
+// p(s) = a s + b s^3 + c s^5 is 0 at 0 and continuous, so singular values of
+// [0, m] go to [0, max |p|] of it, all of it: the ranges below are exact for
+// single steps.  The product of a group is bounded by its factors' largest values.
+MuonRange muon_range(double a, double b, double c, int steps) {
+  constexpr double kMost = 65504.0 / kScale * 0.999, kMostD = 65504.0 / kScaleD * 0.999;
+  MuonRange fit{true, true};
+  double m = 1.0, product = 1.0, alone = 1.0;   // of a group: P's largest values, and q = a^steps
+  for (int i = 0; i < steps; ++i) {
+    const double top = m * m;
+    if (!(top < kMost) || !(largest({0, b, c, 0}, top, false) < kMost)) fit.steps = false;   // A, B = b A + c A A
+    const bool first = i % kGroupSteps == 0, last = i % kGroupSteps == kGroupSteps - 1 || i + 1 == steps;
+    product = (first ? 1.0 : product) * largest({a, b, c, 0}, top, false);
+    alone = (first ? 1.0 : alone) * std::fabs(a);
+    if (!last && !(largest({0, a, b, c}, top, false) < kMost)) fit.groups = false;           // P A
+    if (!first && !(product + alone < kMostD)) fit.groups = false;                           // D
+    m = largest({a, b, c, 0}, top, true);
+  }
+  fit.groups = fit.groups && fit.steps;
+  return fit;
+}
 
 // Tile and K ranges of a product of `z` matrices C [high, wide], K deep,
 // symmetric or not.  Measured on single products from 128 to 8192 a side:
@@ -805,7 +852,7 @@ MuonPlan plan_muon(int count, int64_t n, int64_t k, bool loose) {
   if (n > k) std::swap(p.last.rows, p.last.cols);
   // two launches more, less work: not where launches are all there is (256 x 512)
   const bool grouped = p.l >= 2 * p.r && p.apply.rows > 32;
-  p.group = loose && grouped ? 3 : 1;
+  p.group = loose && grouped ? kGroupSteps : 1;
   // sides padded so that the tiles of every product are whole (the same for
   // either `loose`: the workspace is asked for before the steps' form is known)
   int64_t pr = std::max(p.apply.rows, std::max(p.gram.cols, p.sym.cols)), pl = p.apply.cols;

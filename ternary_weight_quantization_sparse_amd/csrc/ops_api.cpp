@@ -79,10 +79,12 @@ int run_muon(MuonArgs a, int32_t dtype, void* workspace, size_t workspace_bytes,
     return SHERRY_ERR_ALIGN;
   // groups of steps: not for fp32 results, and only where the coefficients keep
   // a group's product in the range of its float16 planes
-  const bool loose = (dtype == SHERRY_BF16 || a.w) && std::fabs(a.ca) <= 4.0f;
+  const MuonRange range = muon_range(a.ca, a.cb, a.cc, a.steps);
+  const bool loose = (dtype == SHERRY_BF16 || a.w) && range.groups;
   const MuonPlan plan = plan_muon(a.count, a.n, a.k, loose);
   if (!workspace || workspace_bytes < plan.workspace_bytes) return SHERRY_ERR_WORKSPACE;
   if (!aligned16(workspace)) return SHERRY_ERR_ALIGN;
+  if (!range.steps) return SHERRY_ERR_ARG;
   return hip_status(launch_muon(plan, a, dtype == SHERRY_BF16, static_cast<char*>(workspace),
                                 static_cast<hipStream_t>(stream)));
 }

@@ -157,6 +157,12 @@ struct MuonPlan {
   int64_t parts;                  // workgroups of the sum of squares
   size_t u, sums, x, xt0, xt1, a, b, pa, d0, d1, partial, workspace_bytes;
 };
+// Whether everything that the steps keep stays in the range of its float16
+// planes for every matrix of norm 1: taken one by one, and in groups.
+struct MuonRange {
+  bool steps, groups;
+};
+MuonRange muon_range(double a, double b, double c, int steps);
 // loose: steps may be taken in groups (see muon.hip).
 MuonPlan plan_muon(int count, int64_t n, int64_t k, bool loose);
 hipError_t launch_muon(const MuonPlan& p, const MuonArgs& a, bool bf16, char* ws, hipStream_t s);

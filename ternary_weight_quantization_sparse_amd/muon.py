@@ -38,7 +38,9 @@ def _coeffs(coeffs):
 def orthogonalize(g, steps: int = 5, coeffs=None, eps: float = 1e-7, stream=None, out=None):
     """``steps`` Newton-Schulz steps on a matrix ``g`` [N, K], or on each of
     [C, N, K] at once (fp32 or bf16): every singular value that is not far
-    below the largest comes near 1.  Returns g's shape and dtype (``out``, which may be g)."""
+    below the largest comes near 1.  Returns g's shape and dtype (``out``, which may be g).
+    ``coeffs`` (a, b, c) that can raise a singular value above 2.82 before the
+    last step, or |b t + c t^2| (t its square) above 7.98, raise ValueError."""
     torch = _torch()
     code, count, n, k = _matrices(g, "g")
     with _on_stream(stream):
@@ -59,7 +61,7 @@ def muon_step(w, grad, buf, lr: float, momentum: float = 0.95, nesterov: bool = 
         buf' = momentum * buf + grad,   u = grad + momentum * buf'  (buf' without nesterov)
         w' = w * (1 - lr * weight_decay) - lr * scale * orthogonalize(u)
 
-    ``scale`` defaults to sqrt(max(1, N / K)).  Returns ``(w', buf')``, new
+    ``scale`` defaults to sqrt(max(1, N / K)); ``coeffs`` as for `orthogonalize`.  Returns ``(w', buf')``, new
     tensors or ``out``: ``out=(w, buf)`` updates in place."""
     torch = _torch()
     code, count, n, k = _matrices(w, "w")

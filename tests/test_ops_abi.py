@@ -147,3 +147,15 @@ def test_binding_rejects_host_tensors():
     ads = S.AdapterSet(torch.zeros(1, 8, 256), torch.zeros(1, 64, 8), torch.zeros(1))
     with pytest.raises(ValueError):
         S.adapter_gemv(pw, torch.zeros(1, 256), ads, torch.zeros(1, dtype=torch.int32))
+
+
+REFUSED = [((3.3, -0.4, 0.0), 2), ((2.83, 0.0, 0.0), 2), ((8.3, -23.6, 17.3), 1), ((8.3, -23.6, 17.3), 5),
+           ((1.0, 9.0, 0.0), 1), ((3.0, -4.0, 2.0), 5), ((1e30, -1e30, 1e30), 2)]
+
+
+@pytest.mark.parametrize("coeffs,steps", REFUSED)
+def test_muon_refuses_coefficients_that_leave_its_range(lib, coeffs, steps):
+    """A singular value that reaches 2.82 before the last step, or |b t + c t^2| that reaches 8."""
+    a, b, c = coeffs
+    assert muon(lib, a=a, b=b, c=c, steps=steps) == L.ERR_ARG
+    assert lib.sherry_orthogonalize(1, 64, 64, P, L.BF16, P, steps, a, b, c, 1e-7, P, 1 << 40, None) == L.ERR_ARG

@@ -214,3 +214,25 @@ def test_refusals():
         S.muon_step(w, w.bfloat16(), w, 0.1)
     with pytest.raises(ValueError):
         S.muon_step(w, w, w, float("nan"))
+
+
+@pytest.mark.parametrize("coeffs,steps", [((2.82, 0.0, 0.0), 2), ((3.3, -0.4, 0.0), 1), ((1.0, 7.9, 0.0), 1),
+                                          ((4.2, -5.2, 1.6), 5), ((3.9, -5.2, 1.8), 5), ((-3.4445, 4.775, -2.0315), 3)])
+@pytest.mark.parametrize("n,k", [(1, 1), (40, 60), (520, 1200)])
+def test_coefficients_at_the_edge(coeffs, steps, n, k):
+    """Coefficients that just keep what the steps hold in range, single and (updates of 520 x 1200) grouped: 15
+    products of |a| + |b| + |c| ~ 11, 2.5 times as much where steps are grouped."""
+    g = torch.ones(1, 1, device=DEV) if n == 1 else rand(n, k, seed=5)
+    want = steps64(g, steps, coeffs)
+    assert off(S.orthogonalize(g, steps=steps, coeffs=coeffs), want) < 1e-4
+    w, _ = S.muon_step(torch.zeros_like(g), g, torch.zeros_like(g), 1.0, momentum=0.0, scale=1.0, steps=steps, coeffs=coeffs)
+    assert off(-w, want) < 2.5e-4
+
+
+def test_coefficients_out_of_range_are_refused():
+    g = rand(8, 8)
+    for coeffs, steps in (((3.3, -0.4, 0.0), 2), ((8.3, -23.6, 17.3), 5), ((2.83, 0.0, 0.0), 3)):
+        with pytest.raises(ValueError):
+            S.orthogonalize(g, steps=steps, coeffs=coeffs)
+        with pytest.raises(ValueError):
+            S.muon_step(g, g, g, 0.1, steps=steps, coeffs=coeffs)
