@@ -817,6 +817,25 @@ MuonRange muon_range(double a, double b, double c, int steps) {
   return fit;
 }
 
+static int64_t up_to(int64_t side, int64_t tile) { return (side + tile - 1) / tile * tile; }
+
+// Tiles that a matrix's own sides admit, however many there are: the larger
+// one's padding may not cost more products (r r l of the padded sides) than its rate gains.
+// * 64 x 64 against 32 x 32, up to 1.3 times: 2000 x 128 x 128 (1.0) 1877 us
+//   against 2023, 64 x 400 x 400 (1.25) 804 against 825; 300 x 288 x 288 (1.37)
+//   2049 against 1800, 2000 x 96 x 96 (2.4) 1864 against 1133.
+// * 128 x 256 against 64 x 64, up to 1.4 times, or where one matrix by itself is
+//   enough work for it (cut_of): 20 x 1100 x 1100 (1.37) 2690 us against 3150, 256 x
+//   256 x 256 (1.0) 876 against 1095; 64 x 400 x 400 (1.49) 875 against 804, 64 x 300
+//   x 300 (4.1) 855 against 425, 2000 x 128 x 128 (8) 5229 against 1877.
+struct MuonTiles {
+  bool mid, big;
+};
+static MuonTiles tiles_for(int64_t r, int64_t l) {
+  auto products = [&](int64_t t) { return (double)up_to(r, t) * (double)up_to(r, t) * (double)up_to(l, t); };
+  return {products(64) <= 1.3 * products(32), products(256) <= 1.4 * products(64)};
+}
+
 // Tile and K ranges of a product of `z` matrices C [high, wide], K deep,
 // symmetric or not.  Measured on single products from 128 to 8192 a side:
 // * up to 320 tiles of 32 x 32 (one a CU and some): these.  C 512 x 512
@@ -827,25 +846,35 @@ MuonRange muon_range(double a, double b, double c, int steps) {
 // * else 128 x 256 tiles through LDS, K split while the launch stays within 224
 //   workgroups, 24 stages of 16 and 8 ranges: C 2048 x 2048 symmetric, K
 //   2048: 59 us whole, 40 in 3 ranges, 51 in 4; C 1024 x 4096, K 1024: 38 whole, 41 in 2.
-static MuonCut cut_of(int64_t high, int64_t wide, int64_t k, int64_t z, bool sym) {
+static MuonCut cut_of(const MuonTiles& admitted, int64_t high, int64_t wide, int64_t k, int64_t z, bool sym) {
   auto tiles = [&](int64_t h, int64_t w) {
     const int64_t m = (high + h - 1) / h, n = (wide + w - 1) / w;
-    return (sym ? m * (n + 1) / 2 : m * n) * z;
+    return sym ? m * (n + 1) / 2 : m * n;
   };
-  if (tiles(32, 32) <= 320) return {32, 32, 1};
-  if (tiles(64, 64) * k <= 500000) return {64, 64, 1};
-  const int64_t most = std::min<int64_t>(std::min<int64_t>(8, k / 16 / 24), 224 / tiles(128, 256));
-  return {128, 256, (int)std::max<int64_t>(1, most)};
+  constexpr int64_t kBigWork = 500000;
+  if (tiles(32, 32) * z <= 320) return {32, 32, 1};
+  const int64_t work = tiles(64, 64) * k;
+  if (work > kBigWork || (work * z > kBigWork && admitted.big)) {
+    const int64_t most = std::min<int64_t>(std::min<int64_t>(8, k / 16 / 24), 224 / (tiles(128, 256) * z));
+    return {128, 256, (int)std::max<int64_t>(1, most)};
+  }
+  return admitted.mid ? MuonCut{64, 64, 1} : MuonCut{32, 32, 1};
 }
 
-MuonPlan plan_muon(int count, int64_t n, int64_t k, bool loose) {
+MuonPlan plan_muon(int matrices, int64_t n, int64_t k, bool loose) {
   MuonPlan p{};
   p.r = std::min(n, k);
   p.l = std::max(n, k);
-  p.gram = cut_of(p.r, p.r, p.l, count, true);
-  p.sym = cut_of(p.r, p.r, p.r, count, true);
-  p.pair = cut_of(p.r, p.r, p.r, 2 * (int64_t)count, true);
-  p.apply = cut_of(p.r, p.l, p.r, count, false);
+  // Matrices at a time: 2^26 elements keep every CU busy for many tiles, and the
+  // workspace within about 2.5 GB (or one matrix's) and a launch within 2^32 threads for any count.
+  constexpr int64_t kElements = (int64_t)1 << 26;
+  p.count = (int)std::min<int64_t>(matrices, std::max<int64_t>(1, kElements / (up_to(p.r, 32) * up_to(p.l, 32))));
+  const int count = p.count;
+  const MuonTiles admitted = tiles_for(p.r, p.l);
+  p.gram = cut_of(admitted, p.r, p.r, p.l, count, true);
+  p.sym = cut_of(admitted, p.r, p.r, p.r, count, true);
+  p.pair = cut_of(admitted, p.r, p.r, p.r, 2 * (int64_t)count, true);
+  p.apply = cut_of(admitted, p.r, p.l, p.r, count, false);
   // the result of n > k has X's columns as its rows, so its tile stands upright: the shorter side is
   // padded to 128 either way (8000 x 600 update: 225 us against 298 with the 128 x 256 tile and 256)
   p.last = p.apply;
@@ -859,8 +888,8 @@ MuonPlan plan_muon(int count, int64_t n, int64_t k, bool loose) {
   if (grouped) pr = std::max<int64_t>(pr, p.pair.cols);
   pr = std::max<int64_t>(pr, n > k ? p.last.cols : p.last.rows);
   pl = std::max<int64_t>(pl, n > k ? p.last.rows : p.last.cols);
-  p.rp = (p.r + pr - 1) / pr * pr;
-  p.lp = (p.l + pl - 1) / pl * pl;
+  p.rp = up_to(p.r, pr);
+  p.lp = up_to(p.l, pl);
   p.parts = std::min<int64_t>(1024, (n * k + 8 * kThreads - 1) / (8 * kThreads));
   const size_t c = (size_t)count;
   size_t at = 0;
@@ -896,7 +925,8 @@ MuonPlan plan_muon(int count, int64_t n, int64_t k, bool loose) {
   return p;
 }
 
-hipError_t launch_muon(const MuonPlan& p, const MuonArgs& a, bool bf16, char* ws, hipStream_t s) {
+// The plan's matrices at a time.
+static hipError_t launch_part(const MuonPlan& p, const MuonArgs& a, bool bf16, char* ws, hipStream_t s) {
   float* u = a.buf ? reinterpret_cast<float*>(ws + p.u) : nullptr;
   double* sums = reinterpret_cast<double*>(ws + p.sums);
   const dim3 g1((unsigned)p.parts, (unsigned)a.count);
@@ -918,6 +948,23 @@ hipError_t launch_muon(const MuonPlan& p, const MuonArgs& a, bool bf16, char* ws
   e = hipGetLastError();
   if (e != hipSuccess) return e;
   return steps(p, a, bf16, ws, s);
+}
+
+hipError_t launch_muon(const MuonPlan& p, const MuonArgs& a, bool bf16, char* ws, hipStream_t s) {
+  const int64_t item = bf16 ? 2 : 4;
+  for (int at = 0; at < a.count; at += p.count) {
+    auto from = [&](const void* t) { return t ? static_cast<const char*>(t) + at * a.n * a.k * item : nullptr; };
+    MuonArgs part = a;
+    part.count = std::min(p.count, a.count - at);
+    part.w = from(a.w);
+    part.grad = from(a.grad);
+    part.buf = from(a.buf);
+    part.w_out = const_cast<char*>(from(a.w_out));
+    part.buf_out = const_cast<char*>(from(a.buf_out));
+    const hipError_t e = launch_part(p, part, bf16, ws, s);
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 }  // namespace sherry

@@ -151,6 +151,7 @@ struct MuonCut {
   int rows, cols, splits;         // an output tile, and the K ranges of it
 };
 struct MuonPlan {
+  int count;                      // matrices at a time
   int group;                      // steps between two looks at X
   MuonCut gram, sym, pair, apply, last;
   int64_t r, l, rp, lp;           // smaller and larger side, and padded to whole tiles
@@ -164,7 +165,7 @@ struct MuonRange {
 };
 MuonRange muon_range(double a, double b, double c, int steps);
 // loose: steps may be taken in groups (see muon.hip).
-MuonPlan plan_muon(int count, int64_t n, int64_t k, bool loose);
+MuonPlan plan_muon(int matrices, int64_t n, int64_t k, bool loose);
 hipError_t launch_muon(const MuonPlan& p, const MuonArgs& a, bool bf16, char* ws, hipStream_t s);
 
 }  // namespace sherry

@@ -159,3 +159,17 @@ def test_muon_refuses_coefficients_that_leave_its_range(lib, coeffs, steps):
     a, b, c = coeffs
     assert muon(lib, a=a, b=b, c=c, steps=steps) == L.ERR_ARG
     assert lib.sherry_orthogonalize(1, 64, 64, P, L.BF16, P, steps, a, b, c, 1e-7, P, 1 << 40, None) == L.ERR_ARG
+
+
+@pytest.mark.parametrize("n,k", [(8, 8), (64, 64), (96, 100), (128, 128), (300, 300), (16, 2048), (600, 600), (1, 16384)])
+def test_muon_workspace_follows_the_count(lib, n, k):
+    """Bytes grow with the matrices at most by the padding of the tiles that their own sides admit (1.4 times the
+    products of 64-tiles), without a jump, and not past what 2^26 elements of a time need."""
+    f = lib.sherry_muon_workspace_bytes
+    counts = sorted({min(65535, max(1, int(2 ** (i / 4)))) for i in range(65)} | {7811, 7812, 7813, 62499, 62500, 65535})
+    up = lambda x, t: -(-x // t) * t  # noqa: E731
+    r, l = min(n, k), max(n, k)
+    one = 4 * n * k + 3 * 4 * up(r, 64) * up(l, 64) * 1.4 + 5 * 4 * up(r, 64) ** 2 * 1.4   # u; X and its copies; A and the like
+    for c in counts:
+        assert f(c, n, k) <= c * one * 1.01 + (32 << 20), (c, f(c, n, k))   # and partials of split K, sums
+        assert f(c, n, k) < 4 << 30, (c, f(c, n, k))

@@ -236,3 +236,25 @@ def test_coefficients_out_of_range_are_refused():
             S.orthogonalize(g, steps=steps, coeffs=coeffs)
         with pytest.raises(ValueError):
             S.muon_step(g, g, g, 0.1, steps=steps, coeffs=coeffs)
+
+
+@pytest.mark.parametrize("count,n,k", [(131, 1, 16384), (1030, 256, 200), (4100, 100, 128), (65535, 8, 8), (18, 2048, 2040)])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_batches_of_several_launches(count, n, k, dtype):
+    """More matrices than are taken at a time (2^26 elements): those around the cuts and some others against 64 bits."""
+    g = rand(count, n, k, seed=count)
+    g *= torch.logspace(-3, 3, count, device=DEV)[:, None, None]
+    g = g.to(dtype)
+    up = lambda x: -(-x // 32) * 32  # noqa: E731
+    per = (1 << 26) // (up(n) * up(k))
+    at = torch.tensor(sorted({0, 1, per - 1, per, per + 1, count // 2, count - 2, count - 1} & set(range(count))), device=DEV)
+    want = steps64(g[at])
+    got = S.orthogonalize(g)
+    half = 2.0 ** -8 if dtype == BF16 else 0.0
+    for i in range(len(at)):
+        assert off(got[at[i]], want[i]) < 1e-4 + half, int(at[i])
+    if dtype == F32:
+        w, b = S.muon_step(torch.zeros_like(g), g, g, 1.0, momentum=0.5, nesterov=False, scale=1.0)
+        for i in range(len(at)):
+            assert off(-w[at[i]], want[i]) < 2.5e-4, int(at[i])
+        assert torch.equal(b, 1.5 * g)
