@@ -22,10 +22,14 @@
 // c A A, P = a I + B, the next step's A is P A P, and X <- P'' P' P X.  P'' P' P is
 // kept as q I + D (the large part apart), D at 2^9: it reaches a^3.  Where L >=
 // 2 R the R x R products cost less than two passes over X: 38 R^3 against 65 R^3
-// multiply-adds at L = 4 R (1.19 ms against 1.89 ms for 2048 x 8192).  It loses some accuracy (3.0e-6 against
-// 1.8e-6 of the result there), so fp32 results of sherry_orthogonalize, which
-// shows them whole, take every step by itself; bf16 results and the update of
-// weights do not see it.
+// multiply-adds at L = 4 R (1.19 ms against 1.89 ms for 2048 x 8192).  Their roundings reach
+// the result larger, up to what fp32 arithmetic loses on the same steps.  Off from 64
+// bits, of the result, grouped (single steps; fp32 products): Gaussian 512 x 2048
+// 3.1e-6 (1.6e-6; 3.3e-6) and 2048 x 8192 5.2e-6 (2.3e-6; 5.3e-6), rank 8 and a tail
+// 1.1e-5 (1.1e-5; 3.2e-5) and 5.3e-5 (4.1e-5; 6.4e-5), rank 256 and a tail of 2048 x 8192
+// 3.6e-6 (1.5e-6; 3.0e-6).  So sherry_orthogonalize takes every step of fp32
+// matrices by itself; bf16 results and the update of weights, where fp32's own
+// error will do, take groups.  A caller who wants single steps in an update adds the former's result.
 //
 // The matrix cores bound the large sizes, at the clock that their power leaves:
 // 2048 x 8192 runs its products with X at 1.1 PFLOP/s of float16 (185 us each),
