@@ -227,7 +227,11 @@ __global__ __launch_bounds__(kThreads) void muon_split(const void* __restrict__ 
   if (lane == 0) part[wave] = s;
   __syncthreads();
   s = (part[0] + part[1]) + (part[2] + part[3]);
-  const float mul = (float)((double)kScale / (sqrt(s) + (double)eps));
+  // kScale / (|u| + eps) in two factors, the first a power of two: alone it leaves
+  // fp32's range for norms below 2^-115
+  const double norm = sqrt(s) + (double)eps;
+  const float pre = norm < 0x1p-60 ? 0x1p96f : norm > 0x1p60 ? 0x1p-64f : 1.f;
+  const float mul = (float)((double)kScale / (norm * (double)pre));
   rows.m += c * rows.size;
   cols.m += c * cols.size;
   for (; t < tiles; t += step) {
@@ -235,7 +239,7 @@ __global__ __launch_bounds__(kThreads) void muon_split(const void* __restrict__ 
     __builtin_amdgcn_wave_barrier();
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      *reinterpret_cast<f32x4*>(mine + (i * 8 + (lane >> 3)) * kPad + (lane & 7) * 4) = in[i] * mul;
+      *reinterpret_cast<f32x4*>(mine + (i * 8 + (lane >> 3)) * kPad + (lane & 7) * 4) = in[i] * pre * mul;
     if (t + step < tiles) load(t + step);
     __builtin_amdgcn_wave_barrier();
     const int r = lane & 31, h = lane >> 5;

@@ -314,3 +314,13 @@ def test_bf16_results_are_rounded_once_and_repeat():
         junk = [torch.full((1 << 22,), float("nan"), device=DEV) for _ in range(30)]
         del junk
         assert torch.equal(S.orthogonalize(g), first)
+
+
+@pytest.mark.parametrize("std", [1e-38, 1e-36, 1e-34, 5e37])
+@pytest.mark.parametrize("n,k", [(70, 90), (90, 70), (600, 1400)])
+def test_norms_at_the_ends_of_fp32(n, k, std):
+    """Without eps the result does not see the gradient's scale (1e-38: most values are subnormal)."""
+    g = rand(n, k, seed=6) * std
+    want = steps64(g, eps=0.0)
+    assert off(S.orthogonalize(g, eps=0.0), want) < 1e-4
+    assert off(update(g, eps=0.0), want) < 1e-4
