@@ -54,7 +54,7 @@ size_t sherry_block_norm_backward_bytes(int64_t rows, int64_t dim, int32_t gate_
 
 /*
  * sherry_block_norm_backward -- gradients of the above from those of its
- * outputs: dh_out (NULL: zero) and dn_out (NULL: zero), dtype of h.
+ * outputs: dh_out (NULL: zero) and dn_out (NULL: none; dw_pre is zero), dtype of h.
  *   dh, dy   [rows, dim]; dgate the gate's shape; dtype of h.
  *   dw_post, dw_pre   [dim], w_dtype.  Sums over rows are taken in fp32 in an
  *   order fixed by the sizes and rounded once.

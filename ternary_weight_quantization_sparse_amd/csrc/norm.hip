@@ -511,7 +511,10 @@ __global__ __launch_bounds__(kThreads) void norm_join(NormArgs a, NormGrads d, N
   const int slice = threadIdx.x >> 5;
   const int which = blockIdx.y;
   const float* src = which == 0 ? d.part_pre : which == 1 ? d.part_post : d.part_gate;
-  if (!src) return;
+  if (!src) {   // no gradient came from the norm before the next block
+    if (which == 0 && d.dw_pre && slice == 0 && col < a.dim) store_vec(static_cast<W*>(d.dw_pre) + col, {0.f});
+    return;
+  }
   const int64_t q = which < 2 ? 0 : which - 2;
   const int64_t blocks = which < 2 ? sp.blocks : sp.blocks_per_seq;
   src += q * sp.blocks_per_seq * a.dim;
@@ -753,7 +756,7 @@ hipError_t backward_v(const NormArgs& a, const NormGrads& d, const NormSplit& sp
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  if (!a.w_pre && !a.w_post && !d.part_gate) return hipSuccess;
+  if (!d.dw_pre && !a.w_post && !d.part_gate) return hipSuccess;
   hipLaunchKernelGGL((norm_join<T, W>), dim3((unsigned)((a.dim + 31) / 32), (unsigned)(2 + (d.part_gate ? sp.seqs : 0))),
                      dim3(kThreads), 0, s, a, d, sp);
   return hipGetLastError();

@@ -130,16 +130,19 @@ int32_t sherry_block_norm_backward(int64_t rows, int64_t dim, const void* h, con
   if (!workspace || workspace_bytes < w.bytes) return SHERRY_ERR_WORKSPACE;
   if (!aligned16(workspace)) return SHERRY_ERR_ALIGN;
   char* ws = static_cast<char*>(workspace);
-  const NormArgs a{rows,      (int)dim, h,       y,       w_post, w_pre, gate, gate_kind,
+  // a norm that no gradient comes from takes no part: dw_pre is zero, and what h_out
+  // holds (infinities among it) does not meet the other gradients
+  const bool pre = w_pre && dn_out;
+  const NormArgs a{rows,      (int)dim, h,       y,       w_post, pre ? w_pre : nullptr, gate, gate_kind,
                    gate_rows, res_scale, eps, nullptr, nullptr, 0};
   const NormGrads d{dh_out,
-                    w_pre ? dn_out : nullptr,
+                    pre ? dn_out : nullptr,
                     dh,
                     dy,
                     dw_post,
-                    dw_pre,
+                    w_pre ? dw_pre : nullptr,
                     dgate,
-                    w_pre ? reinterpret_cast<float*>(ws + w.pre) : nullptr,
+                    pre ? reinterpret_cast<float*>(ws + w.pre) : nullptr,
                     w_post ? reinterpret_cast<float*>(ws + w.post) : nullptr,
                     w.gate ? reinterpret_cast<float*>(ws + w.gate) : nullptr,
                     reinterpret_cast<float*>(ws + w.stats)};

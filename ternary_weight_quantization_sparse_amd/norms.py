@@ -144,7 +144,7 @@ def block_norm(h, w_pre=None, y=None, w_post=None, gate=None, res_scale: float =
 def block_norm_backward(dh_out, dn, h, w_pre=None, y=None, w_post=None, gate=None, res_scale: float = 1.0,
                         eps: float = 1e-6, stream=None):
     """Gradients ``(dh, dw_pre, dy, dw_post, dgate)`` of `block_norm` from those
-    of its outputs (either may be None: zero), None for absent operands.
+    of its outputs (either may be None: no gradient), None for absent operands.
     h' is recomputed from y and h in fp32, and sums over rows and over a gate's
     broadcast are fp32 in a fixed order."""
     layout = _layout(h, w_pre, y, w_post, gate, res_scale)

@@ -344,3 +344,20 @@ def test_rows_of_more_than_one_launch(rows, dim, gate):
     for at in range(0, rows, step):
         part = slice(at, min(at + step, rows))
         assert all(torch.equal(a[part], b) for a, b in zip(out, call(part))), at
+
+
+@pytest.mark.parametrize("dim", [100, 2048, 9001])
+@pytest.mark.parametrize("eps", [0.0, 1e-6])
+def test_an_unused_norm_takes_no_part(dim, eps):
+    """No gradient from n: the others are those of a call without its norm, whatever h' holds, and dw_pre is zero."""
+    a, (dh, _) = inputs(12, dim, F32, F32, "channel")
+    a["h"][3, 5], a["h"][4], a["y"][4] = float("inf"), 0, 0
+    kw = {k: v for k, v in a.items() if k not in ("h", "w_pre")}
+    got = S.block_norm_backward(dh, None, a["h"], a["w_pre"], eps=eps, **kw)
+    want = S.block_norm_backward(dh, None, a["h"], eps=eps, **kw)
+    assert torch.equal(got[0], want[0]) and bool(torch.isfinite(got[0]).all()) and torch.equal(got[0], dh)
+    for i in (2, 3, 4):
+        assert torch.equal(got[i].nan_to_num(7.0), want[i].nan_to_num(7.0))
+    assert got[1].shape == (dim,) and not got[1].any()
+    alone = S.block_norm_backward(dh, None, a["h"], a["w_pre"], eps=eps)
+    assert torch.equal(alone[0], dh) and not alone[1].any()
