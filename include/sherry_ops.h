@@ -126,7 +126,8 @@ int32_t sherry_orthogonalize(int32_t count, int64_t n, int64_t k, const void* g,
  *   w_out = w * (1 - lr * weight_decay) - lr * scale * orthogonalize(u)
  * Wide and tall matrices take their steps in groups (as sherry_orthogonalize does in bf16): the update is
  * off by up to 2.5 times as much as with steps one by one, about what fp32 products are off by.
- *   w, grad, buf, w_out, buf_out   [count, N, K], one dtype; w_out may be w, buf_out may be buf.
+ *   w, grad, buf, w_out, buf_out   [count, N, K], one dtype; w_out may be w, grad or buf, buf_out grad or buf.
+ *   Outputs that overlap an input otherwise, and buf_out on w or w_out, return SHERRY_ERR_ARG.
  */
 int32_t sherry_muon_step(int32_t count, int64_t n, int64_t k, const void* w, const void* grad, const void* buf,
                          int32_t dtype, void* w_out, void* buf_out, float lr, float momentum, int32_t nesterov,

@@ -85,6 +85,16 @@ int run_muon(MuonArgs a, int32_t dtype, void* workspace, size_t workspace_bytes,
   if (!workspace || workspace_bytes < plan.workspace_bytes) return SHERRY_ERR_WORKSPACE;
   if (!aligned16(workspace)) return SHERRY_ERR_ALIGN;
   if (!range.steps) return SHERRY_ERR_ARG;
+  // an output is an input or apart from it; buf_out is written before w is read, and with w_out
+  const uintptr_t bytes = (uintptr_t)a.count * (uintptr_t)a.n * (uintptr_t)a.k * item;
+  auto apart = [&](const void* p, const void* q) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(p), y = reinterpret_cast<uintptr_t>(q);
+    return !p || !q || (x < y ? y - x : x - y) >= bytes;
+  };
+  for (const void* in : {a.w, a.grad, a.buf})
+    for (const void* out : {static_cast<const void*>(a.w_out), static_cast<const void*>(a.buf_out)})
+      if (in != out && !apart(in, out)) return SHERRY_ERR_ARG;
+  if (!apart(a.buf_out, a.w) || !apart(a.buf_out, a.w_out)) return SHERRY_ERR_ARG;
   return hip_status(launch_muon(plan, a, dtype == SHERRY_BF16, static_cast<char*>(workspace),
                                 static_cast<hipStream_t>(stream)));
 }

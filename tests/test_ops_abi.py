@@ -173,3 +173,16 @@ def test_muon_workspace_follows_the_count(lib, n, k):
     for c in counts:
         assert f(c, n, k) <= c * one * 1.01 + (32 << 20), (c, f(c, n, k))   # and partials of split K, sums
         assert f(c, n, k) < 4 << 30, (c, f(c, n, k))
+
+
+def test_muon_refuses_overlapping_outputs(lib):
+    a, b, c, d = (0x10000000 * i for i in range(1, 5))
+    size = 64 * 64 * 4
+    good = dict(a=1.5, b=-0.5, c=0.0, ws=None)           # in order but for the workspace
+    assert muon(lib, w=a, g=b, buf=c, wo=a, bo=c, **good) == L.ERR_WORKSPACE
+    good["ws"] = P
+    for kw in (dict(wo=a, bo=a), dict(wo=d, bo=a), dict(wo=d, bo=d), dict(wo=a + 16, bo=c), dict(wo=a - size + 4, bo=c),
+               dict(wo=a, bo=c + 16), dict(wo=b + 8, bo=c), dict(wo=d, bo=d + 64)):
+        assert muon(lib, w=a, g=b, buf=c, **kw, **good) == L.ERR_ARG, kw
+    for out in (a + 4, a - 4, a + size - 4):
+        assert lib.sherry_orthogonalize(1, 64, 64, a, L.F32, out, 5, 1.5, -0.5, 0.0, 1e-7, P, 1 << 40, None) == L.ERR_ARG

@@ -324,3 +324,19 @@ def test_norms_at_the_ends_of_fp32(n, k, std):
     want = steps64(g, eps=0.0)
     assert off(S.orthogonalize(g, eps=0.0), want) < 1e-4
     assert off(update(g, eps=0.0), want) < 1e-4
+
+
+def test_outputs_on_inputs():
+    """An output may be an input; the momentum's may not be the weights' (they are read after it is written)."""
+    w, g, b = (rand(64, 96, seed=i) for i in range(3))
+    want = S.muon_step(w, g, b, 0.1)
+    for i in range(3):
+        t = [w.clone(), g.clone(), b.clone()]
+        got = S.muon_step(*t, 0.1, out=(t[i], torch.empty_like(b)))
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    for out in ((w, w), (g, w), (b, b)):
+        with pytest.raises(ValueError):
+            S.muon_step(w, g, b, 0.1, out=out)
+    flat = torch.zeros(2 * w.numel(), device=DEV)
+    with pytest.raises(ValueError):
+        S.orthogonalize(flat[:w.numel()].reshape(w.shape), out=flat[4:4 + w.numel()].reshape(w.shape))
