@@ -10,8 +10,8 @@
 // same launch), and adapter_finish.  Latency and the call's host side bound it: 16 tokens x 16384 x
 // 2048 with rank 64, 8.1 us and 8.6 us (34 MB of b), 18 us a call; by itself
 // the packed product's call takes 17.  Prefill is v, then the packed product's GEMM
-// with B_c v in its epilogue: 2048 tokens x 16384 x 2048, rank 64, 13 us and 163
-// us; without adapters that GEMM takes 124.
+// with B_c v in its epilogue: 2048 tokens x 16384 x 2048, rank 64, 13 us and 149
+// us (at the clocks of a long loop; 179 in the first calls); without adapters that GEMM takes 123.
 #include <algorithm>
 
 #include "ops_internal.h"

@@ -22,7 +22,7 @@
 // c A A, P = a I + B, the next step's A is P A P, and X <- P'' P' P X.  P'' P' P is
 // kept as q I + D (the large part apart), D at 2^9: it reaches a^3.  Where L >=
 // 2 R the R x R products cost less than two passes over X: 38 R^3 against 65 R^3
-// multiply-adds at L = 4 R (1.19 ms against 1.89 ms for 2048 x 8192).  Their roundings reach
+// flops at L = 4 R (8192 x 2048: bf16 in 1.14 ms, fp32, step by step, in 1.65).  Their roundings reach
 // the result larger, up to what fp32 arithmetic loses on the same steps.  Off from 64
 // bits, of the result, grouped (single steps; fp32 products): Gaussian 512 x 2048
 // 3.1e-6 (1.6e-6; 3.3e-6) and 2048 x 8192 5.2e-6 (2.3e-6; 5.3e-6), rank 8 and a tail
@@ -33,8 +33,8 @@
 //
 // The matrix cores bound the large sizes, at the clock that their power leaves:
 // 2048 x 8192 runs its products with X at 1.1 PFLOP/s of float16 (185 us each),
-// the matrix cores 70% busy at 1.8 GHz; a step of an 8192 x 2048 fp32 weight takes 1.18 ms, 1.68
-// PFLOP of float16 if every step went over X.  Small ones are bound by their 15 to 17
+// the matrix cores 70% busy at 1.8 GHz; a step of an 8192 x 2048 fp32 weight takes 1.19 to 1.25
+// ms by card, 0.98 PFLOP of float16 (1.68 if every step went over X).  Small ones are bound by their 15 to 17
 // launches of about 5 us (256 x 512: 82 us).
 #include <algorithm>
 #include <cmath>
