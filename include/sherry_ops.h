@@ -1,8 +1,9 @@
 /*
  * sherry_ops.h -- operators around the packed ternary layer of libsherry:
  * adapters of many requests beside a packed projection, the norms before and
- * after a block with its gate and residual scale, and the orthogonalised
- * (Newton-Schulz) update of latent weights.
+ * after a block with its gate and residual scale, the orthogonalised
+ * (Newton-Schulz) update of latent weights, and the distillation of a student
+ * from a teacher's top logits.
  *
  * Conventions are those of sherry.h (streams as void*, caller-provided
  * workspaces, host-side argument checks before any launch, no allocation, no
@@ -133,6 +134,47 @@ int32_t sherry_muon_step(int32_t count, int64_t n, int64_t k, const void* w, con
                          int32_t dtype, void* w_out, void* buf_out, float lr, float momentum, int32_t nesterov,
                          float weight_decay, float scale, int32_t steps, float a, float b, float c, float eps,
                          void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes of sherry_distill_loss (dtype of the logits); (size_t)-1 on invalid arguments. */
+size_t sherry_distill_workspace_bytes(int64_t rows, int64_t vocab, int32_t dtype);
+
+/*
+ * sherry_distill_loss -- the loss of `rows` student rows s [vocab] against a teacher's `slots` top logits u_j of
+ * ids i_j (t the temperature, q = softmax(s / t)):
+ *
+ *   p_j = exp(u_j / t - teacher_lse), rest = max(0, 1 - sum_j p_j);   teacher_lse NULL: p = softmax(u / t), rest = 0
+ *   kd = t^2 (sum_j p_j log(p_j / q_ij) + rest log(rest / q_rest)),   q_rest = the sum of q outside the ids
+ *   loss = kd_weight kd + (1 - kd_weight) (-log softmax(s)_label)
+ *
+ *   logits   [rows, vocab], dtype SHERRY_F32 or SHERRY_BF16, rows `row_stride` >= vocab elements apart.
+ *   teacher  [rows, slots], teacher_dtype; ids [rows, slots] int32 (ids_64: int64).  A slot whose id lies outside
+ *            [0, vocab) is empty, whatever its logit.  An id in several slots counts once for each, and once as a
+ *            place outside the tail.  A row without a slot (without teacher_lse also one whose logits are all
+ *            -infinity) has kd = 0; where the ids are the whole vocabulary, rest is 0.
+ *   teacher_lse [rows] fp32: log of the sum of exp(u / t) over the teacher's whole vocabulary.
+ *   labels   [rows] int32 (labels_64: int64) or NULL; outside [0, vocab): no label, the second term is 0.
+ *   loss     [rows] fp32.  stats [rows, 4 + slots] fp32 for the backward pass, or NULL.
+ *   A kd_weight of 0 (1) leaves the first (second) term out, whatever it is.
+ *   rows 1 .. 2^31 - 1, vocab 1 .. 2^30, slots 1 .. 1024, temperature 1e-3 .. 1e3; pointers need
+ *   their element's alignment (16-byte aligned rows are not needed for 16-byte loads).  Sums and logarithms of a
+ *   row are taken in 64 bits.
+ */
+int32_t sherry_distill_loss(int64_t rows, int64_t vocab, const void* logits, int64_t row_stride, int32_t dtype,
+                            const void* teacher, int32_t teacher_dtype, const void* ids, int32_t ids_64,
+                            int32_t slots, float temperature, const float* teacher_lse, const void* labels,
+                            int32_t labels_64, float kd_weight, float* loss, float* stats, void* workspace,
+                            size_t workspace_bytes, void* stream);
+
+/*
+ * sherry_distill_loss_backward -- dlogits [rows, vocab], dtype of the logits, from the gradients g [rows] of the
+ * losses and the stats of a sherry_distill_loss with the same arguments.  A row with g = 0 gets zeros and is not
+ * read.  dlogits may be logits (same rows); outputs that overlap them otherwise return SHERRY_ERR_ARG.
+ */
+int32_t sherry_distill_loss_backward(int64_t rows, int64_t vocab, const float* g, const void* logits,
+                                     int64_t row_stride, int32_t dtype, const void* ids, int32_t ids_64,
+                                     int32_t slots, float temperature, const void* labels, int32_t labels_64,
+                                     float kd_weight, const float* stats, void* dlogits, int64_t dlogits_stride,
+                                     void* stream);
 
 #ifdef __cplusplus
 }

@@ -24,7 +24,7 @@ __all__ = [
     "FusedWeight", "quantize_pack_fused", "gemv_fused", "arenas_lambda", "arenas_gemm",
     "compare_repack", "compare_gemv", "gemm_fused", "quantize_pack_noalloc",
     "AdapterSet", "adapter_gemv", "adapter_gemm", "block_norm", "block_norm_backward", "block_norm_ad",
-    "orthogonalize", "muon_step", "NEWTON_SCHULZ",
+    "orthogonalize", "muon_step", "NEWTON_SCHULZ", "distill_loss", "distill_loss_backward", "distill_loss_ad",
 ]
 
 
@@ -70,6 +70,14 @@ def _need_gpu(t, name, device=None):
         raise ValueError(f"{name} must be a CUDA (HIP) tensor")
     if device is not None and t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
+
+
+def _need_current(device):
+    """The kernels go to the current device's stream (inside `_on_stream`: the
+    given stream's device), so that has to be the operands' device."""
+    here = _torch()._C._cuda_getDevice()
+    if device.index != here:
+        raise ValueError(f"the operands are on {device}, the stream is on cuda:{here}")
 
 
 def _need_out(t, name, dtype, numel, device):
@@ -490,5 +498,6 @@ def gemm(pw: PackedWeight, x, stream=None, out=None):
 
 
 from .adapters import AdapterSet, adapter_gemm, adapter_gemv  # noqa: E402
+from .distill import distill_loss, distill_loss_ad, distill_loss_backward  # noqa: E402
 from .muon import NEWTON_SCHULZ, muon_step, orthogonalize  # noqa: E402
 from .norms import block_norm, block_norm_ad, block_norm_backward  # noqa: E402

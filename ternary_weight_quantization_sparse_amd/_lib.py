@@ -40,6 +40,7 @@ OPS_SYMBOLS = (
     "sherry_block_norm", "sherry_block_norm_backward_bytes", "sherry_block_norm_backward",
     "sherry_adapter_workspace_bytes", "sherry_adapter_gemv", "sherry_adapter_gemm",
     "sherry_muon_workspace_bytes", "sherry_orthogonalize", "sherry_muon_step",
+    "sherry_distill_workspace_bytes", "sherry_distill_loss", "sherry_distill_loss_backward",
 )
 
 _i32, _i64, _sz, _vp = ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t, ctypes.c_void_p
@@ -79,6 +80,11 @@ _SIGNATURES = {
     "sherry_orthogonalize": ([_i32, _i64, _i64, _vp, _i32, _vp, _i32, _f32, _f32, _f32, _f32, _vp, _sz, _vp], _i32),
     "sherry_muon_step": ([_i32, _i64, _i64, _vp, _vp, _vp, _i32, _vp, _vp, _f32, _f32, _i32, _f32, _f32, _i32, _f32,
                           _f32, _f32, _f32, _vp, _sz, _vp], _i32),
+    "sherry_distill_workspace_bytes": ([_i64, _i64, _i32], _sz),
+    "sherry_distill_loss": ([_i64, _i64, _vp, _i64, _i32, _vp, _i32, _vp, _i32, _i32, _f32, _vp, _vp, _i32, _f32, _vp,
+                             _vp, _vp, _sz, _vp], _i32),
+    "sherry_distill_loss_backward": ([_i64, _i64, _vp, _vp, _i64, _i32, _vp, _i32, _i32, _f32, _vp, _i32, _f32, _vp,
+                                      _vp, _i64, _vp], _i32),
 }
 
 _lib = None

@@ -99,6 +99,31 @@ int run_muon(MuonArgs a, int32_t dtype, void* workspace, size_t workspace_bytes,
                                 static_cast<hipStream_t>(stream)));
 }
 
+constexpr int64_t kMaxVocab = (int64_t)1 << 30;
+
+int check_distill(int64_t rows, int64_t vocab, const void* logits, int64_t stride, int32_t dtype, const void* ids,
+                  int32_t ids_64, int32_t slots, float temperature, const void* labels, int32_t labels_64,
+                  float kd_weight) {
+  if (rows < 1 || rows > kMaxRows || vocab < 1 || vocab > kMaxVocab || stride < vocab) return SHERRY_ERR_ARG;
+  if (stride > ((int64_t)1 << 60) / rows) return SHERRY_ERR_ARG;
+  if (slots < 1 || slots > kDistillSlots) return SHERRY_ERR_ARG;
+  if (!(temperature >= 1e-3f && temperature <= 1e3f) || !std::isfinite(kd_weight)) return SHERRY_ERR_ARG;
+  if (dtype != SHERRY_F32 && dtype != SHERRY_BF16) return SHERRY_ERR_DTYPE;
+  if (!logits || !ids) return SHERRY_ERR_NULL;
+  if (!multiple_of(logits, dtype == SHERRY_F32 ? 4 : 2) || !multiple_of(ids, ids_64 ? 8 : 4) ||
+      !multiple_of(labels, labels_64 ? 8 : 4))
+    return SHERRY_ERR_ALIGN;
+  return SHERRY_OK;
+}
+
+// log2(e) / t as two fp32 terms, both above zero: a distance of -infinity stays one
+void exp_terms(float temperature, float* hi, float* lo) {
+  const double c = 1.4426950408889634 / (double)temperature;
+  *hi = (float)c;
+  if ((double)*hi >= c) *hi = std::nextafterf(*hi, 0.f);
+  *lo = (float)(c - (double)*hi);
+}
+
 }  // namespace
 
 extern "C" {
@@ -232,6 +257,62 @@ int32_t sherry_muon_step(int32_t count, int64_t n, int64_t k, const void* w, con
   const MuonArgs m{count, n, k, w, grad, buf, w_out, buf_out, lr, momentum, weight_decay, scale, eps, nesterov != 0,
                    steps, a, b, c};
   return run_muon(m, dtype, workspace, workspace_bytes, stream);
+}
+
+size_t sherry_distill_workspace_bytes(int64_t rows, int64_t vocab, int32_t dtype) {
+  if (rows < 1 || rows > kMaxRows || vocab < 1 || vocab > kMaxVocab || (dtype != SHERRY_F32 && dtype != SHERRY_BF16))
+    return (size_t)-1;
+  return plan_distill(rows, vocab, dtype == SHERRY_BF16, false).workspace_bytes;
+}
+
+int32_t sherry_distill_loss(int64_t rows, int64_t vocab, const void* logits, int64_t row_stride, int32_t dtype,
+                            const void* teacher, int32_t teacher_dtype, const void* ids, int32_t ids_64,
+                            int32_t slots, float temperature, const float* teacher_lse, const void* labels,
+                            int32_t labels_64, float kd_weight, float* loss, float* stats, void* workspace,
+                            size_t workspace_bytes, void* stream) {
+  const int st = check_distill(rows, vocab, logits, row_stride, dtype, ids, ids_64, slots, temperature, labels,
+                               labels_64, kd_weight);
+  if (st != SHERRY_OK) return st;
+  if (teacher_dtype != SHERRY_F32 && teacher_dtype != SHERRY_BF16) return SHERRY_ERR_DTYPE;
+  if (!teacher || !loss) return SHERRY_ERR_NULL;
+  if (!multiple_of(teacher, teacher_dtype == SHERRY_F32 ? 4 : 2) || !multiple_of(teacher_lse, 4) ||
+      !multiple_of(loss, 4) || !multiple_of(stats, 4))
+    return SHERRY_ERR_ALIGN;
+  const bool bf16 = dtype == SHERRY_BF16;
+  const DistillSplit plan = plan_distill(rows, vocab, bf16, false);
+  if (!workspace || workspace_bytes < plan.workspace_bytes) return SHERRY_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return SHERRY_ERR_ALIGN;
+  DistillArgs a{logits, row_stride, vocab, teacher, ids, labels, ids_64 != 0, labels_64 != 0, slots, teacher_lse,
+                1.0 / (double)temperature, 0.f, 0.f, kd_weight, plan.ranges, plan.range_groups,
+                static_cast<DistillRange*>(workspace), loss, stats};
+  exp_terms(temperature, &a.exp_hi, &a.exp_lo);
+  return hip_status(launch_distill(a, rows, bf16, teacher_dtype == SHERRY_BF16, static_cast<hipStream_t>(stream)));
+}
+
+int32_t sherry_distill_loss_backward(int64_t rows, int64_t vocab, const float* g, const void* logits,
+                                     int64_t row_stride, int32_t dtype, const void* ids, int32_t ids_64,
+                                     int32_t slots, float temperature, const void* labels, int32_t labels_64,
+                                     float kd_weight, const float* stats, void* dlogits, int64_t dlogits_stride,
+                                     void* stream) {
+  const int st = check_distill(rows, vocab, logits, row_stride, dtype, ids, ids_64, slots, temperature, labels,
+                               labels_64, kd_weight);
+  if (st != SHERRY_OK) return st;
+  if (dlogits_stride < vocab || dlogits_stride > ((int64_t)1 << 60) / rows) return SHERRY_ERR_ARG;
+  if (!g || !stats || !dlogits) return SHERRY_ERR_NULL;
+  if (!multiple_of(g, 4) || !multiple_of(stats, 4) || !multiple_of(dlogits, dtype == SHERRY_F32 ? 4 : 2))
+    return SHERRY_ERR_ALIGN;
+  // the gradient takes the logits' own place or one apart from them
+  const uintptr_t item = dtype == SHERRY_F32 ? 4 : 2, x = reinterpret_cast<uintptr_t>(logits),
+                  y = reinterpret_cast<uintptr_t>(dlogits);
+  const uintptr_t xe = x + ((uintptr_t)(rows - 1) * row_stride + vocab) * item,
+                  ye = y + ((uintptr_t)(rows - 1) * dlogits_stride + vocab) * item;
+  if (x < ye && y < xe && !(x == y && (row_stride == dlogits_stride || rows == 1))) return SHERRY_ERR_ARG;
+  const DistillSplit plan = plan_distill(rows, vocab, dtype == SHERRY_BF16, true);
+  DistillGrad a{g, logits, row_stride, vocab, ids, labels, ids_64 != 0, labels_64 != 0, slots, stats,
+                1.0 / (double)temperature, 0.f, 0.f, kd_weight, plan.ranges, plan.range_groups, dlogits,
+                dlogits_stride};
+  exp_terms(temperature, &a.exp_hi, &a.exp_lo);
+  return hip_status(launch_distill_backward(a, rows, dtype == SHERRY_BF16, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

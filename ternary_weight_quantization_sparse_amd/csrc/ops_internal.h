@@ -1,5 +1,6 @@
 // Internal declarations of the operators around the packed layer
-// (include/sherry_ops.h): block norms, adapters, orthogonalised updates.
+// (include/sherry_ops.h): block norms, adapters, orthogonalised updates,
+// distillation.
 #pragma once
 
 #include "../../include/sherry_ops.h"
@@ -167,5 +168,51 @@ MuonRange muon_range(double a, double b, double c, int steps);
 // loose: steps may be taken in groups (see muon.hip).
 MuonPlan plan_muon(int matrices, int64_t n, int64_t k, bool loose);
 hipError_t launch_muon(const MuonPlan& p, const MuonArgs& a, bool bf16, char* ws, hipStream_t s);
+
+// ---------------------------------------------------------------- distillation
+constexpr int kDistillSlots = 1024;   // teacher slots a row
+struct DistillRange {
+  double s, s1;      // sums of exp((s - m) / t) and exp(s - m)
+  float m;
+  int twice;         // an id stands in two slots
+};
+struct DistillSplit {
+  int ranges;                // workgroups of a row
+  int64_t range_groups;      // 16-byte groups of each
+  size_t workspace_bytes;
+};
+struct DistillArgs {
+  const void* logits;
+  int64_t stride, vocab;
+  const void *teacher, *ids, *labels;
+  bool ids_wide, labels_wide;     // int64 indexes
+  int slots;
+  const float* teacher_lse;
+  double inv_t;                   // 1 / temperature
+  float exp_hi, exp_lo;           // log2(e) / temperature
+  float kd_weight;
+  int ranges;
+  int64_t range_groups;
+  DistillRange* part;
+  float *loss, *stats;
+};
+struct DistillGrad {
+  const float* g;
+  const void* logits;
+  int64_t stride, vocab;
+  const void *ids, *labels;
+  bool ids_wide, labels_wide;
+  int slots;
+  const float* stats;
+  double inv_t;
+  float exp_hi, exp_lo, kd_weight;
+  int ranges;
+  int64_t range_groups;
+  void* out;
+  int64_t out_stride;
+};
+DistillSplit plan_distill(int64_t rows, int64_t vocab, bool bf16, bool backward);
+hipError_t launch_distill(const DistillArgs& a, int64_t rows, bool bf16, bool teacher_bf16, hipStream_t s);
+hipError_t launch_distill_backward(const DistillGrad& a, int64_t rows, bool bf16, hipStream_t s);
 
 }  // namespace sherry
