@@ -2,8 +2,9 @@
  * sherry_ops.h -- operators around the packed ternary layer of libsherry:
  * adapters of many requests beside a packed projection, the norms before and
  * after a block with its gate and residual scale, the orthogonalised
- * (Newton-Schulz) update of latent weights, and the distillation of a student
- * from a teacher's top logits.
+ * (Newton-Schulz) update of latent weights, the distillation of a student
+ * from a teacher's top logits, the packed product with bias, activation and
+ * residual, and a mixture-of-experts layer of packed experts for a few tokens.
  *
  * Conventions are those of sherry.h (streams as void*, caller-provided
  * workspaces, host-side argument checks before any launch, no allocation, no
@@ -175,6 +176,73 @@ int32_t sherry_distill_loss_backward(int64_t rows, int64_t vocab, const float* g
                                      int32_t slots, float temperature, const void* labels, int32_t labels_64,
                                      float kd_weight, const float* stats, void* dlogits, int64_t dlogits_stride,
                                      void* stream);
+
+typedef enum {
+  SHERRY_ACT_NONE = 0,
+  SHERRY_ACT_RELU = 1,
+  SHERRY_ACT_RELU2 = 2,     /* max(z, 0)^2 */
+  SHERRY_ACT_SILU = 3,
+  SHERRY_ACT_GELU = 4,      /* z Phi(z) */
+  SHERRY_ACT_GELU_TANH = 5  /* its tanh form */
+} sherry_activation;
+
+/*
+ * sherry_linear_gemv / sherry_linear_gemm -- the packed product of 1..16 tokens (one launch, no workspace) or of m
+ * tokens (MFMA), with what follows it before its one rounding:
+ *
+ *   z[m, n] = sum_k x[m, k] T[n, k] alpha(n, k) + bias[n]
+ *   y = f(z) + res_scale * residual;   gated: y[m, j] = f(z[m, j]) z[m, N/2 + j] + res_scale * residual[m, j]
+ *
+ *   The packed operand and x as for sherry_gemv.  gated: N is even, rows [gate; values] packed as one weight.
+ *   y        [tokens, N or N/2], bf16; gemv also SHERRY_F32.
+ *   bias     [N], bias_dtype SHERRY_F32 or SHERRY_BF16, or NULL.
+ *   residual [tokens, N or N/2] bf16 or NULL (res_scale 1).  y (bf16) may be residual; outputs that overlap it
+ *            otherwise, or x, return SHERRY_ERR_ARG.
+ *   bias, and gemv's residual and y, need their element's alignment, gemm's residual 8-byte, the rest 16-byte.
+ *   gemm's workspace is that of sherry_gemm: sherry_workspace_bytes(SHERRY_OP_GEMM, n, k, .., m, 1).
+ */
+int32_t sherry_linear_gemv(int64_t n, int64_t k, int32_t granularity, int32_t group_size, const void* packed,
+                           const float* alpha, const void* x, int32_t batch, void* y, int32_t y_dtype,
+                           const void* bias, int32_t bias_dtype, int32_t activation, int32_t gated,
+                           const void* residual, float res_scale, void* stream);
+int32_t sherry_linear_gemm(int64_t n, int64_t k, int32_t granularity, int32_t group_size, const void* packed,
+                           const float* alpha, const void* x, int64_t m, void* y, const void* bias,
+                           int32_t bias_dtype, int32_t activation, int32_t gated, const void* residual,
+                           float res_scale, void* workspace, size_t workspace_bytes, void* stream);
+
+typedef enum { SHERRY_SCORE_SOFTMAX = 0, SHERRY_SCORE_SIGMOID = 1 } sherry_scoring;
+
+/* Workspace bytes of sherry_moe_decode; (size_t)-1 on invalid arguments. */
+size_t sherry_moe_workspace_bytes(int32_t tokens, int64_t dim, int64_t hidden, int32_t experts, int32_t shared,
+                                  int32_t top_k);
+
+/*
+ * sherry_moe_decode -- a whole mixture-of-experts layer of packed experts for 1..16 tokens x [tokens, dim]:
+ *
+ *   l = x router^T;  s = softmax(l) over the experts, or sigmoid(l)
+ *   the top_k largest of s, or of s + bias (the lowest index of equal ones);  w = s (normalize: / their sum) * scale
+ *   y = sum_j w_j down_j h_j + sum of the shared experts' down h + residual
+ *   h = f(up x), or with gated f(gate x) * (up x), rows [gate; up] packed as one weight
+ *
+ *   x        bf16; router [experts, dim], router_dtype SHERRY_F32 or SHERRY_BF16; bias [experts] fp32 or NULL.
+ *   An expert whose key is -infinity (a bias of -infinity) is off: a token with fewer than top_k others meets only
+ *   those, with none only the shared experts.  Equal logits count as equal scores.
+ *   up       [experts + shared] packed weights [hidden (gated: 2 hidden), dim], one after another, and their scales
+ *            [experts + shared][sherry_num_scales]; the shared experts, which every token meets with the weight 1,
+ *            are the last.  down the same for [dim, hidden].
+ *   residual [tokens, dim] bf16 or NULL; y [tokens, dim] SHERRY_BF16 or SHERRY_F32; y may be residual (bf16) or x.
+ *   h is kept as two bf16 terms (2^-17 of it); sums are fp32 in an order fixed by the sizes and the choices.
+ *   dim, hidden multiples of 128, at most 65536; experts 1 .. 512, top_k 1 .. min(16, experts), shared 0 .. 4.
+ *   No token's values reach another's result, but the order of its sums follows the experts that the batch uses.
+ *   No host synchronisation; capturable.
+ */
+int32_t sherry_moe_decode(int32_t tokens, int64_t dim, int64_t hidden, const void* x, const void* router,
+                          int32_t router_dtype, int32_t experts, int32_t shared, int32_t top_k, int32_t scoring,
+                          int32_t normalize, const float* bias, float scale, int32_t activation, int32_t gated,
+                          const void* up, const float* up_alpha, int32_t up_granularity, int32_t up_group,
+                          const void* down, const float* down_alpha, int32_t down_granularity, int32_t down_group,
+                          const void* residual, void* y, int32_t y_dtype, void* workspace, size_t workspace_bytes,
+                          void* stream);
 
 #ifdef __cplusplus
 }

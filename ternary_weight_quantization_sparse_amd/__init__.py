@@ -25,6 +25,7 @@ __all__ = [
     "compare_repack", "compare_gemv", "gemm_fused", "quantize_pack_noalloc",
     "AdapterSet", "adapter_gemv", "adapter_gemm", "block_norm", "block_norm_backward", "block_norm_ad",
     "orthogonalize", "muon_step", "NEWTON_SCHULZ", "distill_loss", "distill_loss_backward", "distill_loss_ad",
+    "linear_gemv", "linear_gemm", "PackedExperts", "quantize_pack_experts", "moe_decode",
 ]
 
 
@@ -499,5 +500,7 @@ def gemm(pw: PackedWeight, x, stream=None, out=None):
 
 from .adapters import AdapterSet, adapter_gemm, adapter_gemv  # noqa: E402
 from .distill import distill_loss, distill_loss_ad, distill_loss_backward  # noqa: E402
+from .experts import PackedExperts, moe_decode, quantize_pack_experts  # noqa: E402
+from .linear import linear_gemm, linear_gemv  # noqa: E402
 from .muon import NEWTON_SCHULZ, muon_step, orthogonalize  # noqa: E402
 from .norms import block_norm, block_norm_ad, block_norm_backward  # noqa: E402

@@ -24,6 +24,8 @@ CMP_2BIT, CMP_TL2 = 0, 1
 F32, BF16, I8 = 0, 1, 2
 OP_QUANTIZE_PACK, OP_UNPACK, OP_GEMV, OP_GEMM, OP_FAKE_QUANT, OP_ARENAS_GEMM = 0, 1, 2, 3, 4, 5
 ERR_ARG = 11
+ACTIVATIONS = {"none": 0, "relu": 1, "relu2": 2, "silu": 3, "gelu": 4, "gelu_tanh": 5}
+SCORING = {"softmax": 0, "sigmoid": 1}
 GATE_NONE, GATE_TOKEN, GATE_CHANNEL, GATE_ROWS = 0, 1, 2, 3
 QUANTIZE_SCRATCH_BYTES = 8 << 20   # SHERRY_QUANTIZE_SCRATCH_BYTES
 
@@ -41,6 +43,7 @@ OPS_SYMBOLS = (
     "sherry_adapter_workspace_bytes", "sherry_adapter_gemv", "sherry_adapter_gemm",
     "sherry_muon_workspace_bytes", "sherry_orthogonalize", "sherry_muon_step",
     "sherry_distill_workspace_bytes", "sherry_distill_loss", "sherry_distill_loss_backward",
+    "sherry_linear_gemv", "sherry_linear_gemm", "sherry_moe_workspace_bytes", "sherry_moe_decode",
 )
 
 _i32, _i64, _sz, _vp = ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t, ctypes.c_void_p
@@ -85,6 +88,13 @@ _SIGNATURES = {
                              _vp, _vp, _sz, _vp], _i32),
     "sherry_distill_loss_backward": ([_i64, _i64, _vp, _vp, _i64, _i32, _vp, _i32, _i32, _f32, _vp, _i32, _f32, _vp,
                                       _vp, _i64, _vp], _i32),
+    "sherry_linear_gemv": ([_i64, _i64, _i32, _i32, _vp, _vp, _vp, _i32, _vp, _i32, _vp, _i32, _i32, _i32, _vp, _f32,
+                            _vp], _i32),
+    "sherry_linear_gemm": ([_i64, _i64, _i32, _i32, _vp, _vp, _vp, _i64, _vp, _vp, _i32, _i32, _i32, _vp, _f32, _vp,
+                            _sz, _vp], _i32),
+    "sherry_moe_workspace_bytes": ([_i32, _i64, _i64, _i32, _i32, _i32], _sz),
+    "sherry_moe_decode": ([_i32, _i64, _i64, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _i32, _vp, _f32, _i32, _i32, _vp,
+                           _vp, _i32, _i32, _vp, _vp, _i32, _i32, _vp, _vp, _i32, _vp, _sz, _vp], _i32),
 }
 
 _lib = None

@@ -21,7 +21,7 @@ LIB_PATH = os.path.join(PKG_DIR, LIB_NAME)
 
 ARCH = "gfx950"
 SOURCES = ["sherry_api.cpp", "quantize_pack.hip", "unpack.hip", "gemv.hip", "gemm.hip", "compare.hip",
-           "ops_api.cpp", "norm.hip", "adapter.hip", "muon.hip", "distill.hip"]
+           "ops_api.cpp", "norm.hip", "adapter.hip", "muon.hip", "distill.hip", "decode.hip"]
 
 COMMON = [
     f"--offload-arch={ARCH}", "-O3", "-fPIC", "-std=c++17", "-Wall",
@@ -31,10 +31,10 @@ COMMON = [
     "-I", os.path.join(ROOT, "include"),
 ]
 # the scale sums must be plain fp32 adds in a fixed order
-# gemv.hip: MFMA accumulators in VGPRs, so the per-group scale FMAs read them
+# gemv.hip, decode.hip: MFMA accumulators in VGPRs, so the per-group scale FMAs read them
 # without a copy out of the accumulation registers first
 PER_SOURCE = {"quantize_pack.hip": ["-ffp-contract=off"],
-              "gemv.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
+              "gemv.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"], "decode.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
 
 
 def hipcc() -> str:

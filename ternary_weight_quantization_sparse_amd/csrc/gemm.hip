@@ -45,10 +45,15 @@
 // the B operand, added to the tokens of that adapter only.  The fp32 a x go in as
 // three bf16 terms, which together are the fp32 value (24 bits): two would lose
 // 2^-18 of the low-rank sum, which shows where y is much smaller than it.
+//
+// Epilogue (EP): bias, activation and residual on the fp32 accumulators before
+// their one rounding.  GATED: a wave's tiles are half gate rows and half the
+// same outputs' rows of the other half of the weight, so a lane holds both
+// factors of its outputs and y is written once, at half the width.
 #include <cmath>
 #include <type_traits>
 
-#include "ops_internal.h"
+#include "epilogue.h"
 
 namespace sherry {
 namespace {
@@ -121,10 +126,102 @@ struct GemmCfg {
 template <int J>
 using Slot = std::integral_constant<int, J>;
 
+// Bias, activation and residual of four consecutive outputs of a row, sums z
+// (and u, the other factors) scaled already.
+template <bool GATED>
+__device__ inline void finish_outputs(const LinearArgs& a, float (&z)[4], float (&u)[4], int64_t row, int64_t col,
+                                      int64_t outs, bool full4, uint16_t* __restrict__ y) {
+  uint16_t res[4] = {0, 0, 0, 0};
+  const int64_t at = row * outs + col;
+  if (a.residual) {
+    if (full4) {
+      const uint2 v = *reinterpret_cast<const uint2*>(a.residual + at);
+      res[0] = (uint16_t)v.x; res[1] = (uint16_t)(v.x >> 16); res[2] = (uint16_t)v.y; res[3] = (uint16_t)(v.y >> 16);
+    } else {
+      for (int e = 0; e < 4; ++e)
+        if (col + e < outs) res[e] = a.residual[at + e];
+    }
+  }
+  uint16_t h[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const int64_t c = min(col + e, outs - 1);
+    float v = z[e];
+    if (a.bias) v += load_float(a.bias, c, a.bias_bf16);
+    v = activate(v, a.activation);
+    if constexpr (GATED) v *= a.bias ? u[e] + load_float(a.bias, outs + c, a.bias_bf16) : u[e];
+    if (a.residual) v += a.res_scale * bf16_to_f32(res[e]);
+    h[e] = __builtin_bit_cast(uint16_t, (__bf16)v);
+  }
+  if (full4) {
+    *reinterpret_cast<uint2*>(y + at) = make_uint2(h[0] | ((uint32_t)h[1] << 16), h[2] | ((uint32_t)h[3] << 16));
+  } else {
+    for (int e = 0; e < 4; ++e)
+      if (col + e < outs) y[at + e] = h[e];
+  }
+}
+
+// The accumulators of a wave: to fp32 partials (a split of K: unscaled where
+// scales are a row's or the weight's), or to y.
+template <int GRAN, bool GATED, int TN, int TM>
+__device__ inline void linear_epilogue(const f32x4 (&acc)[TN][TM], const float* __restrict__ alpha, float* partial,
+                                       uint16_t* __restrict__ y, int64_t n, int64_t m, int64_t m0, int64_t col0, int r,
+                                       int q, int kz, const LinearArgs& a) {
+  constexpr int kOut = GATED ? TN / 2 : TN;
+  const int64_t outs = GATED ? n / 2 : n;
+  auto scale = [&](int64_t row) {
+    return GRAN == SHERRY_PER_CHANNEL ? alpha[row] : GRAN == SHERRY_PER_TENSOR ? alpha[0] : 1.f;
+  };
+#pragma unroll
+  for (int i = 0; i < kOut; ++i) {
+    const int64_t col = col0 + i * 16 + 4 * q;
+    if (col >= outs) continue;
+    const bool full4 = col + 3 < outs && (outs & 3) == 0;
+    float sz[4], su[4];
+    if (partial == nullptr) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int64_t c = min(col + e, outs - 1);
+        sz[e] = scale(c);
+        su[e] = GATED ? scale(outs + c) : 1.f;
+      }
+    }
+#pragma unroll
+    for (int jj = 0; jj < TM; ++jj) {
+      const int64_t gm = m0 + jj * 16 + r;
+      if (gm >= m) continue;
+      if (partial != nullptr) {
+        float* dst = partial + ((int64_t)kz * m + gm) * n + col;
+        if (full4) {   // (then outs is a multiple of 4, and so is the other half's place)
+          *reinterpret_cast<f32x4*>(dst) = acc[i][jj];
+          if constexpr (GATED) *reinterpret_cast<f32x4*>(dst + outs) = acc[i + (GATED ? kOut : 0)][jj];
+        } else {
+          for (int e = 0; e < 4; ++e)
+            if (col + e < outs) {
+              dst[e] = acc[i][jj][e];
+              if constexpr (GATED) dst[outs + e] = acc[i + (GATED ? kOut : 0)][jj][e];
+            }
+        }
+        continue;
+      }
+      float z[4], u[4] = {1.f, 1.f, 1.f, 1.f};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        z[e] = GRAN == SHERRY_PER_GROUP ? acc[i][jj][e] : acc[i][jj][e] * sz[e];
+        if constexpr (GATED) {
+          const float v = acc[i + (GATED ? kOut : 0)][jj][e];
+          u[e] = GRAN == SHERRY_PER_GROUP ? v : v * su[e];
+        }
+      }
+      finish_outputs<GATED>(a, z, u, gm, col, outs, full4, y);
+    }
+  }
+}
+
 // grid: x = tiles (tiles_m * tiles_n), y = K splits.  partial == nullptr:
 // write bf16 Y; else write fp32 partial[split][m][n] (per_group already
 // scaled, per_channel / per_tensor not yet; AR: fully scaled).
-template <int GRAN, int TM, bool AR, int TN, bool MERGE, bool AD>
+template <int GRAN, int TM, bool AR, int TN, bool MERGE, bool AD, bool GATED = false, typename... EP>
 __global__ __launch_bounds__(kThreads, AR ? (GRAN != SHERRY_PER_GROUP || MERGE ? 2 : 1) : (TN == 4 ? 2 : 3)) void gemm_kernel(const uint8_t* packed,
                                                      const float* __restrict__ alpha,
                                                      const uint16_t* __restrict__ x,
@@ -132,7 +229,7 @@ __global__ __launch_bounds__(kThreads, AR ? (GRAN != SHERRY_PER_GROUP || MERGE ?
                                                      int64_t n, int64_t k, int64_t m, int group_sbs,
                                                      int tiles_m, int tiles_n, int sb_per_split,
                                                      const uint16_t* __restrict__ wd, float lam,
-                                                     AdapterTerm ad) {
+                                                     AdapterTerm ad, EP... ep) {
   using C = GemmCfg<GRAN, TM, AR, TN, MERGE>;
   static_assert(!MERGE || (AR && GRAN == SHERRY_PER_GROUP), "MERGE is the per_group Arenas variant");
   constexpr int kTM = C::kTM, kBM = C::kBM, kXLoads = C::kXLoads, kRecWave = C::kRecWave;
@@ -181,7 +278,7 @@ __global__ __launch_bounds__(kThreads, AR ? (GRAN != SHERRY_PER_GROUP || MERGE ?
     tn = bid % tiles_n;
   }
   const int64_t m0 = (int64_t)tm * kBM;
-  const int64_t n0 = (int64_t)tn * kBN;
+  const int64_t n0 = (int64_t)tn * (GATED ? kBN / 2 : kBN);   // of the outputs
   const int kz = blockIdx.y;
   const int64_t sb0 = (int64_t)kz * sb_per_split;  // first superblock of this split
   const int stages = sb_per_split;
@@ -211,8 +308,15 @@ __global__ __launch_bounds__(kThreads, AR ? (GRAN != SHERRY_PER_GROUP || MERGE ?
 
   // weight row whose records this lane copies: n0 + kWN wave + lane % kWN
   // (clamped rows feed only outputs that are not stored)
-  int64_t crow = n0 + wave * kWN + (lane % kWN);
-  crow = crow < n ? crow : n - 1;
+  int64_t crow;
+  if constexpr (GATED) {
+    constexpr int kHalf = kWN / 2;
+    const int64_t outs = n / 2, col = n0 + wave * kHalf + lane % kHalf;
+    crow = (lane % kWN < kHalf ? 0 : outs) + (col < outs ? col : outs - 1);
+  } else {
+    crow = n0 + wave * kWN + (lane % kWN);
+    crow = crow < n ? crow : n - 1;
+  }
 
   u32x4 wreg[C::kWReg ? 2 : 1][C::kWReg ? kTN : 1][4];  // dense-weight operands, one stage per slot
   auto issue = [&](auto J, int st) {
@@ -564,6 +668,13 @@ __global__ __launch_bounds__(kThreads, AR ? (GRAN != SHERRY_PER_GROUP || MERGE ?
     }
   }
 
+  if constexpr (sizeof...(EP) > 0) {
+    (linear_epilogue<GRAN, GATED, kTN, kTM>(acc, alpha, partial, y, n, m, m0, n0 + wave * (GATED ? kWN / 2 : kWN), r, q,
+                                            kz, ep),
+     ...);
+    return;
+  }
+
   // epilogue: lane holds Y[m0 + 16jj + r][n0 + 32 wave + 16i + 4q + e]
 #pragma unroll
   for (int i = 0; i < kTN; ++i) {
@@ -658,6 +769,57 @@ __global__ __launch_bounds__(256) void gemm_split_reduce(const float* __restrict
   }
 }
 
+// The same with the epilogue: four outputs of a row a thread.
+template <int GRAN, bool GATED>
+__global__ __launch_bounds__(256) void linear_split_finish(const float* __restrict__ partial,
+                                                           const float* __restrict__ alpha, uint16_t* __restrict__ y,
+                                                           int64_t m, int64_t n, int splits, LinearArgs a) {
+  const int64_t outs = GATED ? n / 2 : n, quads = (outs + 3) / 4;
+  const int64_t idx = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+  if (idx >= m * quads) return;
+  const int64_t row = idx / quads, col = idx % quads * 4;
+  const bool full4 = (outs & 3) == 0;
+  float z[4] = {0.f, 0.f, 0.f, 0.f}, u[4] = {0.f, 0.f, 0.f, 0.f};
+  const float* p = partial + row * n + col;
+  if (full4) {
+    f32x4 v[8], w[GATED ? 8 : 1];
+#pragma unroll
+    for (int s = 0; s < 8; ++s)
+      if (s < splits) {
+        v[s] = *reinterpret_cast<const f32x4*>(p + s * m * n);
+        if constexpr (GATED) w[s] = *reinterpret_cast<const f32x4*>(p + s * m * n + outs);
+      }
+#pragma unroll
+    for (int s = 0; s < 8; ++s)
+      if (s < splits)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          z[e] += v[s][e];
+          if constexpr (GATED) u[e] += w[s][e];
+        }
+  } else {
+    for (int s = 0; s < splits; ++s)
+      for (int e = 0; e < 4; ++e)
+        if (col + e < outs) {
+          z[e] += p[s * m * n + e];
+          if constexpr (GATED) u[e] += p[s * m * n + outs + e];
+        }
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const int64_t c = min(col + e, outs - 1);
+    if constexpr (GRAN == SHERRY_PER_CHANNEL) {
+      z[e] *= alpha[c];
+      if constexpr (GATED) u[e] *= alpha[outs + c];
+    }
+    if constexpr (GRAN == SHERRY_PER_TENSOR) {
+      z[e] *= alpha[0];
+      if constexpr (GATED) u[e] *= alpha[0];
+    }
+  }
+  finish_outputs<GATED>(a, z, u, row, col, outs, full4, y);
+}
+
 // Rows of X per launch: buffer offsets, including the tail tile's rows past
 // the end, stay below 2^31 bytes.
 int64_t gemm_chunk_rows(int64_t k) { return ((((int64_t)1 << 31) / (2 * k) - kMaxBM) / kMaxBM) * kMaxBM; }
@@ -695,6 +857,37 @@ hipError_t launch_g(const GemmPlan& p, int64_t n, int64_t k, int group_sbs, cons
       e = hipGetLastError();
       if (e != hipSuccess) return e;
     }
+  }
+  return hipSuccess;
+}
+
+template <int GRAN, int TN, bool GATED>
+hipError_t launch_linear(const GemmPlan& p, LinearArgs a, const uint16_t* x, int64_t m, uint16_t* y, float* ws,
+                         hipStream_t s) {
+  using C = GemmCfg<GRAN, kGemmTM, false, TN, false>;
+  const int64_t n = a.n, k = a.k, outs = GATED ? n / 2 : n, chunk = gemm_chunk_rows(k);
+  constexpr int kWide = GATED ? C::kBN / 2 : C::kBN;   // outputs of a tile
+  if (chunk < kMaxBM || p.splits < 1 || p.splits > 8) return hipErrorInvalidValue;
+  const int tiles_n = (int)((outs + kWide - 1) / kWide);
+  const int sb_per_split = (int)(k / kSuperblock / p.splits);
+  for (int64_t r0 = 0; r0 < m; r0 += chunk) {
+    const int64_t mc = m - r0 < chunk ? m - r0 : chunk;
+    const int tiles_m = (int)((mc + C::kBM - 1) / C::kBM);
+    uint16_t* yc = y + r0 * outs;
+    hipLaunchKernelGGL((gemm_kernel<GRAN, kGemmTM, false, TN, false, false, GATED, LinearArgs>),
+                       dim3((unsigned)(tiles_m * tiles_n), (unsigned)p.splits), dim3(kThreads), 0, s, a.packed, a.alpha,
+                       x + r0 * k, yc, p.splits > 1 ? ws : nullptr, n, k, mc, a.group_sbs ? a.group_sbs : 1, tiles_m,
+                       tiles_n, sb_per_split, nullptr, 0.f, AdapterTerm{}, a);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    if (p.splits > 1) {
+      const int64_t threads = mc * ((outs + 3) / 4);
+      hipLaunchKernelGGL((linear_split_finish<GRAN, GATED>), dim3((unsigned)((threads + 255) / 256)), dim3(256), 0, s, ws,
+                         a.alpha, yc, mc, n, p.splits, a);
+      e = hipGetLastError();
+      if (e != hipSuccess) return e;
+    }
+    if (a.residual) a.residual += mc * outs;
   }
   return hipSuccess;
 }
@@ -765,6 +958,24 @@ hipError_t launch_gemm_adapted(const GemmPlan& p, int64_t n, int64_t k, int gran
   }
   if (gran == SHERRY_PER_GROUP) SHERRY_GEMM_LAUNCH(SHERRY_PER_GROUP, 2);
   if (gran == SHERRY_PER_CHANNEL) SHERRY_GEMM_LAUNCH(SHERRY_PER_CHANNEL, 2);
+  SHERRY_GEMM_LAUNCH(SHERRY_PER_TENSOR, 2);
+#undef SHERRY_GEMM_LAUNCH
+}
+
+hipError_t launch_linear_gemm(const GemmPlan& p, const LinearArgs& a, const uint16_t* x, int64_t m, uint16_t* y,
+                              float* ws, hipStream_t s) {
+#define SHERRY_GEMM_LAUNCH(G, TN)                                   \
+  do {                                                              \
+    if (a.gated) return launch_linear<G, TN, true>(p, a, x, m, y, ws, s); \
+    return launch_linear<G, TN, false>(p, a, x, m, y, ws, s);       \
+  } while (0)
+  if (p.tile_n == 256) {
+    if (a.gran == SHERRY_PER_GROUP) SHERRY_GEMM_LAUNCH(SHERRY_PER_GROUP, 4);
+    if (a.gran == SHERRY_PER_CHANNEL) SHERRY_GEMM_LAUNCH(SHERRY_PER_CHANNEL, 4);
+    SHERRY_GEMM_LAUNCH(SHERRY_PER_TENSOR, 4);
+  }
+  if (a.gran == SHERRY_PER_GROUP) SHERRY_GEMM_LAUNCH(SHERRY_PER_GROUP, 2);
+  if (a.gran == SHERRY_PER_CHANNEL) SHERRY_GEMM_LAUNCH(SHERRY_PER_CHANNEL, 2);
   SHERRY_GEMM_LAUNCH(SHERRY_PER_TENSOR, 2);
 #undef SHERRY_GEMM_LAUNCH
 }

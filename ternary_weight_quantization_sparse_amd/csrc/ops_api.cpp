@@ -116,6 +116,45 @@ int check_distill(int64_t rows, int64_t vocab, const void* logits, int64_t strid
   return SHERRY_OK;
 }
 
+// Whether two ranges of memory share a byte.
+bool overlap(const void* a, size_t a_bytes, const void* b, size_t b_bytes) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a && b && x < y + b_bytes && y < x + a_bytes;
+}
+
+// The product's operands and epilogue, but for the number of tokens.
+int check_linear(int64_t n, int64_t k, int32_t gran, int32_t group_size, const void* packed, const float* alpha,
+                 const void* x, int64_t tokens, const void* y, int32_t y_dtype, const void* bias, int32_t bias_dtype,
+                 int32_t activation, int32_t gated, const void* residual, float res_scale) {
+  if (activation < SHERRY_ACT_NONE || activation > SHERRY_ACT_GELU_TANH || (gated && n % 2 != 0)) return SHERRY_ERR_ARG;
+  if (!std::isfinite(res_scale) || (!residual && res_scale != 1.0f)) return SHERRY_ERR_ARG;
+  if (y_dtype != SHERRY_BF16 && y_dtype != SHERRY_F32) return SHERRY_ERR_DTYPE;
+  if (bias_dtype != SHERRY_F32 && bias_dtype != SHERRY_BF16) return SHERRY_ERR_DTYPE;
+  if (!packed || !alpha || !x || !y) return SHERRY_ERR_NULL;
+  const uintptr_t item = y_dtype == SHERRY_F32 ? 4 : 2;
+  if (!aligned16(packed) || !aligned16(alpha) || !aligned16(x) || !multiple_of(y, item) || !multiple_of(residual, 2) ||
+      !multiple_of(bias, bias_dtype == SHERRY_F32 ? 4 : 2))
+    return SHERRY_ERR_ALIGN;
+  const size_t outs = (size_t)tokens * (size_t)(gated ? n / 2 : n);
+  if (overlap(y, outs * item, x, (size_t)tokens * (size_t)k * 2)) return SHERRY_ERR_ARG;
+  if (overlap(y, outs * item, residual, outs * 2) && !(y == residual && item == 2)) return SHERRY_ERR_ARG;
+  return SHERRY_OK;
+}
+
+int group_sbs_of(int32_t gran, int32_t group_size) { return gran == SHERRY_PER_GROUP ? group_size / 128 : 0; }
+
+constexpr int64_t kMoeMaxSide = 65536;
+
+int check_moe_sizes(int32_t tokens, int64_t dim, int64_t hidden, int32_t experts, int32_t shared, int32_t top_k) {
+  if (tokens < 1 || tokens > 16) return SHERRY_ERR_BATCH;
+  if (dim < 128 || hidden < 128 || dim % 128 != 0 || hidden % 128 != 0 || dim > kMoeMaxSide || hidden > kMoeMaxSide)
+    return SHERRY_ERR_ARG;
+  if (experts < 1 || experts > kMoeExperts || shared < 0 || shared > kMoeShared || top_k < 1 || top_k > kMoeTopK ||
+      top_k > experts)
+    return SHERRY_ERR_ARG;
+  return SHERRY_OK;
+}
+
 // log2(e) / t as two fp32 terms, both above zero: a distance of -infinity stays one
 void exp_terms(float temperature, float* hi, float* lo) {
   const double c = 1.4426950408889634 / (double)temperature;
@@ -313,6 +352,93 @@ int32_t sherry_distill_loss_backward(int64_t rows, int64_t vocab, const float* g
                 dlogits_stride};
   exp_terms(temperature, &a.exp_hi, &a.exp_lo);
   return hip_status(launch_distill_backward(a, rows, dtype == SHERRY_BF16, static_cast<hipStream_t>(stream)));
+}
+
+int32_t sherry_linear_gemv(int64_t n, int64_t k, int32_t granularity, int32_t group_size, const void* packed,
+                           const float* alpha, const void* x, int32_t batch, void* y, int32_t y_dtype,
+                           const void* bias, int32_t bias_dtype, int32_t activation, int32_t gated,
+                           const void* residual, float res_scale, void* stream) {
+  if (batch < 1 || batch > 16) return SHERRY_ERR_BATCH;
+  // the packed product's own limits
+  if (sherry_workspace_bytes(SHERRY_OP_GEMV, n, k, granularity, group_size, batch, 1) == (size_t)-1)
+    return SHERRY_ERR_SHAPE;
+  const int st = check_linear(n, k, granularity, group_size, packed, alpha, x, batch, y, y_dtype, bias, bias_dtype,
+                              activation, gated, residual, res_scale);
+  if (st != SHERRY_OK) return st;
+  const LinearArgs a{static_cast<const uint8_t*>(packed), alpha, n, k, granularity, group_sbs_of(granularity, group_size),
+                     bias, bias_dtype == SHERRY_BF16, activation, gated != 0, static_cast<const uint16_t*>(residual),
+                     res_scale};
+  return hip_status(launch_linear_decode(a, static_cast<const uint16_t*>(x), batch, y, y_dtype == SHERRY_BF16,
+                                         static_cast<hipStream_t>(stream)));
+}
+
+int32_t sherry_linear_gemm(int64_t n, int64_t k, int32_t granularity, int32_t group_size, const void* packed,
+                           const float* alpha, const void* x, int64_t m, void* y, const void* bias, int32_t bias_dtype,
+                           int32_t activation, int32_t gated, const void* residual, float res_scale, void* workspace,
+                           size_t workspace_bytes, void* stream) {
+  if (m < 1 || (m + 127) / 128 > 65535) return SHERRY_ERR_BATCH;
+  // the packed product's own limits
+  if (sherry_workspace_bytes(SHERRY_OP_GEMM, n, k, granularity, group_size, m, 1) == (size_t)-1) return SHERRY_ERR_SHAPE;
+  if (k > ((int64_t)1 << 21)) return SHERRY_ERR_UNSUPPORTED;   // as sherry_gemm
+  if (m > ((int64_t)1 << 46) / k) return SHERRY_ERR_BATCH;
+  const int st = check_linear(n, k, granularity, group_size, packed, alpha, x, m, y, SHERRY_BF16, bias, bias_dtype,
+                              activation, gated, residual, res_scale);
+  if (st != SHERRY_OK) return st;
+  if (!aligned16(y) || !multiple_of(residual, 8)) return SHERRY_ERR_ALIGN;
+  const GemmPlan plan = plan_gemm(n, k, granularity, group_size, m, true);
+  if (plan.workspace_bytes > 0 && (!workspace || workspace_bytes < plan.workspace_bytes)) return SHERRY_ERR_WORKSPACE;
+  if (plan.workspace_bytes > 0 && !aligned16(workspace)) return SHERRY_ERR_ALIGN;
+  const LinearArgs a{static_cast<const uint8_t*>(packed), alpha, n, k, granularity, group_sbs_of(granularity, group_size),
+                     bias, bias_dtype == SHERRY_BF16, activation, gated != 0, static_cast<const uint16_t*>(residual),
+                     res_scale};
+  return hip_status(launch_linear_gemm(plan, a, static_cast<const uint16_t*>(x), m, static_cast<uint16_t*>(y),
+                                       static_cast<float*>(workspace), static_cast<hipStream_t>(stream)));
+}
+
+size_t sherry_moe_workspace_bytes(int32_t tokens, int64_t dim, int64_t hidden, int32_t experts, int32_t shared,
+                                  int32_t top_k) {
+  if (check_moe_sizes(tokens, dim, hidden, experts, shared, top_k) != SHERRY_OK) return (size_t)-1;
+  return plan_moe(tokens, experts, top_k + shared, hidden).workspace_bytes;
+}
+
+int32_t sherry_moe_decode(int32_t tokens, int64_t dim, int64_t hidden, const void* x, const void* router,
+                          int32_t router_dtype, int32_t experts, int32_t shared, int32_t top_k, int32_t scoring,
+                          int32_t normalize, const float* bias, float scale, int32_t activation, int32_t gated,
+                          const void* up, const float* up_alpha, int32_t up_granularity, int32_t up_group,
+                          const void* down, const float* down_alpha, int32_t down_granularity, int32_t down_group,
+                          const void* residual, void* y, int32_t y_dtype, void* workspace, size_t workspace_bytes,
+                          void* stream) {
+  int st = check_moe_sizes(tokens, dim, hidden, experts, shared, top_k);
+  if (st != SHERRY_OK) return st;
+  if (scoring != SHERRY_SCORE_SOFTMAX && scoring != SHERRY_SCORE_SIGMOID) return SHERRY_ERR_ARG;
+  if (activation < SHERRY_ACT_NONE || activation > SHERRY_ACT_GELU_TANH || !std::isfinite(scale)) return SHERRY_ERR_ARG;
+  const int64_t up_n = gated ? 2 * hidden : hidden;
+  if (sherry_workspace_bytes(SHERRY_OP_GEMV, up_n, dim, up_granularity, up_group, tokens, 1) == (size_t)-1 ||
+      sherry_workspace_bytes(SHERRY_OP_GEMV, dim, hidden, down_granularity, down_group, tokens, 1) == (size_t)-1)
+    return SHERRY_ERR_SHAPE;
+  if ((router_dtype != SHERRY_F32 && router_dtype != SHERRY_BF16) || (y_dtype != SHERRY_F32 && y_dtype != SHERRY_BF16))
+    return SHERRY_ERR_DTYPE;
+  if (!x || !router || !up || !up_alpha || !down || !down_alpha || !y) return SHERRY_ERR_NULL;
+  const uintptr_t item = y_dtype == SHERRY_F32 ? 4 : 2;
+  if (!aligned16(x) || !aligned16(router) || !aligned16(up) || !aligned16(up_alpha) || !aligned16(down) ||
+      !aligned16(down_alpha) || !multiple_of(bias, 4) || !multiple_of(residual, 2) || !multiple_of(y, item))
+    return SHERRY_ERR_ALIGN;
+  const size_t outs = (size_t)tokens * (size_t)dim;
+  if (overlap(y, outs * item, residual, outs * 2) && !(y == residual && item == 2)) return SHERRY_ERR_ARG;
+  const MoePlan p = plan_moe(tokens, experts, top_k + shared, hidden);
+  if (!workspace || workspace_bytes < p.workspace_bytes) return SHERRY_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return SHERRY_ERR_ALIGN;
+  char* ws = static_cast<char*>(workspace);
+  const MoeArgs a{static_cast<const uint16_t*>(x), tokens, experts, top_k, shared, top_k + shared, dim, hidden, router,
+                  router_dtype == SHERRY_BF16, scoring == SHERRY_SCORE_SOFTMAX, normalize != 0, gated != 0, bias, scale,
+                  activation, static_cast<const uint8_t*>(up), static_cast<const uint8_t*>(down), up_alpha, down_alpha,
+                  (int64_t)sherry_packed_bytes(up_n, dim), (int64_t)sherry_packed_bytes(dim, hidden),
+                  sherry_num_scales(up_n, dim, up_granularity, up_group),
+                  sherry_num_scales(dim, hidden, down_granularity, down_group), up_granularity,
+                  group_sbs_of(up_granularity, up_group), down_granularity, group_sbs_of(down_granularity, down_group),
+                  static_cast<const uint16_t*>(residual), reinterpret_cast<float*>(ws),
+                  reinterpret_cast<__bf16*>(ws + p.h_offset), p.h_plane, false, 0};
+  return hip_status(launch_moe(a, y, y_dtype == SHERRY_BF16, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -1,6 +1,6 @@
 // Internal declarations of the operators around the packed layer
 // (include/sherry_ops.h): block norms, adapters, orthogonalised updates,
-// distillation.
+// distillation, the product with an epilogue, mixture of experts.
 #pragma once
 
 #include "../../include/sherry_ops.h"
@@ -214,5 +214,53 @@ struct DistillGrad {
 DistillSplit plan_distill(int64_t rows, int64_t vocab, bool bf16, bool backward);
 hipError_t launch_distill(const DistillArgs& a, int64_t rows, bool bf16, bool teacher_bf16, hipStream_t s);
 hipError_t launch_distill_backward(const DistillGrad& a, int64_t rows, bool bf16, hipStream_t s);
+
+// ---------------------------------------------------------------- product with an epilogue
+struct LinearArgs {
+  const uint8_t* packed;
+  const float* alpha;
+  int64_t n, k;              // gated: n counts the gate's and the values' rows
+  int gran, group_sbs;
+  const void* bias;          // [n] or null
+  bool bias_bf16;
+  int activation;
+  bool gated;
+  const uint16_t* residual;  // [tokens, outputs] or null
+  float res_scale;
+};
+hipError_t launch_linear_decode(const LinearArgs& a, const uint16_t* x, int tokens, void* y, bool y_bf16,
+                                hipStream_t s);
+
+hipError_t launch_linear_gemm(const GemmPlan& p, const LinearArgs& a, const uint16_t* x, int64_t m, uint16_t* y,
+                              float* ws, hipStream_t s);
+
+// ---------------------------------------------------------------- mixture of experts
+constexpr int kMoeExperts = 512, kMoeTopK = 16, kMoeShared = 4;
+struct MoeArgs {
+  const uint16_t* x;
+  int tokens, experts, top_k, shared, slots;   // slots = top_k + shared
+  int64_t dim, hidden;
+  const void* router;
+  bool router_bf16, softmax, normalize, gated;
+  const float* bias;                           // [experts] or null
+  float scale;
+  int activation;
+  const uint8_t *up, *down;                    // [experts + shared] packed weights, one after another
+  const float *up_alpha, *down_alpha;
+  int64_t up_bytes, down_bytes, up_scales, down_scales;
+  int up_gran, up_group_sbs, down_gran, down_group_sbs;
+  const uint16_t* residual;
+  float* logits;                               // [tokens, experts]
+  __bf16* h;                                   // [2][tokens, slots, hidden]
+  int64_t h_plane;
+  bool by_choice;                              // launches over (token, rank), not experts
+  int choices;
+};
+struct MoePlan {
+  size_t h_offset, workspace_bytes;
+  int64_t h_plane;
+};
+MoePlan plan_moe(int tokens, int experts, int slots, int64_t hidden);
+hipError_t launch_moe(MoeArgs a, void* y, bool y_bf16, hipStream_t s);
 
 }  // namespace sherry

@@ -1,0 +1,124 @@
+"""The packed product with what follows it: bias, activation and residual.
+
+    y = f(x (T alpha)^T + bias) + res_scale * residual
+
+or, for a gate and its values packed as one weight (`quantize_pack_fused`),
+with their rows [gate; values]:
+
+    y = f(z_gate) * z_values + res_scale * residual
+"""
+
+from __future__ import annotations
+
+from . import _gran, _lib, _need_current, _need_gpu, _on_stream, _stream, _torch, _y_dtype
+from ._lib import check, load
+
+_NONE = (1 << 64) - 1
+
+
+def _planes(packed, alpha, n, k, granularity, group_size, count, dev, name=""):
+    """Checks the planes and scales of ``count`` packed weights [n, k]; their granularity's code."""
+    torch = _torch()
+    gran = _gran(granularity)
+    if n < 1 or k < 1 or (gran == _lib.PER_GROUP and group_size < 1):
+        raise ValueError(f"{name}packed weight [{n}, {k}], group size {group_size}: not a shape")
+    scales = {_lib.PER_TENSOR: 1, _lib.PER_CHANNEL: n}.get(gran, n * (k // group_size) if group_size > 0 else 0)
+    for t, what, dtype, size in ((packed, "packed", torch.uint8, n * k // 32 * 5), (alpha, "alpha", torch.float32, scales)):
+        if t.dtype != dtype or t.device != dev or not t.is_contiguous() or t.numel() < count * size:
+            _need_gpu(t, name + what, dev)
+            raise ValueError(f"{name}{what} must be a contiguous {dtype} tensor of {count} x {size} elements")
+    return gran
+
+
+def _activation(name):
+    try:
+        return _lib.ACTIVATIONS[name]
+    except KeyError:
+        raise ValueError(f"activation must be one of {', '.join(_lib.ACTIVATIONS)}, got {name!r}") from None
+
+
+def _rows(t, name, shape, dev):
+    """A bf16 operand or output of this shape."""
+    torch = _torch()
+    if t.dtype != torch.bfloat16 or t.shape != shape or t.device != dev:
+        _need_gpu(t, name, dev)
+        raise ValueError(f"{name} must be bfloat16 {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
+    return t if t.is_contiguous() else t.contiguous()
+
+
+def _place(out, dtype, shape, dev):
+    """The caller's output, or a new one."""
+    if out is None:
+        return _torch().empty(shape, dtype=dtype, device=dev)
+    if out.dtype != dtype or out.shape != shape or out.device != dev or not out.is_contiguous():
+        _need_gpu(out, "out", dev)
+        raise ValueError(f"out must be contiguous {dtype} {tuple(shape)}, got {out.dtype} {tuple(out.shape)}")
+    return out
+
+
+def _linear(pw, x, bias, activation, gated, residual, res_scale, decode, y_dtype, stream, out):
+    torch = _torch()
+    packed, n, k = pw.packed, pw.n, pw.k
+    dev = packed.device
+    if not packed.is_cuda:
+        _need_gpu(packed, "packed")
+    _need_current(dev)
+    gran = _planes(packed, pw.alpha, n, k, pw.granularity, pw.group_size, 1, dev)
+    act = _activation(activation)
+    if gated and n % 2:
+        raise ValueError(f"a gated product needs an even number of rows [gate; values], got {n}")
+    if decode and x.dim() == 1:
+        x = x.unsqueeze(0)
+        residual = residual if residual is None or residual.dim() != 1 else residual.unsqueeze(0)
+    m, outs = x.shape[0] if x.dim() == 2 else -1, n // 2 if gated else n
+    x = _rows(x, "x", (m, k), dev)
+    y = _place(out, y_dtype[0], (m, outs), dev)
+    res = None
+    if residual is not None:
+        residual = _rows(residual, "residual", (m, outs), dev)
+        res = residual.data_ptr()
+    elif res_scale != 1.0:
+        raise ValueError("res_scale belongs to a residual")
+    b, b_code = None, 0
+    if bias is not None:
+        b_code = {torch.float32: _lib.F32, torch.bfloat16: _lib.BF16}.get(bias.dtype)
+        if b_code is None or bias.shape != (n,) or bias.device != dev:
+            _need_gpu(bias, "bias", dev)
+            raise ValueError(f"bias must be float32 or bfloat16 [{n}], got {bias.dtype} {tuple(bias.shape)}")
+        bias = bias if bias.is_contiguous() else bias.contiguous()
+        b = bias.data_ptr()
+    lib = load()
+    head = (n, k, gran, pw.group_size, packed.data_ptr(), pw.alpha.data_ptr(), x.data_ptr(), m, y.data_ptr())
+    tail = (b, b_code, act, bool(gated), res, res_scale)
+    if decode:
+        check(lib.sherry_linear_gemv(*head, y_dtype[1], *tail, _stream(stream)))
+        return y
+    nbytes = lib.sherry_workspace_bytes(_lib.OP_GEMM, n, k, gran, pw.group_size, m, 1)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if 0 < nbytes < _NONE else None
+    check(lib.sherry_linear_gemm(*head, *tail, None if ws is None else ws.data_ptr(), 0 if ws is None else nbytes,
+                                 _stream(stream)))
+    return y
+
+
+def _on(stream, *args):
+    if stream is None:
+        return _linear(*args[:-1], None, args[-1])
+    with _on_stream(stream):
+        return _linear(*args[:-1], stream, args[-1])
+
+
+def linear_gemv(pw, x, bias=None, activation: str = "none", gated: bool = False, residual=None, res_scale: float = 1.0,
+                y_dtype="bfloat16", stream=None, out=None):
+    """The product of a decode batch ``x`` [B, K] bf16 (B = 1..16) with its epilogue, in one launch and with one
+    rounding.
+
+    ``bias`` [N] fp32 or bf16; ``activation`` none, relu, relu2 (squared), silu, gelu or gelu_tanh; ``gated``: the
+    weight's rows are [gate; values] and y is [B, N/2]; ``residual`` bf16 of y's shape.  ``out`` may be ``residual``
+    (the residual stream updated in place)."""
+    return _on(stream, pw, x, bias, activation, gated, residual, res_scale, True, _y_dtype(y_dtype), out)
+
+
+def linear_gemm(pw, x, bias=None, activation: str = "none", gated: bool = False, residual=None, res_scale: float = 1.0,
+                stream=None, out=None):
+    """The same for prefill activations ``x`` [M, K] bf16 -> bf16 [M, N or N/2], on MFMA."""
+    return _on(stream, pw, x, bias, activation, gated, residual, res_scale, False, (_torch().bfloat16, _lib.BF16), out)

@@ -1,0 +1,261 @@
+"""The mixture-of-experts layer of packed experts against its definition in 64
+bits (the packed experts as the library unpacks them).
+
+Tolerances, as in the product's tests: fp32 sums of K products by steps of 32
+and of 128 are off by (K / 32 + K / 128 + 64) 2^-23 of the sum of magnitudes; an
+activation by 2^-17 of itself, its argument's error times its slope; h, two
+bf16 terms, by 2^-17; a weight of the router by twice its logits' error and
+2^-18; y by one rounding."""
+
+import pytest
+
+torch = pytest.importorskip("torch")
+S = pytest.importorskip("ternary_weight_quantization_sparse_amd")
+
+from test_ops_linear import act, act_tol, close  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+F32, BF16, F64 = torch.float32, torch.bfloat16, torch.float64
+INF = float("inf")
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a GPU")
+    S.load()
+
+
+def rand(gen, *shape, std=1.0, dtype=F32):
+    return (torch.randn(*shape, generator=gen, device=DEV) * std).to(dtype)
+
+
+class Layer:
+    def __init__(self, experts, dim, hidden, shared=0, grain="per_group", group=128, gated=True, router=BF16, seed=0):
+        gen = self.gen = torch.Generator(device=DEV).manual_seed(seed + experts + 3 * dim + hidden)
+        total = experts + shared
+        self.experts, self.shared, self.dim, self.hidden, self.gated = experts, shared, dim, hidden, gated
+        self.up = S.quantize_pack_experts(rand(gen, total, (2 if gated else 1) * hidden, dim, std=0.04), grain, group)
+        self.down = S.quantize_pack_experts(rand(gen, total, dim, hidden, std=0.04), grain, group)
+        self.router = self.steps(rand(gen, experts, dim, std=1.5 * dim ** -0.5), 512, 0.5).to(router)
+
+    def dense(self, packed, e):
+        return S.unpack(S.PackedWeight(packed.packed[e].clone(), packed.alpha[e].clone(), packed.n, packed.k, packed.granularity,
+                                       packed.group_size), "float32").double()
+
+    @staticmethod
+    def steps(t, per_one, most):
+        return ((t * per_one).round() / per_one).clamp(-most, most)
+
+    def tokens(self, m):
+        return self.steps(rand(self.gen, m, self.dim), 8, 8).to(BF16), rand(self.gen, m, self.dim, std=0.3, dtype=BF16)
+
+    def oracle(self, x, top_k, scoring, normalize, bias, scale, activation, residual, margin=True):
+        """(y, tolerance) in 64 bits."""
+        xd, r = x.double(), self.router.double()
+        logits = xd @ r.t().contiguous()
+        if margin:
+            assert (xd.abs() @ r.abs().t().contiguous()).max() * 2 ** 12 < 2 ** 24
+        score = logits.softmax(1) if scoring == "softmax" else logits.sigmoid()
+        key = logits if bias is None else score + bias.double()     # scores rise with their logits, also where they round to 1
+        y = torch.zeros_like(xd) if residual is None else residual.double()
+        dy = 2.0 ** -22 * y.abs()
+        for t in range(len(x)):
+            on = [e for e in range(self.experts) if float(key[t, e]) != -INF]
+            rank = sorted(on, key=lambda e: (-float(key[t, e]), e))
+            chosen = rank[:top_k]
+            if bias is not None and margin and len(rank) > len(chosen) and chosen:   # scores are rounded
+                gap = float(key[t, chosen[-1]] - key[t, rank[len(chosen)]])
+                assert gap == 0 or gap > 2.0 ** -20, "a draw too near"
+            w = score[t, chosen]
+            if normalize and len(chosen):
+                w = w / w.sum()
+            pairs = [(e, float(v) * scale, 2.0 ** -18) for e, v in zip(chosen, w)]
+            pairs += [(self.experts + s, 1.0, 0.0) for s in range(self.shared)]
+            for e, v, dv in pairs:
+                up, down = self.dense(self.up, e), self.dense(self.down, e)
+                z, dz = up.mv(xd[t]), (self.dim / 32 + self.dim / 128 + 64) * 2.0 ** -23 * up.abs().mv(xd[t].abs())
+                if self.gated:
+                    f, u = act(z[:self.hidden], activation), z[self.hidden:]
+                    df = act_tol(z[:self.hidden], dz[:self.hidden], activation)
+                    h, dh = f * u, df * u.abs() + (f.abs() + df) * dz[self.hidden:]
+                else:
+                    h, dh = act(z, activation), act_tol(z, dz, activation)
+                dh = dh + 2.0 ** -16 * h.abs()
+                size = down.abs().mv(h.abs())
+                y[t] += v * down.mv(h)
+                chain = (len(pairs) * self.hidden / 32 + self.hidden / 128 + 64) * 2.0 ** -23
+                dy[t] += abs(v) * ((1 + dv) * down.abs().mv(dh) + (dv + chain) * size)
+        return y, dy
+
+    def check(self, m, top_k, scoring="softmax", normalize=True, bias=None, scale=1.0, activation="silu", residual=True,
+              x=None, margin=True, **kw):
+        x, res = (x, None) if x is not None else self.tokens(m)
+        res = res if residual else None
+        y = S.moe_decode(x, self.router, self.up, self.down, top_k, shared=self.shared, scoring=scoring,
+                         normalize=normalize, bias=bias, scale=scale, activation=activation, residual=res, **kw)
+        want, tol = self.oracle(x, top_k, scoring, normalize, bias, scale, activation, res, margin)
+        close(y, want, tol)
+        return x, res, y
+
+
+@pytest.mark.parametrize("tokens", [1, 2, 5, 16])
+@pytest.mark.parametrize("experts,top_k,shared", [(1, 1, 0), (4, 4, 1), (8, 2, 0), (30, 3, 2), (64, 8, 0), (65, 1, 0),
+                                                  (128, 16, 1), (200, 6, 0), (512, 4, 4)])
+def test_experts(tokens, experts, top_k, shared):
+    Layer(experts, 256, 128, shared).check(tokens, top_k)
+
+
+@pytest.mark.parametrize("dim,hidden", [(128, 128), (128, 1024), (1152, 384), (2048, 512), (384, 3200)])
+@pytest.mark.parametrize("tokens", [1, 7])
+@pytest.mark.parametrize("grain,group", [("per_group", 128), ("per_group", 384), ("per_channel", 128), ("per_tensor", 128)])
+def test_sizes(dim, hidden, tokens, grain, group):
+    group = 128 if dim % group or hidden % group else group
+    Layer(5, dim, hidden, 1, grain, group).check(tokens, 2)
+
+
+@pytest.mark.parametrize("activation", ["none", "relu", "relu2", "silu", "gelu", "gelu_tanh"])
+@pytest.mark.parametrize("gated", [False, True])
+def test_activations(activation, gated):
+    Layer(6, 256, 256, gated=gated).check(3, 2, activation=activation)
+
+
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("normalize", [False, True])
+@pytest.mark.parametrize("biased", [False, True])
+@pytest.mark.parametrize("router", [BF16, F32])
+def test_routing(scoring, normalize, biased, router):
+    layer = Layer(70, 384, 128, 1, router=router)
+    bias = rand(layer.gen, 70, std=0.05) if biased else None
+    layer.check(9, 4, scoring, normalize, bias, scale=2.5, y_dtype="float32")
+    layer.check(1, 4, scoring, normalize, bias, scale=2.5, residual=False)
+
+
+@pytest.mark.parametrize("router", [BF16, F32])
+def test_router_of_full_precision(router):
+    """Logits of any rounding, where every expert is taken.  They are off by (D / 32 + 64) 2^-23 of the sum of
+    magnitudes (about 20), below 2^-12, and the weights by at most twice that of themselves; each expert's part of y is
+    below y's own largest, six of which are added."""
+    layer = Layer(6, 1024, 128, router=router)
+    layer.router = rand(layer.gen, 6, 1024, std=0.03, dtype=router)
+    x = rand(layer.gen, 5, 1024, dtype=BF16)
+    size = (x.double().abs() @ layer.router.double().abs().t().contiguous()).max()
+    assert (1024 / 32 + 64) * 2.0 ** -23 * size < 2.0 ** -12
+    y = S.moe_decode(x, layer.router, layer.up, layer.down, 6, y_dtype="float32")
+    want, tol = layer.oracle(x, 6, "softmax", True, None, 1.0, "silu", None, margin=False)
+    close(y, want, tol + 6 * 2.0 ** -11 * want.abs().max())
+
+
+def test_equal_logits_take_the_lower_index():
+    layer = Layer(12, 256, 128)
+    layer.router[3], layer.router[7], layer.router[11] = layer.router[1], layer.router[1], layer.router[1]
+    for m in (1, 9):
+        for top_k in (1, 2, 3, 6):
+            layer.check(m, top_k)
+    layer.router.zero_()                       # every expert the same, for every token
+    layer.check(5, 4, margin=False)
+    layer.check(1, 4, bias=torch.zeros(12, device=DEV), margin=False)
+
+
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("tokens", [1, 6])
+def test_experts_that_are_off(scoring, tokens):
+    layer = Layer(10, 256, 128, 1)
+    bias = torch.zeros(10, device=DEV)
+    bias[[0, 2, 3, 5, 6, 8, 9]] = -INF
+    layer.check(tokens, 2, scoring, bias=bias)
+    layer.check(tokens, 5, scoring, bias=bias)                          # three are left
+    layer.check(tokens, 5, scoring, normalize=False, bias=bias)
+    x, res, y = layer.check(tokens, 3, scoring, bias=torch.full((10,), -INF, device=DEV))   # the shared one alone
+    bare = Layer(10, 256, 128, 0)
+    x, res = bare.tokens(tokens)
+    y = S.moe_decode(x, bare.router, bare.up, bare.down, 3, scoring=scoring, bias=torch.full((10,), -INF, device=DEV),
+                     residual=res)
+    assert torch.equal(y, res)
+
+
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+def test_weights_of_far_logits(scoring):
+    """Logits of hundreds: weights by their logarithms lose none to another's size."""
+    layer = Layer(9, 256, 128, router=F32)
+    layer.router *= 32
+    layer.check(4, 3, scoring)
+    layer.router[:] = -layer.router.abs()
+    x = torch.ones(3, 256, dtype=BF16, device=DEV) * torch.tensor([[0.5], [0.25], [0.125]], device=DEV).to(BF16)
+    layer.check(3, 2, scoring, x=x)      # (logits of -300 to -50)
+
+
+def test_tokens_do_not_meet():
+    layer = Layer(16, 512, 256, 1)
+    x, res, clean = layer.check(8, 3)
+    x[2, 9], x[5] = float("nan"), INF
+    y = S.moe_decode(x, layer.router, layer.up, layer.down, 3, shared=1, residual=res)
+    others = [0, 1, 3, 4, 6, 7]
+    assert y[2].isnan().all() and y[5].isnan().any()
+    want, tol = layer.oracle(x[others], 3, "softmax", True, None, 1.0, "silu", res[others])
+    close(y[others], want, tol)
+
+
+def test_one_expert_for_all_and_all_experts():
+    layer = Layer(64, 256, 128)
+    x, res = layer.tokens(16)
+    layer.check(16, 2, x=x[:1].expand(16, -1).contiguous(), residual=False)
+    small = Layer(4, 256, 128)
+    small.check(16, 4)
+
+
+def test_in_place():
+    layer = Layer(8, 512, 256)
+    x, res, want = layer.check(5, 2)
+    args = (layer.router, layer.up, layer.down, 2)
+    other = res.clone()
+    assert S.moe_decode(x, *args, residual=other, out=other) is other and torch.equal(other, want)
+    assert torch.equal(S.moe_decode(x.clone(), *args, residual=res), want)
+    own = x.clone()
+    assert torch.equal(S.moe_decode(own, *args, residual=own, out=own), S.moe_decode(x, *args, residual=x))
+
+
+def test_repeats_and_streams():
+    layer = Layer(32, 1024, 512)
+    x, res, want = layer.check(16, 4)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    ys = [S.moe_decode(x, layer.router, layer.up, layer.down, 4, residual=res, stream=s) for s in (None, side, None)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, want) for y in ys)
+
+
+def test_experts_past_32_bits():
+    """Planes of 2.4 * 10^9 bytes and more: the last experts lie past them."""
+    dim, hidden, experts = 4096, 4096, 460
+    layer = Layer(2, dim, hidden)
+    def grow(p):
+        packed = torch.zeros(experts, p.packed.shape[1], dtype=torch.uint8, device=DEV)
+        alpha = torch.zeros(experts, p.alpha.shape[1], device=DEV)
+        packed[:2], alpha[:2], packed[-2:], alpha[-2:] = p.packed, p.alpha, p.packed, p.alpha
+        return S.PackedExperts(packed, alpha, experts, p.n, p.k)
+    up, down = grow(layer.up), grow(layer.down)
+    assert up.packed.numel() > 1 << 31
+    router = torch.zeros(experts, dim, dtype=BF16, device=DEV)
+    router[-2:] = layer.router
+    x, res = layer.tokens(3)
+    bias = torch.full((experts,), -INF, device=DEV)
+    bias[-2:] = 0
+    y = S.moe_decode(x, router, up, down, 2, bias=bias, residual=res)
+    assert torch.equal(y, S.moe_decode(x, layer.router, layer.up, layer.down, 2, bias=bias[-2:], residual=res))
+
+
+def test_refusals():
+    layer = Layer(4, 256, 128)
+    x, res = layer.tokens(3)
+    args = dict(x=x, router=layer.router, up=layer.up, down=layer.down, top_k=2)
+    short = S.PackedExperts(layer.up.packed[:3], layer.up.alpha, 4, 256, 256)
+    for bad in (dict(x=x.float()), dict(x=x[:, :128]), dict(x=x[0]), dict(x=x[:0]), dict(x=x.cpu()), dict(top_k=5), dict(top_k=0),
+                dict(shared=1), dict(shared=4), dict(router=layer.router[:3]), dict(router=layer.router.double()),
+                dict(scoring="max"), dict(activation="tanh"), dict(bias=torch.zeros(3, device=DEV)), dict(bias=torch.zeros(4)),
+                dict(residual=res.float()), dict(residual=res[:2]), dict(out=res.float()), dict(out=res[:2]), dict(up=layer.down),
+                dict(up=short), dict(down=layer.up), dict(y_dtype="float16"), dict(x=x[:1].expand(17, -1))):
+        with pytest.raises(ValueError):
+            S.moe_decode(**{**args, **bad})
+    assert S.moe_decode(**args).shape == (3, 256)
