@@ -27,149 +27,311 @@ struct Planes {
   const float* alpha;
   int64_t n;
   int group_sbs;      // superblocks of a scale group; 0: scales of a row or of the weight
-  uint32_t row_step;  // scales: 1 a row, 0 one for the weight
+  uint32_t row_step;  // bytes from one row's scale to the next: 4, or 0 (one for the weight)
 };
 __device__ inline Planes planes(const uint8_t* packed, const float* alpha, int64_t n, int64_t k, int gran,
                                 int group_sbs) {
   return Planes{packed, packed + nibble_plane_bytes(n, k), alpha, n, gran == SHERRY_PER_GROUP ? group_sbs : 0,
-                gran == SHERRY_PER_TENSOR ? 0u : 1u};
+                gran == SHERRY_PER_TENSOR ? 0u : 4u};
 }
 
-// Records of one superblock of TR row tiles.
+__device__ inline __amdgpu_buffer_rsrc_t buffer(const void* p, uint32_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), (short)0, (int)bytes, kBufferWord3);
+}
+#ifndef SHERRY_STREAM
+#define SHERRY_STREAM 0
+#endif
+constexpr int kStream = SHERRY_STREAM;
+constexpr uint32_t kNowhere = 1u << 31; // an offset outside every buffer here: reads zeros, without traffic
+
+struct Block {   // one superblock's slices of the planes and scales
+  __amdgpu_buffer_rsrc_t nib, sgn, al;
+};
+__device__ inline Block block(const Planes& p, int sb) {
+  const uint32_t n = (uint32_t)p.n;
+  const int group = p.group_sbs == 0 ? 0 : p.group_sbs == 1 ? sb : sb / p.group_sbs;
+  return Block{buffer(p.nib + (int64_t)sb * p.n * 16, n * 16u), buffer(p.sgn + (int64_t)sb * p.n * 4, n * 4u),
+               buffer(p.alpha + group * p.n, n * 4u)};   // (one scale for the weight: only the first is read)
+}
+
+// Records of one superblock of TR row tiles, as loaded and as the products take them: lane (r, q) of tile i has
+// nibble dword q, the sign dword and the scale of its row r.  Buffer loads, so that the loads of
+// an item past the end (rows nowhere) are issued like any other and cost no
+// traffic: the compiler can then count what is in flight, which a branch around them prevents.
+template <int TR>
+struct TileRecords {
+  uint32_t nib[TR], sgn[TR];
+  float al[TR];
+};
+// One and two tiles: each lane loads its own words.
 template <int TR>
 struct Records {
   uint32_t nib[TR], sgn[TR];
   float al[TR];
-};
-template <int TR>
-__device__ inline void load_records(const Planes& p, int sb, const uint32_t (&row)[TR], int q, Records<TR>& r) {
-  const uint8_t* nib = p.nib + (int64_t)sb * p.n * 16;
-  const uint8_t* sgn = p.sgn + (int64_t)sb * p.n * 4;
-  const int group = p.group_sbs == 0 ? 0 : p.group_sbs == 1 ? sb : sb / p.group_sbs;
-  const float* al = p.alpha + group * p.n;
+  __device__ void load(const Block& b, const uint32_t (&row)[TR], uint32_t row_step, int q) {
 #pragma unroll
-  for (int i = 0; i < TR; ++i) {
-    r.nib[i] = __builtin_nontemporal_load(reinterpret_cast<const uint32_t*>(nib + (row[i] * 16u + q * 4u)));
-    r.sgn[i] = __builtin_nontemporal_load(reinterpret_cast<const uint32_t*>(sgn + row[i] * 4u));
-    r.al[i] = al[row[i] * p.row_step];
+    for (int i = 0; i < TR; ++i) {
+      nib[i] = __builtin_amdgcn_raw_buffer_load_b32(b.nib, row[i] * 16u + q * 4u, 0, kStream);
+      sgn[i] = __builtin_amdgcn_raw_buffer_load_b32(b.sgn, row[i] * 4u, 0, kStream);
+      al[i] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(b.al, row[i] * row_step, 0, 0));
+    }
   }
+  __device__ TileRecords<TR> tiles() const {
+    TileRecords<TR> r;
+#pragma unroll
+    for (int i = 0; i < TR; ++i) r.nib[i] = nib[i], r.sgn[i] = sgn[i], r.al[i] = al[i];
+    return r;
+  }
+};
+// Four tiles: lane (r, q) loads the whole record of row r of tile q (three loads of 1 KB and 256 bytes instead of twelve),
+// and the 4 x 4 words of four lanes change places: M[q][word] to M[tile][q].
+template <>
+struct Records<4> {
+  u32x4 nib;
+  uint32_t sgn, al;
+  __device__ void load(const Block& b, const uint32_t (&row)[1], uint32_t row_step, int) {
+    nib = __builtin_amdgcn_raw_buffer_load_b128(b.nib, row[0] * 16u, 0, kStream);
+    sgn = __builtin_amdgcn_raw_buffer_load_b32(b.sgn, row[0] * 4u, 0, kStream);
+    al = __builtin_amdgcn_raw_buffer_load_b32(b.al, row[0] * row_step, 0, 0);
+  }
+  // halves, and odd with even rows of 16 lanes, change places
+  __device__ static void swap32(uint32_t& a, uint32_t& b) {
+    const auto v = __builtin_amdgcn_permlane32_swap(a, b, false, false);
+    a = v[0], b = v[1];
+  }
+  __device__ static void swap16(uint32_t& a, uint32_t& b) {
+    const auto v = __builtin_amdgcn_permlane16_swap(a, b, false, false);
+    a = v[0], b = v[1];
+  }
+  __device__ static void spread(uint32_t v, uint32_t (&w)[4]) {   // row q of 16 lanes to every row of w[q]
+    w[0] = w[2] = v;
+    swap32(w[0], w[2]);
+    w[1] = w[0], w[3] = w[2];
+    swap16(w[0], w[1]);
+    swap16(w[2], w[3]);
+  }
+  __device__ TileRecords<4> tiles() const {
+    TileRecords<4> r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r.nib[i] = nib[i];
+    swap32(r.nib[0], r.nib[2]);
+    swap32(r.nib[1], r.nib[3]);
+    swap16(r.nib[0], r.nib[1]);
+    swap16(r.nib[2], r.nib[3]);
+    spread(sgn, r.sgn);
+    uint32_t a[4];
+    spread(al, a);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r.al[i] = __uint_as_float(a[i]);
+    return r;
+  }
+};
+// A lane's rows of TR tiles whose row of tile i is row_of(i, r); kNoRow: its offsets lie outside every plane.
+constexpr uint32_t kNoRow = 1u << 27;
+template <int TR> constexpr int kRowsOf = TR == 4 ? 1 : TR;
+template <int TR, typename F>
+__device__ inline void lane_rows(F row_of, int r, int q, uint32_t (&row)[kRowsOf<TR>]) {
+#pragma unroll
+  for (int i = 0; i < kRowsOf<TR>; ++i) row[i] = row_of(TR == 4 ? q : i, r);
+}
+// A superblock of one token's bf16 values: lane (r, q)'s k = 32 t + 8 q .. + 7.
+__device__ inline void load_tokens(__amdgpu_buffer_rsrc_t x, uint32_t at, u32x4 (&xf)[4]) {
+#pragma unroll
+  for (int t = 0; t < 4; ++t) xf[t] = __builtin_amdgcn_raw_buffer_load_b128(x, at + 64u * t, 0, 0);
 }
 
 // acc += scale * weight * (tokens x tile) over one superblock; the tokens'
 // values are the sum of TERMS bf16 terms.
+// Tiles take turns, so that a tile's products are not a chain that each waits for.
 template <int TR, int TERMS>
-__device__ inline void multiply(const Records<TR>& r, const u32x4 (&x)[TERMS][4], const char* dtab, int q,
+__device__ inline void multiply(const Records<TR>& rec, const u32x4 (&x)[TERMS][4], const char* dtab, int q,
                                 const f32x4 weight, f32x4 (&acc)[TR]) {
+  const TileRecords<TR> r = rec.tiles();
+  uint32_t lo[TR], hi[TR];
+  f32x4 g[TR];
 #pragma unroll
   for (int i = 0; i < TR; ++i) {
-    const uint32_t lo = quad_offsets8(r.nib[i], r.sgn[i], 2 * q), hi = quad_offsets8(r.nib[i], r.sgn[i], 2 * q + 1);
-    f32x4 g = {0.f, 0.f, 0.f, 0.f};
+    lo[i] = quad_offsets8(r.nib[i], r.sgn[i], 2 * q);
+    hi[i] = quad_offsets8(r.nib[i], r.sgn[i], 2 * q + 1);
+    g[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+  }
 #pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      const uint2 e0 = *reinterpret_cast<const uint2*>(dtab + __builtin_amdgcn_ubfe(lo, 8 * t, 8));
-      const uint2 e1 = *reinterpret_cast<const uint2*>(dtab + __builtin_amdgcn_ubfe(hi, 8 * t, 8));
+  for (int t = 0; t < 4; ++t)
+#pragma unroll
+    for (int i = 0; i < TR; ++i) {
+      const uint2 e0 = *reinterpret_cast<const uint2*>(dtab + __builtin_amdgcn_ubfe(lo[i], 8 * t, 8));
+      const uint2 e1 = *reinterpret_cast<const uint2*>(dtab + __builtin_amdgcn_ubfe(hi[i], 8 * t, 8));
       const bf16x8 w = __builtin_bit_cast(bf16x8, u32x4{e0.x, e0.y, e1.x, e1.y});
 #pragma unroll
       for (int m = TERMS - 1; m >= 0; --m)
-        g = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x[m][t]), w, g, 0, 0, 0);
+        g[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x[m][t]), w, g[i], 0, 0, 0);
     }
 #pragma unroll
-    for (int e = 0; e < 4; ++e) acc[i][e] += r.al[i] * weight[e] * g[e];
+  for (int i = 0; i < TR; ++i)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[i][e] += r.al[i] * weight[e] * g[i][e];
+}
+
+// Items [j0, j1) of a wave: records through a ring of RING register sets, tokens through one of XRING; an item's
+// loads are issued as soon as its set is free.  records(j, live, set), tokens(j, live, set), weight(j).
+template <int TR, int TERMS, int RING, int XRING, typename R, typename X, typename W>
+__device__ inline void run_items(int j0, int j1, const char* dtab, int q, R records, X tokens, W weight,
+                                 f32x4 (&acc)[TR]) {
+  static_assert(RING % XRING == 0, "sets of one item in step");
+  if (j0 >= j1) return;
+  Records<TR> rec[RING];
+  u32x4 x[XRING][TERMS][4];
+  const int last = j1 - 1;
+#pragma unroll
+  for (int d = 0; d < RING; ++d) {
+    if (d < XRING) tokens(min(j0 + d, last), j0 + d < j1, x[d < XRING ? d : 0]);
+    records(min(j0 + d, last), j0 + d < j1, rec[d]);
+  }
+  for (int j = j0;; j += RING) {
+#pragma unroll
+    for (int d = 0; d < RING; ++d) {
+      const int at = j + d;
+      multiply<TR, TERMS>(rec[d], x[d % XRING], dtab, q, weight(at), acc);
+      if (at + 1 >= j1) return;
+      tokens(min(at + XRING, last), at + XRING < j1, x[d % XRING]);
+      records(min(at + RING, last), at + RING < j1, rec[d]);
+    }
   }
 }
 
-// Items [j0, j1) of a wave, DEPTH at a time, the next ones' loads under the
-// current ones' products.  load(j, records, x) and weight(j); items past the
-// end are not loaded.
-template <int TR, int TERMS, int DEPTH, typename Load, typename Weight>
-__device__ inline void run_items(int j0, int j1, const char* dtab, int q, Load load, Weight weight,
-                                 f32x4 (&acc)[TR]) {
-  Records<TR> rec[2][DEPTH];
-  u32x4 x[2][DEPTH][TERMS][4];
-  auto fetch = [&](int buf, int j) {
+// One output tile of a packed weight: TR row tiles (GATED: half gate rows, half the same outputs' rows of the
+// weight's second half).  The waves split K; a wave issues all its loads at once where it has up to XS superblocks (0: more,
+// through a ring), and the waves join through LDS: sums(which, token, column) afterwards adds them in order.  Short
+// workgroups, eight waves a SIMD, hide the latency better than ones that walk several tiles and load
+// ahead (mixture of experts, 16 tokens, 56 experts of 2048 x 2048: 18 us against 20 to 25).
+template <int TR, int WAVES, bool GATED, int XS>
+__device__ inline void tile_product(const Planes& p, int64_t outs, int sbs, __amdgpu_buffer_rsrc_t x, uint32_t x_lane,
+                                    int64_t tile, const char* dtab, f32x4 (&part)[WAVES][TR][64]) {
+  constexpr int kOut = GATED ? TR / 2 : TR, kHeld = XS > 0 ? XS : 1;
+  const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int j0 = sbs * wave / WAVES, j1 = sbs * (wave + 1) / WAVES;
+  const f32x4 one = {1.f, 1.f, 1.f, 1.f};
+  uint32_t row[kRowsOf<TR>];
+  lane_rows<TR>(
+      [&](int i, int rr) {
+        const int64_t col = tile * (16 * kOut) + (i % kOut) * 16 + rr;
+        return col < outs ? (uint32_t)(i < kOut ? col : outs + col) : kNoRow;
+      },
+      r, q, row);
+  f32x4 acc[TR];
 #pragma unroll
-    for (int d = 0; d < DEPTH; ++d)
-      if (j + d < j1) load(j + d, rec[buf][d], x[buf][d]);
-  };
-  auto use = [&](int buf, int j) {
+  for (int i = 0; i < TR; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+  if constexpr (XS > 0) {
+    Records<TR> rec[kHeld];
+    u32x4 xs[kHeld][1][4];
+    // (a set past the wave's range repeats a superblock with tokens of zeros)
 #pragma unroll
-    for (int d = 0; d < DEPTH; ++d)
-      if (j + d < j1) multiply<TR, TERMS>(rec[buf][d], x[buf][d], dtab, q, weight(j + d), acc);
-  };
-  fetch(0, j0);
-  for (int j = j0; j < j1; j += 2 * DEPTH) {
-    fetch(1, j + DEPTH);
-    use(0, j);
-    fetch(0, j + 2 * DEPTH);
-    use(1, j + DEPTH);
+    for (int d = 0; d < kHeld; ++d) {
+      rec[d].load(block(p, max(min(j0 + d, j1 - 1), 0)), row, p.row_step, q);
+      load_tokens(x, j0 + d < j1 ? x_lane + (uint32_t)(j0 + d) * (2 * kSuperblock) : kNowhere, xs[d][0]);
+    }
+    lds_barrier();   // the table is written
+#pragma unroll
+    for (int d = 0; d < kHeld; ++d) multiply<TR, 1>(rec[d], xs[d], dtab, q, one, acc);
+  } else {
+    lds_barrier();
+    run_items<TR, 1, 2, 2>(
+        j0, j1, dtab, q,
+        [&](int j, bool live, Records<TR>& to) { if (live) to.load(block(p, j), row, p.row_step, q); },
+        [&](int j, bool live, u32x4 (&to)[1][4]) {
+          if (live) load_tokens(x, x_lane + (uint32_t)j * (2 * kSuperblock), to[0]);
+        },
+        [&](int) { return one; }, acc);
   }
+#pragma unroll
+  for (int i = 0; i < TR; ++i) part[wave][i][lane] = acc[i];
+  lds_barrier();
+}
+template <int TR, int WAVES>
+__device__ inline float wave_sums(const f32x4 (&part)[WAVES][TR][64], int which, int token, int c) {
+  float sum = 0.f;
+#pragma unroll
+  for (int w = 0; w < WAVES; ++w) sum += part[w][which][(token >> 2) * 16 + c][token & 3];
+  return sum;
 }
 
 // ------------------------------------------------------------ linear, 1..16 tokens
-// Workgroup: TR row tiles (gated: the first half of them gate rows, the others
-// the same outputs' rows of the second half), WAVES ranges of K.
-template <int TR, int WAVES, bool GATED>
+template <int TR, int WAVES, bool GATED, int XS>
 __global__ __launch_bounds__(64 * WAVES) void linear_decode(LinearArgs a, const uint16_t* __restrict__ x, int tokens,
                                                             void* __restrict__ y, bool y_bf16) {
   static_assert(!GATED || TR % 2 == 0, "a gate tile and its other half");
   constexpr int kOut = GATED ? TR / 2 : TR;   // output tiles
   __shared__ __attribute__((aligned(16))) uint2 dtab[32];
   __shared__ f32x4 part[WAVES][TR][64];
-  const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int r = lane & 15, q = lane >> 4;
+  const int tid = threadIdx.x, lane = tid & 63, r = lane & 15, q = lane >> 4;
   if (tid < 32) dtab[tid] = decode_bf16(tid);
   const int64_t outs = GATED ? a.n / 2 : a.n;
-  const int64_t col0 = (int64_t)blockIdx.x * (16 * kOut);
   const Planes p = planes(a.packed, a.alpha, a.n, a.k, a.gran, a.group_sbs);
-  uint32_t row[TR];
-#pragma unroll
-  for (int i = 0; i < TR; ++i) {
-    const int64_t col = min(col0 + (i % kOut) * 16 + r, outs - 1);   // (repeated rows are not stored)
-    row[i] = (uint32_t)(i < kOut ? col : outs + col);
-  }
-  f32x4 acc[TR];
-#pragma unroll
-  for (int i = 0; i < TR; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-  __syncthreads();
-  const int sbs = (int)(a.k / kSuperblock);
-  const int j0 = sbs * wave / WAVES, j1 = sbs * (wave + 1) / WAVES;
-  const uint16_t* xr = x + (int64_t)r * a.k + 8 * q;
-  run_items<TR, 1, TR == 1 ? 2 : 1>(
-      j0, j1, reinterpret_cast<const char*>(dtab), q,
-      [&](int j, Records<TR>& rec, u32x4 (&xf)[1][4]) {
-        load_records<TR>(p, j, row, q, rec);
-#pragma unroll
-        for (int t = 0; t < 4; ++t)
-          xf[0][t] = r < tokens ? *reinterpret_cast<const u32x4*>(xr + (int64_t)j * kSuperblock + 32 * t)
-                                : u32x4{0u, 0u, 0u, 0u};
-      },
-      [](int) { return f32x4{1.f, 1.f, 1.f, 1.f}; }, acc);
-#pragma unroll
-  for (int i = 0; i < TR; ++i) part[wave][i][lane] = acc[i];
-  __syncthreads();
+  // consecutive workgroups land on different XCDs: give each XCD neighbouring tiles, which share memory lines
+  const int xcd = blockIdx.x & 7, share = gridDim.x >> 3, more = gridDim.x & 7;
+  const int64_t tile = xcd * share + min(xcd, more) + (blockIdx.x >> 3);
+  const uint32_t x_lane = r < tokens ? (uint32_t)(r * a.k + 8 * q) * 2u : kNowhere;
+  tile_product<TR, WAVES, GATED, XS>(p, outs, (int)(a.k / kSuperblock), buffer(x, (uint32_t)(tokens * a.k * 2)), x_lane,
+                                     tile, reinterpret_cast<const char*>(dtab), part);
   for (int o = tid; o < tokens * 16 * kOut; o += 64 * WAVES) {
-    const int tile = o / (16 * tokens), token = o / 16 % tokens, c = o % 16;
-    const int64_t col = col0 + tile * 16 + c;
+    const int token = o / (16 * kOut), which = o / 16 % kOut, c = o % 16;
+    const int64_t col = tile * (16 * kOut) + which * 16 + c;
     if (col >= outs) continue;
-    const int at = (token >> 2) * 16 + c, e = token & 3;
-    float z = 0.f, u = 0.f;
-#pragma unroll
-    for (int w = 0; w < WAVES; ++w) {
-      z += part[w][tile][at][e];
-      if constexpr (GATED) u += part[w][kOut + tile][at][e];
-    }
-    if (a.bias) {
-      z += load_float(a.bias, col, a.bias_bf16);
-      if constexpr (GATED) u += load_float(a.bias, outs + col, a.bias_bf16);
-    }
+    float z = wave_sums<TR, WAVES>(part, which, token, c);
+    if (a.bias) z += load_float(a.bias, col, a.bias_bf16);
     z = activate(z, a.activation);
-    if constexpr (GATED) z *= u;
+    if constexpr (GATED) {
+      float u = wave_sums<TR, WAVES>(part, kOut + which, token, c);
+      if (a.bias) u += load_float(a.bias, outs + col, a.bias_bf16);
+      z *= u;
+    }
     const int64_t to = (int64_t)token * outs + col;
     if (a.residual) z += a.res_scale * bf16_to_f32(a.residual[to]);
     if (y_bf16) static_cast<__bf16*>(y)[to] = (__bf16)z;
     else static_cast<float*>(y)[to] = z;
   }
+}
+
+// ------------------------------------------------------------ linear, 1..16 tokens
+template <int TR, int WAVES, bool GATED, int XS, int AHEAD>
+__global__ __launch_bounds__(64 * WAVES) void linear_decode(LinearArgs a, const uint16_t* __restrict__ x, int tokens,
+                                                            void* __restrict__ y, bool y_bf16) {
+  static_assert(!GATED || TR % 2 == 0, "a gate tile and its other half");
+  constexpr int kOut = GATED ? TR / 2 : TR;   // output tiles
+  __shared__ __attribute__((aligned(16))) uint2 dtab[32];
+  __shared__ f32x4 part[AHEAD == 1 ? 1 : 2][WAVES][TR][64];
+  const int tid = threadIdx.x, lane = tid & 63, r = lane & 15, q = lane >> 4;
+  if (tid < 32) dtab[tid] = decode_bf16(tid);
+  const int64_t outs = GATED ? a.n / 2 : a.n;
+  const Planes p = planes(a.packed, a.alpha, a.n, a.k, a.gran, a.group_sbs);
+  const int tiles = (int)((outs + 16 * kOut - 1) / (16 * kOut));
+  // consecutive workgroups land on different XCDs: give each XCD neighbouring tiles
+  const int xcd = blockIdx.x & 7, share = gridDim.x >> 3, more = gridDim.x & 7;
+  const int64_t group = xcd * share + min(xcd, more) + (blockIdx.x >> 3);
+  const uint32_t x_lane = r < tokens ? (uint32_t)(r * a.k + 8 * q) * 2u : kNowhere;
+  __syncthreads();
+  walk_tiles<TR, WAVES, GATED, XS, AHEAD>(
+      p, outs, (int)(a.k / kSuperblock), buffer(x, (uint32_t)(tokens * a.k * 2)), x_lane,
+      (int)((int64_t)tiles * group / gridDim.x), (int)((int64_t)tiles * (group + 1) / gridDim.x), reinterpret_cast<const char*>(dtab), part, [&](int tile, auto sums) {
+        for (int o = tid; o < tokens * 16 * kOut; o += 64 * WAVES) {
+          const int token = o / (16 * kOut), which = o / 16 % kOut, c = o % 16;
+          const int64_t col = (int64_t)tile * (16 * kOut) + which * 16 + c;
+          if (col >= outs) continue;
+          float z = sums(which, token, c);
+          if (a.bias) z += load_float(a.bias, col, a.bias_bf16);
+          z = activate(z, a.activation);
+          if constexpr (GATED) {
+            float u = sums(kOut + which, token, c);
+            if (a.bias) u += load_float(a.bias, outs + col, a.bias_bf16);
+            z *= u;
+          }
+          const int64_t to = (int64_t)token * outs + col;
+          if (a.residual) z += a.res_scale * bf16_to_f32(a.residual[to]);
+          if (y_bf16) static_cast<__bf16*>(y)[to] = (__bf16)z;
+          else static_cast<float*>(y)[to] = z;
+        }
+      });
 }
 
 // ------------------------------------------------------------ mixture of experts
@@ -217,11 +379,11 @@ struct Keys {
   float logit[R];
 };
 template <int R>
-__device__ inline void load_keys(const MoeArgs& a, int token, int lane, Keys<R>& k) {
+__device__ inline void load_keys(const MoeArgs& a, const float* logits, int lane, Keys<R>& k) {
 #pragma unroll
   for (int i = 0; i < R; ++i) {
     const int e = i * 64 + lane;
-    k.logit[i] = e < a.experts ? a.logits[(int64_t)token * a.experts + e] : -INFINITY;
+    k.logit[i] = e < a.experts ? logits[e] : -INFINITY;
     k.key[i] = e < a.experts ? order(k.logit[i]) : 0u;
   }
   if (!a.bias) return;
@@ -264,212 +426,117 @@ __device__ inline int take_best(Keys<R>& k, int lane) {
   }
   return e;
 }
-// Where expert e stands in the token's order; -1 beyond the top_k or off.
-template <int R>
-__device__ inline int rank_of(const MoeArgs& a, const Keys<R>& k, int e, int lane) {
-  uint32_t mine = 0;
+// Router logits of TILES tiles of 16 experts on MFMA (A: the tokens, B: the router's
+// rows): 32-channel steps [s0, s1), consecutive ones, so that a row's memory lines are read whole.  A float32 router goes in as
+// three bf16 terms (24 bits).
+template <bool R_BF16, int TILES>
+__device__ inline void logit_tiles(const MoeArgs& a, int tile0, int s0, int s1, int lane, f32x4 (&acc)[TILES]) {
+  constexpr int kAhead = TILES == 1 ? 4 : 2;
+  const int r = lane & 15, q = lane >> 4;
+  const uint16_t* xr = a.x + (int64_t)r * a.dim + 8 * q;
+  int64_t rr[TILES];
 #pragma unroll
-  for (int i = 0; i < R; ++i)
-    if (i == e / 64) mine = (uint32_t)__builtin_amdgcn_readlane((int)k.key[i], e & 63);
-  int rank = 0;
+  for (int i = 0; i < TILES; ++i) {
+    rr[i] = (int64_t)min((tile0 + i) * 16 + r, a.experts - 1) * a.dim + 8 * q;
+    acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+  }
+  for (int s = s0; s < s1; s += kAhead) {
+    u32x4 xv[kAhead], w[kAhead][TILES][R_BF16 ? 1 : 2];
 #pragma unroll
-  for (int i = 0; i < R; ++i)
-    rank += __popcll(__ballot(k.key[i] > mine || (k.key[i] == mine && i * 64 + lane < e)));
-  return mine > kOff && rank < a.top_k ? rank : -1;
+    for (int u = 0; u < kAhead; ++u) {
+      const bool in = s + u < s1;
+      xv[u] = in && r < a.tokens ? *reinterpret_cast<const u32x4*>(xr + (int64_t)(s + u) * 32) : u32x4{0u, 0u, 0u, 0u};
+#pragma unroll
+      for (int i = 0; i < TILES; ++i) {
+        const int64_t at = rr[i] + (int64_t)(s + u) * 32;
+        if constexpr (R_BF16) {
+          w[u][i][0] = in ? *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(a.router) + at) : u32x4{0u, 0u, 0u, 0u};
+        } else {
+          const u32x4* src = reinterpret_cast<const u32x4*>(static_cast<const float*>(a.router) + at);
+          w[u][i][0] = in ? src[0] : u32x4{0u, 0u, 0u, 0u};
+          w[u][i][R_BF16 ? 0 : 1] = in ? src[1] : u32x4{0u, 0u, 0u, 0u};
+        }
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      if (s + u >= s1) continue;
+      const bf16x8 xb = __builtin_bit_cast(bf16x8, xv[u]);
+#pragma unroll
+      for (int i = 0; i < TILES; ++i) {
+        if constexpr (R_BF16) {
+          acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xb, __builtin_bit_cast(bf16x8, w[u][i][0]), acc[i], 0, 0, 0);
+        } else {
+          bf16x8 term[3];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            float rest = __uint_as_float(w[u][i][R_BF16 ? 0 : e / 4][e % 4]);
+#pragma unroll
+            for (int t = 0; t < 3; ++t) {
+              term[t][e] = (__bf16)rest;
+              rest -= (float)term[t][e];
+            }
+          }
+#pragma unroll
+          for (int t = 2; t >= 0; --t) acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xb, term[t], acc[i], 0, 0, 0);
+        }
+      }
+    }
+  }
 }
 
-// Router logits [tokens, experts]: 16 experts a workgroup on MFMA (A: the
-// tokens, B: the router's rows), waves split the channels.  A float32 router
-// goes in as three bf16 terms (24 bits).
+// Logits [tokens, experts] of many experts: a tile a workgroup, waves share the channels.
 constexpr int kLogitWaves = 8;
 template <bool R_BF16>
 __global__ __launch_bounds__(64 * kLogitWaves) void moe_logits(MoeArgs a) {
-  constexpr int kAhead = 4;
-  __shared__ f32x4 part[kLogitWaves][64];
+  __shared__ f32x4 part[kLogitWaves][1][64];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int r = lane & 15, q = lane >> 4;
-  const int e0 = blockIdx.x * 16, expert = min(e0 + r, a.experts - 1);
   const int steps = (int)(a.dim / 32);
-  const uint16_t* xr = a.x + (int64_t)r * a.dim + 8 * q;
-  const int64_t rr = (int64_t)expert * a.dim + 8 * q;
-  f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-  for (int s = wave; s < steps; s += kAhead * kLogitWaves) {
-    u32x4 xv[kAhead], w[kAhead][R_BF16 ? 1 : 2];
-#pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      const int at = s + u * kLogitWaves;
-      const bool in = at < steps;
-      xv[u] = in && r < a.tokens ? *reinterpret_cast<const u32x4*>(xr + (int64_t)at * 32) : u32x4{0u, 0u, 0u, 0u};
-      if constexpr (R_BF16) {
-        w[u][0] = in ? *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(a.router) + rr + (int64_t)at * 32)
-                     : u32x4{0u, 0u, 0u, 0u};
-      } else {
-        const u32x4* src = reinterpret_cast<const u32x4*>(static_cast<const float*>(a.router) + rr + (int64_t)at * 32);
-        w[u][0] = in ? src[0] : u32x4{0u, 0u, 0u, 0u};
-        w[u][R_BF16 ? 0 : 1] = in ? src[1] : u32x4{0u, 0u, 0u, 0u};
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      if (s + u * kLogitWaves >= steps) continue;
-      const bf16x8 xb = __builtin_bit_cast(bf16x8, xv[u]);
-      if constexpr (R_BF16) {
-        acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xb, __builtin_bit_cast(bf16x8, w[u][0]), acc, 0, 0, 0);
-      } else {
-        bf16x8 term[3];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          float rest = __uint_as_float(w[u][R_BF16 ? 0 : i / 4][i % 4]);
-#pragma unroll
-          for (int t = 0; t < 3; ++t) {
-            term[t][i] = (__bf16)rest;
-            rest -= (float)term[t][i];
-          }
-        }
-#pragma unroll
-        for (int t = 2; t >= 0; --t) acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xb, term[t], acc, 0, 0, 0);
-      }
-    }
-  }
-  part[wave][lane] = acc;
+  f32x4 acc[1];
+  logit_tiles<R_BF16, 1>(a, blockIdx.x, steps * wave / kLogitWaves, steps * (wave + 1) / kLogitWaves, lane, acc);
+  part[wave][0][lane] = acc[0];
   __syncthreads();
   if (tid < 256) {
-    const int token = tid / 16, c = tid % 16;
-    float s = 0.f;
-#pragma unroll
-    for (int w = 0; w < kLogitWaves; ++w) s += part[w][(token >> 2) * 16 + c][token & 3];
-    if (token < a.tokens && e0 + c < a.experts) a.logits[(int64_t)token * a.experts + e0 + c] = s;
+    const int token = tid / 16, c = tid % 16, e = blockIdx.x * 16 + c;
+    if (token < a.tokens && e < a.experts) a.logits[(int64_t)token * a.experts + e] = wave_sums<1, kLogitWaves>(part, 0, token, c);
   }
 }
 
-// First products and the activation: h[token, slot] of one expert's TR / 2 (or TR) output tiles
-// for its tokens.  blockIdx.y names the expert (every expert, where the tokens' choices are as
-// many), or a (token, rank) whose expert it is: the first token that chose an expert stands for
-// all.  h is kept as two bf16 terms (16 bits, 2^-17 of the value, beside y's 2^-9 or the float32 sums').
-template <int TR, int WAVES, bool GATED, int R>
-__global__ __launch_bounds__(64 * WAVES) void moe_up(MoeArgs a) {
-  constexpr int kOut = GATED ? TR / 2 : TR;
-  __shared__ __attribute__((aligned(16))) uint2 dtab[32];
-  __shared__ f32x4 part[WAVES][TR][64];
-  __shared__ int rank[16];
-  const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int r = lane & 15, q = lane >> 4;
-  if (tid < 32) dtab[tid] = decode_bf16(tid);
-  const int y = blockIdx.y;
-  int expert;
-  if (y >= a.choices) {          // a shared expert: every token's
-    expert = a.experts + y - a.choices;
-    if (tid < 16) rank[tid] = tid < a.tokens ? a.top_k + y - a.choices : -1;
-  } else {
-    int first = 0;
-    if (a.by_choice) {
-      first = y / a.top_k;
-      Keys<R> k;
-      load_keys(a, first, lane, k);
-      for (int j = 0; j < y % a.top_k; ++j) take_best(k, lane);
-      expert = take_best(k, lane);
-      if (expert < 0) return;    // (every wave finds the same)
-    } else {
-      expert = y;
-    }
-    for (int t = wave; t < 16; t += WAVES) {
-      int at = -1;
-      if (t < a.tokens) {
-        Keys<R> k;
-        load_keys(a, t, lane, k);
-        at = rank_of(a, k, expert, lane);
-      }
-      if (lane == 0) rank[t] = at;
-    }
-    __syncthreads();
-    bool any = false;
-    for (int t = 0; t < 16; ++t) {
-      if (rank[t] < 0) continue;
-      if (a.by_choice && t < first) return;   // an earlier token's workgroup does it
-      any = true;
-    }
-    if (!any) return;
-  }
-  __syncthreads();
-  const int64_t outs = a.hidden, n = GATED ? 2 * outs : outs;
-  const int64_t col0 = (int64_t)blockIdx.x * (16 * kOut);
-  const Planes p = planes(a.up + expert * a.up_bytes, a.up_alpha + expert * a.up_scales, n, a.dim, a.up_gran, a.up_group_sbs);
-  uint32_t row[TR];
-#pragma unroll
-  for (int i = 0; i < TR; ++i) {
-    const int64_t col = min(col0 + (i % kOut) * 16 + r, outs - 1);
-    row[i] = (uint32_t)(i < kOut ? col : outs + col);
-  }
-  f32x4 acc[TR];
-#pragma unroll
-  for (int i = 0; i < TR; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-  const int sbs = (int)(a.dim / kSuperblock);
-  const int j0 = sbs * wave / WAVES, j1 = sbs * (wave + 1) / WAVES;
-  const uint16_t* xr = a.x + (int64_t)r * a.dim + 8 * q;
-  const bool mine = rank[r] >= 0;
-  run_items<TR, 1, 2>(
-      j0, j1, reinterpret_cast<const char*>(dtab), q,
-      [&](int j, Records<TR>& rec, u32x4 (&xf)[1][4]) {
-        load_records<TR>(p, j, row, q, rec);
-#pragma unroll
-        for (int t = 0; t < 4; ++t)
-          xf[0][t] = mine ? *reinterpret_cast<const u32x4*>(xr + (int64_t)j * kSuperblock + 32 * t)
-                          : u32x4{0u, 0u, 0u, 0u};
-      },
-      [](int) { return f32x4{1.f, 1.f, 1.f, 1.f}; }, acc);
-#pragma unroll
-  for (int i = 0; i < TR; ++i) part[wave][i][lane] = acc[i];
-  __syncthreads();
-  for (int o = tid; o < 256 * kOut; o += 64 * WAVES) {
-    const int tile = o / 256, token = o / 16 % 16, c = o % 16;
-    const int64_t col = col0 + tile * 16 + c;
-    if (rank[token] < 0 || col >= outs) continue;
-    const int at = (token >> 2) * 16 + c, e = token & 3;
-    float z = 0.f, u = 0.f;
-#pragma unroll
-    for (int w = 0; w < WAVES; ++w) {
-      z += part[w][tile][at][e];
-      if constexpr (GATED) u += part[w][kOut + tile][at][e];
-    }
-    z = activate(z, a.activation);
-    if constexpr (GATED) z *= u;
-    const __bf16 hi = (__bf16)z;
-    const float rest = z - (float)hi;
-    const int64_t to = ((int64_t)token * a.slots + rank[token]) * a.hidden + col;
-    a.h[to] = hi;
-    a.h[a.h_plane + to] = __builtin_isfinite(rest) ? (__bf16)rest : (__bf16)0.f;
-  }
-}
-
-// Second products, weighted and added over a token's experts, 16 output
-// channels a workgroup: its waves first choose (a token each), list the experts in
-// use, and then share their superblocks evenly.  A token's row of the A operand is its h of
-// the expert at hand, or zeros.
-constexpr int kDownWaves = 16;
-template <int R>
-__global__ __launch_bounds__(64 * kDownWaves) void moe_down(MoeArgs a, void* __restrict__ y, bool y_bf16) {
-  __shared__ __attribute__((aligned(16))) uint2 dtab[32];
-  __shared__ f32x4 part[kDownWaves][64];
+// The tokens' experts and weights, a token a wave, and from them the experts in use, in rising order
+// (then the shared ones), each with its place among every token's choices (-1: not chosen) and weight.
+// One workgroup; with few experts it makes the logits too (LOGITS tiles of them; 0: moe_logits did), which
+// saves a launch where one CU reads the router in less time.
+constexpr int kRouteWaves = 16;
+template <int R, int LOGITS, bool R_BF16>
+__global__ __launch_bounds__(64 * kRouteWaves) void moe_route(MoeArgs a) {
+  static_assert(LOGITS == 0 || R == 1, "logits of up to 64 experts");
+  constexpr int kTiles = LOGITS ? LOGITS : 1;
+  __shared__ f32x4 part[LOGITS ? kRouteWaves : 1][kTiles][64];
+  __shared__ float logits[LOGITS ? 16 : 1][64];
   __shared__ uint32_t used[kMoeExperts / 32];
-  __shared__ int list[16 * kMoeTopK + kMoeShared];     // the experts in use
-  __shared__ int8_t slot[16 * kMoeTopK + kMoeShared][16];
-  __shared__ __attribute__((aligned(16))) float weight[16 * kMoeTopK + kMoeShared][16];
+  __shared__ int list[kMoeSlots];
   __shared__ int chosen[16][kMoeTopK];
   __shared__ float chosen_w[16][kMoeTopK];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int r = lane & 15, q = lane >> 4;
-  if (tid < 32) dtab[tid] = decode_bf16(tid);
   if (tid < kMoeExperts / 32) used[tid] = 0u;
+  if constexpr (LOGITS != 0) {
+    const int steps = (int)(a.dim / 32);
+    f32x4 acc[kTiles];
+    logit_tiles<R_BF16, kTiles>(a, 0, steps * wave / kRouteWaves, steps * (wave + 1) / kRouteWaves, lane, acc);
+#pragma unroll
+    for (int i = 0; i < kTiles; ++i) part[wave][i][lane] = acc[i];
+    __syncthreads();
+    for (int o = tid; o < 16 * 16 * kTiles; o += 64 * kRouteWaves) {
+      const int token = o / (16 * kTiles), e = o % (16 * kTiles);
+      logits[token][e] = wave_sums<kTiles, kRouteWaves>(part, e / 16, token, e % 16);
+    }
+  }
   __syncthreads();
   if (wave < a.tokens) {
     Keys<R> k;
-    load_keys(a, wave, lane, k);
-    float logit[R];   // (the keys lose theirs)
-#pragma unroll
-    for (int i = 0; i < R; ++i) logit[i] = k.logit[i];
+    load_keys(a, LOGITS ? logits[wave] : a.logits + (int64_t)wave * a.experts, lane, k);
     int mine = -1;        // lane j: the j-th expert and its logit
     float l = -INFINITY;
     for (int j = 0; j < a.top_k; ++j) {
@@ -478,7 +545,7 @@ __global__ __launch_bounds__(64 * kDownWaves) void moe_down(MoeArgs a, void* __r
       if (e >= 0) {
 #pragma unroll
         for (int i = 0; i < R; ++i)
-          if (i == e / 64) v = __uint_as_float(__builtin_amdgcn_readlane(__float_as_int(logit[i]), e & 63));
+          if (i == e / 64) v = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(k.logit[i]), e & 63));
       }
       if (lane == j) {
         mine = e;
@@ -495,11 +562,11 @@ __global__ __launch_bounds__(64 * kDownWaves) void moe_down(MoeArgs a, void* __r
     } else if (a.softmax) {
       float top = -INFINITY, sum = 0.f;
 #pragma unroll
-      for (int i = 0; i < R; ++i) top = fmaxf(top, logit[i]);
+      for (int i = 0; i < R; ++i) top = fmaxf(top, k.logit[i]);
       top = wave_maxf(top);
 #pragma unroll
       for (int i = 0; i < R; ++i)
-        if (i * 64 + lane < a.experts) sum += expf(logit[i] - top);
+        if (i * 64 + lane < a.experts) sum += expf(k.logit[i] - top);
       w = expf(l - top) / wave_sumf(sum);
     } else {
       w = 1.f / (1.f + expf(-l));
@@ -511,7 +578,6 @@ __global__ __launch_bounds__(64 * kDownWaves) void moe_down(MoeArgs a, void* __r
     }
   }
   __syncthreads();
-  // the experts in use, in rising order, then the shared ones
   int count = 0;
   for (int w = 0; w < (a.experts + 31) / 32; ++w) {
     const uint32_t bits = used[w];
@@ -521,114 +587,252 @@ __global__ __launch_bounds__(64 * kDownWaves) void moe_down(MoeArgs a, void* __r
   if (tid < a.shared) list[count + tid] = a.experts + tid;
   const int total = count + a.shared;
   __syncthreads();
-  for (int i = tid; i < total * 16; i += 64 * kDownWaves) {
+  if (tid == 0) a.route->count = total;
+  for (int i = tid; i < total * 16; i += 64 * kRouteWaves) {
     const int at = i / 16, token = i % 16, e = list[at];
+    if (token == 0) a.route->list[at] = e;
     int s = -1;
     float w = 0.f;
     if (token < a.tokens) {
       if (at >= count) {
         s = a.top_k + at - count;
         w = 1.f;
+      } else {
+        for (int j = 0; j < a.top_k; ++j)
+          if (chosen[token][j] == e) {
+            s = j;
+            w = chosen_w[token][j];
+          }
       }
-      for (int j = 0; j < a.top_k && at < count; ++j)
-        if (chosen[token][j] == e) {
-          s = j;
-          w = chosen_w[token][j];
-        }
     }
-    slot[at][token] = (int8_t)s;
-    weight[at][token] = w;
+    a.route->place[at][token] = (int8_t)s;
+    a.route->weight[at][token] = w;
+  }
+}
+
+// First products and the activation: h[token, place] of the blockIdx.y-th expert in use, for its tokens.
+// h is kept as two bf16 terms (16 bits, 2^-17 of the value, beside y's 2^-9 or the float32 sums').
+template <int TR, int WAVES, bool GATED, int XS>
+__global__ __launch_bounds__(64 * WAVES) void moe_up(MoeArgs a) {
+  constexpr int kOut = GATED ? TR / 2 : TR;
+  __shared__ __attribute__((aligned(16))) uint2 dtab[32];
+  __shared__ f32x4 part[WAVES][TR][64];
+  __shared__ int place[16];
+  const int tid = threadIdx.x, lane = tid & 63, r = lane & 15, q = lane >> 4;
+  const int at = blockIdx.y;
+  const MoeRoute& route = *a.route;
+  const int count = route.count, expert = route.list[at], mine = route.place[at][r];   // (loaded together)
+  if (at >= count) return;
+  if (tid < 16) place[tid] = mine;
+  if (tid < 32) dtab[tid] = decode_bf16(tid);
+  const int64_t outs = a.hidden, n = GATED ? 2 * outs : outs, tile = blockIdx.x;
+  const Planes p = planes(a.up + expert * a.up_bytes, a.up_alpha + expert * a.up_scales, n, a.dim, a.up_gran, a.up_group_sbs);
+  const uint32_t x_lane = mine >= 0 ? (uint32_t)(r * a.dim + 8 * q) * 2u : kNowhere;
+  tile_product<TR, WAVES, GATED, XS>(p, outs, (int)(a.dim / kSuperblock), buffer(a.x, (uint32_t)(a.tokens * a.dim * 2)),
+                                     x_lane, tile, reinterpret_cast<const char*>(dtab), part);
+  for (int o = tid; o < 256 * kOut; o += 64 * WAVES) {
+    const int which = o / 256, token = o / 16 % 16, c = o % 16;
+    const int to_place = place[token];
+    if (to_place < 0) continue;
+    float z = activate(wave_sums<TR, WAVES>(part, which, token, c), a.activation);
+    if constexpr (GATED) z *= wave_sums<TR, WAVES>(part, kOut + which, token, c);
+    const __bf16 hi = (__bf16)z;
+    const float rest = z - (float)hi;
+    const int64_t to = ((int64_t)token * a.slots + to_place) * a.hidden + tile * (16 * kOut) + which * 16 + c;
+    a.h[to] = hi;
+    a.h[a.h_plane + to] = __builtin_isfinite(rest) ? (__bf16)rest : (__bf16)0.f;
+  }
+}
+
+// Second products, weighted and added over the experts in use: TR row tiles of y, one of gridDim.y
+// ranges of the (expert, superblock) items; the waves share a range evenly.  A token's row of the A operand is its h of
+// the expert at hand, or zeros.  Several ranges leave fp32 partials for moe_join.
+#ifndef SHERRY_WIDE
+#define SHERRY_WIDE 256
+#endif
+#ifndef SHERRY_DOWN
+#define SHERRY_DOWN 4, 8, 2, 1
+#endif
+constexpr int kDown[4] = {SHERRY_DOWN};
+constexpr int kDownTiles = kDown[0], kDownWaves = kDown[1], kDownRing = kDown[2], kDownXRing = kDown[3];
+__device__ inline void store_moe(const MoeArgs& a, int64_t to, float s, void* y, bool y_bf16) {
+  if (a.residual) s += bf16_to_f32(a.residual[to]);
+  if (y_bf16) static_cast<__bf16*>(y)[to] = (__bf16)s;
+  else static_cast<float*>(y)[to] = s;
+}
+__global__ __launch_bounds__(64 * kDownWaves) void moe_down(MoeArgs a, void* __restrict__ y, bool y_bf16) {
+  constexpr int TR = kDownTiles;
+  __shared__ __attribute__((aligned(16))) uint2 dtab[32];
+  __shared__ f32x4 part[kDownWaves][TR][64];
+  __shared__ int list[kMoeSlots];
+  __shared__ int8_t place[kMoeSlots][16];
+  __shared__ __attribute__((aligned(16))) float weight[kMoeSlots][16];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int r = lane & 15, q = lane >> 4;
+  if (tid < 32) dtab[tid] = decode_bf16(tid);
+  const MoeRoute& route = *a.route;
+  const int sbs = (int)(a.hidden / kSuperblock), items = route.count * sbs;
+  const int i0 = (int)((int64_t)items * blockIdx.y / gridDim.y), i1 = (int)((int64_t)items * (blockIdx.y + 1) / gridDim.y);
+  const int a0 = i0 / sbs, a1 = (i1 + sbs - 1) / sbs;
+  for (int i = tid; i < (a1 - a0) * 16; i += 64 * kDownWaves) {
+    const int at = i / 16, t = i % 16;
+    place[at][t] = route.place[a0 + at][t];
+    weight[at][t] = route.weight[a0 + at][t];
+    if (t == 0) list[at] = route.list[a0 + at];
   }
   __syncthreads();
-  const int64_t col0 = (int64_t)blockIdx.x * 16;
-  const uint32_t row[1] = {(uint32_t)(col0 + r)};
-  const int sbs = (int)(a.hidden / kSuperblock);
-  const int items = total * sbs;
-  f32x4 acc[1] = {f32x4{0.f, 0.f, 0.f, 0.f}};
-  run_items<1, 2, 1>(
-      items * wave / kDownWaves, items * (wave + 1) / kDownWaves, reinterpret_cast<const char*>(dtab), q,
-      [&](int j, Records<1>& rec, u32x4 (&xf)[2][4]) {
-        const int at = j / sbs, sb = j % sbs, e = __builtin_amdgcn_readfirstlane(list[at]);
+  const int64_t col0 = (int64_t)blockIdx.x * (16 * TR);
+  uint32_t row[kRowsOf<TR>];
+  lane_rows<TR>([&](int i, int rr) { return (uint32_t)col0 + i * 16 + rr; }, r, q, row);   // (dim is whole blocks of 64 rows)
+  f32x4 acc[TR];
+#pragma unroll
+  for (int i = 0; i < TR; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+  const auto h = buffer(a.h, (uint32_t)(2 * a.h_plane * 2));
+  run_items<TR, 2, kDownRing, kDownXRing>(
+      i0 + (i1 - i0) * wave / kDownWaves, i0 + (i1 - i0) * (wave + 1) / kDownWaves, reinterpret_cast<const char*>(dtab), q,
+      [&](int j, bool live, Records<TR>& rec) {
+        const int e = __builtin_amdgcn_readfirstlane(list[j / sbs - a0]);
         const Planes p = planes(a.down + e * a.down_bytes, a.down_alpha + e * a.down_scales, a.dim, a.hidden, a.down_gran,
                                 a.down_group_sbs);
-        load_records<1>(p, sb, row, q, rec);
-        const int s = slot[at][r];
-        const __bf16* h = a.h + ((int64_t)r * a.slots + s) * a.hidden + sb * kSuperblock + 8 * q;
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          xf[0][t] = s >= 0 ? *reinterpret_cast<const u32x4*>(h + 32 * t) : u32x4{0u, 0u, 0u, 0u};
-          xf[1][t] = s >= 0 ? *reinterpret_cast<const u32x4*>(h + a.h_plane + 32 * t) : u32x4{0u, 0u, 0u, 0u};
-        }
+        if (live) rec.load(block(p, j % sbs), row, p.row_step, q);
       },
-      [&](int j) { return *reinterpret_cast<const f32x4*>(&weight[j / sbs][4 * q]); }, acc);
-  part[wave][lane] = acc[0];
+      [&](int j, bool live, u32x4 (&xf)[2][4]) {
+        const int s = place[j / sbs - a0][r];
+        const uint32_t from = (uint32_t)((r * a.slots + s) * a.hidden + j % sbs * kSuperblock + 8 * q) * 2u;
+        if (!live) return;
+        load_tokens(h, s >= 0 ? from : kNowhere, xf[0]);
+        load_tokens(h, s >= 0 ? from + (uint32_t)a.h_plane * 2u : kNowhere, xf[1]);
+      },
+      [&](int j) { return *reinterpret_cast<const f32x4*>(&weight[j / sbs - a0][4 * q]); }, acc);
+#pragma unroll
+  for (int i = 0; i < TR; ++i) part[wave][i][lane] = acc[i];
   __syncthreads();
-  if (tid < 256) {
-    const int token = tid / 16, c = tid % 16;
-    if (token >= a.tokens) return;
+  for (int o = tid; o < a.tokens * 16 * TR; o += 64 * kDownWaves) {
+    const int token = o / (16 * TR), c = o % (16 * TR);
     float s = 0.f;
 #pragma unroll
-    for (int w = 0; w < kDownWaves; ++w) s += part[w][(token >> 2) * 16 + c][token & 3];
+    for (int w = 0; w < kDownWaves; ++w) s += part[w][c / 16][(token >> 2) * 16 + c % 16][token & 3];
     const int64_t to = (int64_t)token * a.dim + col0 + c;
-    if (a.residual) s += bf16_to_f32(a.residual[to]);
-    if (y_bf16) static_cast<__bf16*>(y)[to] = (__bf16)s;
-    else static_cast<float*>(y)[to] = s;
+    if (gridDim.y == 1) store_moe(a, to, s, y, y_bf16);
+    else a.partial[(int64_t)blockIdx.y * a.tokens * a.dim + to] = s;
   }
+}
+__global__ __launch_bounds__(256) void moe_join(MoeArgs a, void* __restrict__ y, bool y_bf16) {
+  const int64_t size = (int64_t)a.tokens * a.dim, to = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (to >= size) return;
+  float s = 0.f;
+  for (int z = 0; z < a.ranges; z += 8) {   // 8 loads ahead of their adds
+    float t[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) t[i] = z + i < a.ranges ? a.partial[(z + i) * size + to] : 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (z + i < a.ranges) s += t[i];
+  }
+  store_moe(a, to, s, y, y_bf16);
 }
 
 }  // namespace
 
-// Tiles of a workgroup and its ranges of K: a wave takes about two tiles'
-// superblocks at once, and 16 waves at most share them.
+// Waves by the superblocks of K, one to four of them each at once.
+#define SHERRY_TILES(RUN, SBS)          \
+  do {                                  \
+    if ((SBS) <= 4) RUN(4, 1);          \
+    else if ((SBS) <= 8) RUN(4, 2);     \
+    else if ((SBS) <= 16) RUN(8, 2);    \
+    else if ((SBS) <= 32) RUN(16, 2);   \
+    else if ((SBS) <= 64) RUN(16, 4);   \
+    else RUN(16, 0);                    \
+  } while (0)
+// 64 weight rows a workgroup where that leaves work for every CU; 16 (32: gate and values) where it does not.
+bool wide_tiles(int64_t blocks64) { return blocks64 >= SHERRY_WIDE; }
+
 hipError_t launch_linear_decode(const LinearArgs& a, const uint16_t* x, int tokens, void* y, bool y_bf16,
                                 hipStream_t s) {
   const int64_t outs = a.gated ? a.n / 2 : a.n;
-  const int sbs = (int)(a.k / kSuperblock);
-#define SHERRY_LINEAR(TR, W, G)                                                                             \
-  hipLaunchKernelGGL((linear_decode<TR, W, G>), dim3((unsigned)((outs + 16 * (G ? TR / 2 : TR) - 1) / (16 * (G ? TR / 2 : TR)))), \
-                     dim3(64 * W), 0, s, a, x, tokens, y, y_bf16)
-#define SHERRY_LINEAR_W(TR, G)            \
-  do {                                    \
-    if (sbs >= 16) SHERRY_LINEAR(TR, 8, G);  \
-    else SHERRY_LINEAR(TR, 4, G);         \
+  const bool wide = wide_tiles((a.n + 63) / 64);
+  const int64_t tile = wide ? (a.gated ? 32 : 64) : 16;
+  const dim3 grid((unsigned)((outs + tile - 1) / tile));
+#define SHERRY_LINEAR_T(TR, W, G, XS) \
+  hipLaunchKernelGGL((linear_decode<TR, W, G, XS>), grid, dim3(64 * W), 0, s, a, x, tokens, y, y_bf16)
+#define SHERRY_LINEAR(W, XS)                          \
+  do {                                                \
+    if (wide && a.gated) SHERRY_LINEAR_T(4, W, true, XS);  \
+    else if (wide) SHERRY_LINEAR_T(4, W, false, XS);  \
+    else if (a.gated) SHERRY_LINEAR_T(2, W, true, XS);\
+    else SHERRY_LINEAR_T(1, W, false, XS);            \
   } while (0)
-  if (a.gated) SHERRY_LINEAR_W(2, true);
-  else SHERRY_LINEAR_W(1, false);
-#undef SHERRY_LINEAR_W
+  SHERRY_TILES(SHERRY_LINEAR, a.k / kSuperblock);
 #undef SHERRY_LINEAR
+#undef SHERRY_LINEAR_T
   return hipGetLastError();
 }
 
-MoePlan plan_moe(int tokens, int experts, int slots, int64_t hidden) {
+// Ranges of the second products: about two items a wave, and at most 512 workgroups.
+MoePlan plan_moe(int tokens, int64_t dim, int64_t hidden, int experts, int shared, int top_k) {
   auto up = [](size_t b) { return (b + 255) & ~(size_t)255; };
+  const int slots = top_k + shared;
   MoePlan p{};
-  p.h_offset = up((size_t)tokens * experts * 4);
+  p.used = std::min(experts, tokens * top_k) + shared;
+  const int64_t items = p.used * (hidden / kSuperblock);
+  const int64_t blocks = dim / (16 * kDownTiles);
+  p.ranges = (int)std::max<int64_t>(1, std::min((items + 2 * kDownWaves - 1) / (2 * kDownWaves), (512 + blocks - 1) / blocks));
   p.h_plane = (int64_t)tokens * slots * hidden;
-  p.workspace_bytes = p.h_offset + up((size_t)p.h_plane * 4);
+  p.logits_offset = up(sizeof(MoeRoute));
+  p.h_offset = p.logits_offset + up((size_t)tokens * experts * 4);
+  p.partial_offset = p.h_offset + up((size_t)p.h_plane * 4);
+  p.workspace_bytes = p.partial_offset + (p.ranges > 1 ? up((size_t)p.ranges * tokens * dim * 4) : 0);
   return p;
 }
 
-hipError_t launch_moe(MoeArgs a, void* y, bool y_bf16, hipStream_t s) {
-  const dim3 routers((unsigned)((a.experts + 15) / 16));
-  if (a.router_bf16) hipLaunchKernelGGL(moe_logits<true>, routers, dim3(64 * kLogitWaves), 0, s, a);
-  else hipLaunchKernelGGL(moe_logits<false>, routers, dim3(64 * kLogitWaves), 0, s, a);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  a.by_choice = a.tokens * a.top_k < a.experts;
-  a.choices = a.by_choice ? a.tokens * a.top_k : a.experts;
-  const unsigned depth = (unsigned)(a.choices + a.shared);
-#define SHERRY_MOE(R)                                                                                                    \
-  do {                                                                                                                  \
-    if (a.gated) hipLaunchKernelGGL((moe_up<2, 4, true, R>), dim3((unsigned)(a.hidden / 16), depth), dim3(256), 0, s, a); \
-    else hipLaunchKernelGGL((moe_up<1, 4, false, R>), dim3((unsigned)(a.hidden / 16), depth), dim3(256), 0, s, a);        \
-    e = hipGetLastError();                                                                                              \
-    if (e != hipSuccess) return e;                                                                                      \
-    hipLaunchKernelGGL(moe_down<R>, dim3((unsigned)(a.dim / 16)), dim3(64 * kDownWaves), 0, s, a, y, y_bf16);            \
+hipError_t launch_moe(const MoePlan& p, MoeArgs a, void* y, bool y_bf16, hipStream_t s) {
+  const dim3 wg(64 * kRouteWaves);
+  hipError_t e;
+  a.ranges = p.ranges;
+  // one CU reads about 64 bytes a cycle: up to 512 KB of router (3.4 us) it does so itself
+  if (a.experts <= 64 && a.experts * a.dim * (a.router_bf16 ? 2 : 4) <= 512 * 1024) {
+#define SHERRY_ROUTE(T)                                                                     \
+  do {                                                                                      \
+    if (a.router_bf16) hipLaunchKernelGGL((moe_route<1, T, true>), dim3(1), wg, 0, s, a);   \
+    else hipLaunchKernelGGL((moe_route<1, T, false>), dim3(1), wg, 0, s, a);                \
   } while (0)
-  if (a.experts <= 64) SHERRY_MOE(1);
-  else if (a.experts <= 128) SHERRY_MOE(2);
-  else SHERRY_MOE(8);
-#undef SHERRY_MOE
+    if (a.experts <= 16) SHERRY_ROUTE(1);
+    else if (a.experts <= 32) SHERRY_ROUTE(2);
+    else SHERRY_ROUTE(4);
+#undef SHERRY_ROUTE
+  } else {
+    const dim3 tiles((unsigned)((a.experts + 15) / 16));
+    if (a.router_bf16) hipLaunchKernelGGL(moe_logits<true>, tiles, dim3(64 * kLogitWaves), 0, s, a);
+    else hipLaunchKernelGGL(moe_logits<false>, tiles, dim3(64 * kLogitWaves), 0, s, a);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    if (a.experts <= 64) hipLaunchKernelGGL((moe_route<1, 0, true>), dim3(1), wg, 0, s, a);
+    else if (a.experts <= 128) hipLaunchKernelGGL((moe_route<2, 0, true>), dim3(1), wg, 0, s, a);
+    else hipLaunchKernelGGL((moe_route<8, 0, true>), dim3(1), wg, 0, s, a);
+  }
+  e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  const bool wide = wide_tiles((a.gated ? 2 : 1) * a.hidden / 64 * p.used);
+  const dim3 first((unsigned)(a.hidden / (wide ? (a.gated ? 32 : 64) : 16)), (unsigned)p.used);
+#define SHERRY_UP_T(TR, W, G, XS) hipLaunchKernelGGL((moe_up<TR, W, G, XS>), first, dim3(64 * W), 0, s, a)
+#define SHERRY_UP(W, XS)                              \
+  do {                                                \
+    if (wide && a.gated) SHERRY_UP_T(4, W, true, XS); \
+    else if (wide) SHERRY_UP_T(4, W, false, XS);      \
+    else if (a.gated) SHERRY_UP_T(2, W, true, XS);    \
+    else SHERRY_UP_T(1, W, false, XS);                \
+  } while (0)
+  SHERRY_TILES(SHERRY_UP, a.dim / kSuperblock);
+#undef SHERRY_UP
+#undef SHERRY_UP_T
+  e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(moe_down, dim3((unsigned)(a.dim / (16 * kDownTiles)), (unsigned)p.ranges), dim3(64 * kDownWaves), 0,
+                     s, a, y, y_bf16);
+  e = hipGetLastError();
+  if (e != hipSuccess || p.ranges == 1) return e;
+  hipLaunchKernelGGL(moe_join, dim3((unsigned)((a.tokens * a.dim + 255) / 256)), dim3(256), 0, s, a, y, y_bf16);
   return hipGetLastError();
 }
 

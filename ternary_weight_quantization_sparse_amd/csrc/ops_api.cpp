@@ -398,7 +398,7 @@ int32_t sherry_linear_gemm(int64_t n, int64_t k, int32_t granularity, int32_t gr
 size_t sherry_moe_workspace_bytes(int32_t tokens, int64_t dim, int64_t hidden, int32_t experts, int32_t shared,
                                   int32_t top_k) {
   if (check_moe_sizes(tokens, dim, hidden, experts, shared, top_k) != SHERRY_OK) return (size_t)-1;
-  return plan_moe(tokens, experts, top_k + shared, hidden).workspace_bytes;
+  return plan_moe(tokens, dim, hidden, experts, shared, top_k).workspace_bytes;
 }
 
 int32_t sherry_moe_decode(int32_t tokens, int64_t dim, int64_t hidden, const void* x, const void* router,
@@ -425,7 +425,7 @@ int32_t sherry_moe_decode(int32_t tokens, int64_t dim, int64_t hidden, const voi
     return SHERRY_ERR_ALIGN;
   const size_t outs = (size_t)tokens * (size_t)dim;
   if (overlap(y, outs * item, residual, outs * 2) && !(y == residual && item == 2)) return SHERRY_ERR_ARG;
-  const MoePlan p = plan_moe(tokens, experts, top_k + shared, hidden);
+  const MoePlan p = plan_moe(tokens, dim, hidden, experts, shared, top_k);
   if (!workspace || workspace_bytes < p.workspace_bytes) return SHERRY_ERR_WORKSPACE;
   if (!aligned16(workspace)) return SHERRY_ERR_ALIGN;
   char* ws = static_cast<char*>(workspace);
@@ -436,9 +436,10 @@ int32_t sherry_moe_decode(int32_t tokens, int64_t dim, int64_t hidden, const voi
                   sherry_num_scales(up_n, dim, up_granularity, up_group),
                   sherry_num_scales(dim, hidden, down_granularity, down_group), up_granularity,
                   group_sbs_of(up_granularity, up_group), down_granularity, group_sbs_of(down_granularity, down_group),
-                  static_cast<const uint16_t*>(residual), reinterpret_cast<float*>(ws),
-                  reinterpret_cast<__bf16*>(ws + p.h_offset), p.h_plane, false, 0};
-  return hip_status(launch_moe(a, y, y_dtype == SHERRY_BF16, static_cast<hipStream_t>(stream)));
+                  static_cast<const uint16_t*>(residual), reinterpret_cast<MoeRoute*>(ws),
+                  reinterpret_cast<float*>(ws + p.logits_offset), reinterpret_cast<__bf16*>(ws + p.h_offset), p.h_plane,
+                  reinterpret_cast<float*>(ws + p.partial_offset), 0};
+  return hip_status(launch_moe(p, a, y, y_dtype == SHERRY_BF16, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -236,6 +236,13 @@ hipError_t launch_linear_gemm(const GemmPlan& p, const LinearArgs& a, const uint
 
 // ---------------------------------------------------------------- mixture of experts
 constexpr int kMoeExperts = 512, kMoeTopK = 16, kMoeShared = 4;
+constexpr int kMoeSlots = 16 * kMoeTopK + kMoeShared;   // experts in use at most
+struct MoeRoute {
+  int count;                         // experts in use
+  int list[kMoeSlots];
+  int8_t place[kMoeSlots][16];       // among the token's choices; -1: not one of them
+  float weight[kMoeSlots][16];
+};
 struct MoeArgs {
   const uint16_t* x;
   int tokens, experts, top_k, shared, slots;   // slots = top_k + shared
@@ -250,17 +257,20 @@ struct MoeArgs {
   int64_t up_bytes, down_bytes, up_scales, down_scales;
   int up_gran, up_group_sbs, down_gran, down_group_sbs;
   const uint16_t* residual;
-  float* logits;                               // [tokens, experts]
+  MoeRoute* route;
+  float* logits;                               // [tokens, experts], more than 64 of them
   __bf16* h;                                   // [2][tokens, slots, hidden]
   int64_t h_plane;
-  bool by_choice;                              // launches over (token, rank), not experts
-  int choices;
+  float* partial;                              // [ranges][tokens, dim]
+  int ranges;
 };
 struct MoePlan {
-  size_t h_offset, workspace_bytes;
+  int used;                                    // experts in use at most
+  int ranges;                                  // of the second products
   int64_t h_plane;
+  size_t logits_offset, h_offset, partial_offset, workspace_bytes;
 };
-MoePlan plan_moe(int tokens, int experts, int slots, int64_t hidden);
-hipError_t launch_moe(MoeArgs a, void* y, bool y_bf16, hipStream_t s);
+MoePlan plan_moe(int tokens, int64_t dim, int64_t hidden, int experts, int shared, int top_k);
+hipError_t launch_moe(const MoePlan& p, MoeArgs a, void* y, bool y_bf16, hipStream_t s);
 
 }  // namespace sherry

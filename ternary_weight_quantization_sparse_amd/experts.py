@@ -42,7 +42,7 @@ def quantize_pack_experts(w, granularity: str = "per_group", group_size: int = 1
 def moe_decode(x, router, up: PackedExperts, down: PackedExperts, top_k: int, shared: int = 0,
                scoring: str = "softmax", normalize: bool = True, bias=None, scale: float = 1.0,
                activation: str = "silu", residual=None, y_dtype="bfloat16", stream=None, out=None):
-    """The whole layer for tokens ``x`` [M, D] bf16, M = 1..16, in three launches.
+    """The whole layer for tokens ``x`` [M, D] bf16, M = 1..16.
 
     ``router`` [E, D] fp32 or bf16.  ``up`` holds E + shared weights [2H, D], rows [gate; up] (or [H, D]: no gate,
     h = f(up x)), ``down`` as many [D, H]; the ``shared`` last ones serve every token with the weight 1.
