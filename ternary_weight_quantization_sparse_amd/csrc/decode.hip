@@ -379,11 +379,17 @@ struct Keys {
   float logit[R];
 };
 template <int R>
-__device__ inline void load_keys(const MoeArgs& a, const float* logits, int lane, Keys<R>& k) {
+__device__ inline void load_keys(const MoeArgs& a, const float* logits, int parts, int64_t part_step, int lane,
+                                 Keys<R>& k) {
 #pragma unroll
   for (int i = 0; i < R; ++i) {
     const int e = i * 64 + lane;
-    k.logit[i] = e < a.experts ? logits[e] : -INFINITY;
+    float v[kMoeParts], sum = 0.f;
+#pragma unroll
+    for (int p = 0; p < kMoeParts; ++p) v[p] = e < a.experts && p < parts ? logits[p * part_step + e] : 0.f;
+#pragma unroll
+    for (int p = 0; p < kMoeParts; ++p) sum += v[p];
+    k.logit[i] = e < a.experts ? sum : -INFINITY;
     k.key[i] = e < a.experts ? order(k.logit[i]) : 0u;
   }
   if (!a.bias) return;
@@ -485,28 +491,28 @@ __device__ inline void logit_tiles(const MoeArgs& a, int tile0, int s0, int s1, 
   }
 }
 
-// Logits [tokens, experts] of many experts: a tile a workgroup, waves share the channels.
-constexpr int kLogitWaves = 8;
+// Logits of many experts, in parts over the channels [part, tokens, experts]: one CU alone reads a cold router slowly (64
+// experts of 2048 channels and 16 tokens, 320 KB: 12 us), so a tile and a part a workgroup.
+constexpr int kLogitWaves = 4;
 template <bool R_BF16>
 __global__ __launch_bounds__(64 * kLogitWaves) void moe_logits(MoeArgs a) {
   __shared__ f32x4 part[kLogitWaves][1][64];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int steps = (int)(a.dim / 32);
+  const int steps = (int)(a.dim / 32), share = a.parts * kLogitWaves, mine = blockIdx.y * kLogitWaves + wave;
   f32x4 acc[1];
-  logit_tiles<R_BF16, 1>(a, blockIdx.x, steps * wave / kLogitWaves, steps * (wave + 1) / kLogitWaves, lane, acc);
+  logit_tiles<R_BF16, 1>(a, blockIdx.x, steps * mine / share, steps * (mine + 1) / share, lane, acc);
   part[wave][0][lane] = acc[0];
   __syncthreads();
-  if (tid < 256) {
-    const int token = tid / 16, c = tid % 16, e = blockIdx.x * 16 + c;
-    if (token < a.tokens && e < a.experts) a.logits[(int64_t)token * a.experts + e] = wave_sums<1, kLogitWaves>(part, 0, token, c);
-  }
+  const int token = tid / 16, c = tid % 16, e = blockIdx.x * 16 + c;
+  if (token < a.tokens && e < a.experts)
+    a.logits[((int64_t)blockIdx.y * a.tokens + token) * a.experts + e] = wave_sums<1, kLogitWaves>(part, 0, token, c);
 }
 
 // The tokens' experts and weights, a token a wave, and from them the experts in use, in rising order
 // (then the shared ones), each with its place among every token's choices (-1: not chosen) and weight.
-// One workgroup; with few experts it makes the logits too (LOGITS tiles of them; 0: moe_logits did), which
-// saves a launch where one CU reads the router in less time.
+// One workgroup; with a small router it makes the logits too (LOGITS tiles of them; 0: moe_logits did), which
+// saves a launch.
 constexpr int kRouteWaves = 16;
 template <int R, int LOGITS, bool R_BF16>
 __global__ __launch_bounds__(64 * kRouteWaves) void moe_route(MoeArgs a) {
@@ -536,7 +542,8 @@ __global__ __launch_bounds__(64 * kRouteWaves) void moe_route(MoeArgs a) {
   __syncthreads();
   if (wave < a.tokens) {
     Keys<R> k;
-    load_keys(a, LOGITS ? logits[wave] : a.logits + (int64_t)wave * a.experts, lane, k);
+    if constexpr (LOGITS != 0) load_keys(a, logits[wave], 1, 0, lane, k);
+    else load_keys(a, a.logits + (int64_t)wave * a.experts, a.parts, (int64_t)a.tokens * a.experts, lane, k);
     int mine = -1;        // lane j: the j-th expert and its logit
     float l = -INFINITY;
     for (int j = 0; j < a.top_k; ++j) {
@@ -647,6 +654,9 @@ __global__ __launch_bounds__(64 * WAVES) void moe_up(MoeArgs a) {
 // Second products, weighted and added over the experts in use: TR row tiles of y, one of gridDim.y
 // ranges of the (expert, superblock) items; the waves share a range evenly.  A token's row of the A operand is its h of
 // the expert at hand, or zeros.  Several ranges leave fp32 partials for moe_join.
+#ifndef SHERRY_ROUTE_BYTES
+#define SHERRY_ROUTE_BYTES 65536   // router and tokens that the routing's one workgroup reads itself
+#endif
 #ifndef SHERRY_WIDE
 #define SHERRY_WIDE 256
 #endif
@@ -770,7 +780,7 @@ hipError_t launch_linear_decode(const LinearArgs& a, const uint16_t* x, int toke
 }
 
 // Ranges of the second products: about two items a wave, and at most 512 workgroups.
-MoePlan plan_moe(int tokens, int64_t dim, int64_t hidden, int experts, int shared, int top_k) {
+MoePlan plan_moe(int tokens, int64_t dim, int64_t hidden, int experts, int shared, int top_k, bool router_bf16) {
   auto up = [](size_t b) { return (b + 255) & ~(size_t)255; };
   const int slots = top_k + shared;
   MoePlan p{};
@@ -780,7 +790,9 @@ MoePlan plan_moe(int tokens, int64_t dim, int64_t hidden, int experts, int share
   p.ranges = (int)std::max<int64_t>(1, std::min((items + 2 * kDownWaves - 1) / (2 * kDownWaves), (512 + blocks - 1) / blocks));
   p.h_plane = (int64_t)tokens * slots * hidden;
   p.logits_offset = up(sizeof(MoeRoute));
-  p.h_offset = p.logits_offset + up((size_t)tokens * experts * 4);
+  const int64_t read = (experts * (router_bf16 ? 2 : 4) + tokens * 2) * dim;
+  p.parts = experts <= 64 && read <= SHERRY_ROUTE_BYTES ? 0 : (int)std::min<int64_t>(kMoeParts, (dim + 511) / 512);
+  p.h_offset = p.logits_offset + up((size_t)p.parts * tokens * experts * 4);
   p.partial_offset = p.h_offset + up((size_t)p.h_plane * 4);
   p.workspace_bytes = p.partial_offset + (p.ranges > 1 ? up((size_t)p.ranges * tokens * dim * 4) : 0);
   return p;
@@ -790,8 +802,8 @@ hipError_t launch_moe(const MoePlan& p, MoeArgs a, void* y, bool y_bf16, hipStre
   const dim3 wg(64 * kRouteWaves);
   hipError_t e;
   a.ranges = p.ranges;
-  // one CU reads about 64 bytes a cycle: up to 512 KB of router (3.4 us) it does so itself
-  if (a.experts <= 64 && a.experts * a.dim * (a.router_bf16 ? 2 : 4) <= 512 * 1024) {
+  a.parts = p.parts;
+  if (p.parts == 0) {
 #define SHERRY_ROUTE(T)                                                                     \
   do {                                                                                      \
     if (a.router_bf16) hipLaunchKernelGGL((moe_route<1, T, true>), dim3(1), wg, 0, s, a);   \
@@ -802,7 +814,7 @@ hipError_t launch_moe(const MoePlan& p, MoeArgs a, void* y, bool y_bf16, hipStre
     else SHERRY_ROUTE(4);
 #undef SHERRY_ROUTE
   } else {
-    const dim3 tiles((unsigned)((a.experts + 15) / 16));
+    const dim3 tiles((unsigned)((a.experts + 15) / 16), (unsigned)p.parts);
     if (a.router_bf16) hipLaunchKernelGGL(moe_logits<true>, tiles, dim3(64 * kLogitWaves), 0, s, a);
     else hipLaunchKernelGGL(moe_logits<false>, tiles, dim3(64 * kLogitWaves), 0, s, a);
     e = hipGetLastError();

@@ -3,6 +3,7 @@
 // on the host before anything is enqueued.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 
@@ -398,7 +399,9 @@ int32_t sherry_linear_gemm(int64_t n, int64_t k, int32_t granularity, int32_t gr
 size_t sherry_moe_workspace_bytes(int32_t tokens, int64_t dim, int64_t hidden, int32_t experts, int32_t shared,
                                   int32_t top_k) {
   if (check_moe_sizes(tokens, dim, hidden, experts, shared, top_k) != SHERRY_OK) return (size_t)-1;
-  return plan_moe(tokens, dim, hidden, experts, shared, top_k).workspace_bytes;
+  // (a float32 router's logits may take the launch that a bf16 one's do not)
+  return std::max(plan_moe(tokens, dim, hidden, experts, shared, top_k, true).workspace_bytes,
+                  plan_moe(tokens, dim, hidden, experts, shared, top_k, false).workspace_bytes);
 }
 
 int32_t sherry_moe_decode(int32_t tokens, int64_t dim, int64_t hidden, const void* x, const void* router,
@@ -425,7 +428,7 @@ int32_t sherry_moe_decode(int32_t tokens, int64_t dim, int64_t hidden, const voi
     return SHERRY_ERR_ALIGN;
   const size_t outs = (size_t)tokens * (size_t)dim;
   if (overlap(y, outs * item, residual, outs * 2) && !(y == residual && item == 2)) return SHERRY_ERR_ARG;
-  const MoePlan p = plan_moe(tokens, dim, hidden, experts, shared, top_k);
+  const MoePlan p = plan_moe(tokens, dim, hidden, experts, shared, top_k, router_dtype == SHERRY_BF16);
   if (!workspace || workspace_bytes < p.workspace_bytes) return SHERRY_ERR_WORKSPACE;
   if (!aligned16(workspace)) return SHERRY_ERR_ALIGN;
   char* ws = static_cast<char*>(workspace);
@@ -437,7 +440,7 @@ int32_t sherry_moe_decode(int32_t tokens, int64_t dim, int64_t hidden, const voi
                   sherry_num_scales(dim, hidden, down_granularity, down_group), up_granularity,
                   group_sbs_of(up_granularity, up_group), down_granularity, group_sbs_of(down_granularity, down_group),
                   static_cast<const uint16_t*>(residual), reinterpret_cast<MoeRoute*>(ws),
-                  reinterpret_cast<float*>(ws + p.logits_offset), reinterpret_cast<__bf16*>(ws + p.h_offset), p.h_plane,
+                  reinterpret_cast<float*>(ws + p.logits_offset), 0, reinterpret_cast<__bf16*>(ws + p.h_offset), p.h_plane,
                   reinterpret_cast<float*>(ws + p.partial_offset), 0};
   return hip_status(launch_moe(p, a, y, y_dtype == SHERRY_BF16, static_cast<hipStream_t>(stream)));
 }

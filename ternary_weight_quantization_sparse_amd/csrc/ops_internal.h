@@ -236,6 +236,7 @@ hipError_t launch_linear_gemm(const GemmPlan& p, const LinearArgs& a, const uint
 
 // ---------------------------------------------------------------- mixture of experts
 constexpr int kMoeExperts = 512, kMoeTopK = 16, kMoeShared = 4;
+constexpr int kMoeParts = 8;                            // of the channels, in a launch for the logits
 constexpr int kMoeSlots = 16 * kMoeTopK + kMoeShared;   // experts in use at most
 struct MoeRoute {
   int count;                         // experts in use
@@ -258,7 +259,8 @@ struct MoeArgs {
   int up_gran, up_group_sbs, down_gran, down_group_sbs;
   const uint16_t* residual;
   MoeRoute* route;
-  float* logits;                               // [tokens, experts], more than 64 of them
+  float* logits;                               // [parts][tokens, experts]
+  int parts;                                   // 0: the routing makes them itself
   __bf16* h;                                   // [2][tokens, slots, hidden]
   int64_t h_plane;
   float* partial;                              // [ranges][tokens, dim]
@@ -267,10 +269,11 @@ struct MoeArgs {
 struct MoePlan {
   int used;                                    // experts in use at most
   int ranges;                                  // of the second products
+  int parts;                                   // of the logits' channels
   int64_t h_plane;
   size_t logits_offset, h_offset, partial_offset, workspace_bytes;
 };
-MoePlan plan_moe(int tokens, int64_t dim, int64_t hidden, int experts, int shared, int top_k);
+MoePlan plan_moe(int tokens, int64_t dim, int64_t hidden, int experts, int shared, int top_k, bool router_bf16);
 hipError_t launch_moe(const MoePlan& p, MoeArgs a, void* y, bool y_bf16, hipStream_t s);
 
 }  // namespace sherry
