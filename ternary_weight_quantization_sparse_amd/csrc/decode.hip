@@ -38,10 +38,6 @@ __device__ inline Planes planes(const uint8_t* packed, const float* alpha, int64
 __device__ inline __amdgpu_buffer_rsrc_t buffer(const void* p, uint32_t bytes) {
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), (short)0, (int)bytes, kBufferWord3);
 }
-#ifndef SHERRY_STREAM
-#define SHERRY_STREAM 0
-#endif
-constexpr int kStream = SHERRY_STREAM;
 constexpr uint32_t kNowhere = 1u << 31; // an offset outside every buffer here: reads zeros, without traffic
 
 struct Block {   // one superblock's slices of the planes and scales
@@ -71,8 +67,8 @@ struct Records {
   __device__ void load(const Block& b, const uint32_t (&row)[TR], uint32_t row_step, int q) {
 #pragma unroll
     for (int i = 0; i < TR; ++i) {
-      nib[i] = __builtin_amdgcn_raw_buffer_load_b32(b.nib, row[i] * 16u + q * 4u, 0, kStream);
-      sgn[i] = __builtin_amdgcn_raw_buffer_load_b32(b.sgn, row[i] * 4u, 0, kStream);
+      nib[i] = __builtin_amdgcn_raw_buffer_load_b32(b.nib, row[i] * 16u + q * 4u, 0, 0);
+      sgn[i] = __builtin_amdgcn_raw_buffer_load_b32(b.sgn, row[i] * 4u, 0, 0);
       al[i] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(b.al, row[i] * row_step, 0, 0));
     }
   }
@@ -90,8 +86,8 @@ struct Records<4> {
   u32x4 nib;
   uint32_t sgn, al;
   __device__ void load(const Block& b, const uint32_t (&row)[1], uint32_t row_step, int) {
-    nib = __builtin_amdgcn_raw_buffer_load_b128(b.nib, row[0] * 16u, 0, kStream);
-    sgn = __builtin_amdgcn_raw_buffer_load_b32(b.sgn, row[0] * 4u, 0, kStream);
+    nib = __builtin_amdgcn_raw_buffer_load_b128(b.nib, row[0] * 16u, 0, 0);
+    sgn = __builtin_amdgcn_raw_buffer_load_b32(b.sgn, row[0] * 4u, 0, 0);
     al = __builtin_amdgcn_raw_buffer_load_b32(b.al, row[0] * row_step, 0, 0);
   }
   // halves, and odd with even rows of 16 lanes, change places
@@ -654,17 +650,7 @@ __global__ __launch_bounds__(64 * WAVES) void moe_up(MoeArgs a) {
 // Second products, weighted and added over the experts in use: TR row tiles of y, one of gridDim.y
 // ranges of the (expert, superblock) items; the waves share a range evenly.  A token's row of the A operand is its h of
 // the expert at hand, or zeros.  Several ranges leave fp32 partials for moe_join.
-#ifndef SHERRY_ROUTE_BYTES
-#define SHERRY_ROUTE_BYTES 65536   // router and tokens that the routing's one workgroup reads itself
-#endif
-#ifndef SHERRY_WIDE
-#define SHERRY_WIDE 256
-#endif
-#ifndef SHERRY_DOWN
-#define SHERRY_DOWN 4, 8, 2, 1
-#endif
-constexpr int kDown[4] = {SHERRY_DOWN};
-constexpr int kDownTiles = kDown[0], kDownWaves = kDown[1], kDownRing = kDown[2], kDownXRing = kDown[3];
+constexpr int kDownTiles = 4, kDownWaves = 8, kDownRing = 2, kDownXRing = 1;
 __device__ inline void store_moe(const MoeArgs& a, int64_t to, float s, void* y, bool y_bf16) {
   if (a.residual) s += bf16_to_f32(a.residual[to]);
   if (y_bf16) static_cast<__bf16*>(y)[to] = (__bf16)s;
@@ -718,16 +704,19 @@ __global__ __launch_bounds__(64 * kDownWaves) void moe_down(MoeArgs a, void* __r
 #pragma unroll
   for (int i = 0; i < TR; ++i) part[wave][i][lane] = acc[i];
   __syncthreads();
+  const int64_t size = (int64_t)a.tokens * a.dim;
+  float* mine = a.partial + (int64_t)blockIdx.y * size;
   for (int o = tid; o < a.tokens * 16 * TR; o += 64 * kDownWaves) {
     const int token = o / (16 * TR), c = o % (16 * TR);
-    float s = 0.f;
-#pragma unroll
-    for (int w = 0; w < kDownWaves; ++w) s += part[w][c / 16][(token >> 2) * 16 + c % 16][token & 3];
+    const float s = wave_sums<TR, kDownWaves>(part, c / 16, token, c % 16);
     const int64_t to = (int64_t)token * a.dim + col0 + c;
     if (gridDim.y == 1) store_moe(a, to, s, y, y_bf16);
-    else a.partial[(int64_t)blockIdx.y * a.tokens * a.dim + to] = s;
+    else mine[to] = s;
   }
 }
+// The ranges' partials, added in their order.  A launch of its own: letting the last range of each row block do it
+// (a count that the routing clears) costs a write-back of the L2 (8 to 19 us), or saves 2 us of 22 with stores past
+// the L2 whose order rests on a wait alone.
 __global__ __launch_bounds__(256) void moe_join(MoeArgs a, void* __restrict__ y, bool y_bf16) {
   const int64_t size = (int64_t)a.tokens * a.dim, to = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (to >= size) return;
@@ -755,8 +744,9 @@ __global__ __launch_bounds__(256) void moe_join(MoeArgs a, void* __restrict__ y,
     else if ((SBS) <= 64) RUN(16, 4);   \
     else RUN(16, 0);                    \
   } while (0)
-// 64 weight rows a workgroup where that leaves work for every CU; 16 (32: gate and values) where it does not.
-bool wide_tiles(int64_t blocks64) { return blocks64 >= SHERRY_WIDE; }
+// 64 weight rows a workgroup where that leaves work for every CU (16 x 16384 x 2048 gated: 5.7 us, with 16 + 16 rows 7.7);
+// 16 (16 + 16: gate and values) where it does not (1 x 2048 x 2048: 3.8 us in 128 workgroups).
+bool wide_tiles(int64_t blocks64) { return blocks64 >= 256; }
 
 hipError_t launch_linear_decode(const LinearArgs& a, const uint16_t* x, int tokens, void* y, bool y_bf16,
                                 hipStream_t s) {
@@ -779,7 +769,12 @@ hipError_t launch_linear_decode(const LinearArgs& a, const uint16_t* x, int toke
   return hipGetLastError();
 }
 
-// Ranges of the second products: about two items a wave, and at most 512 workgroups.
+// Router and tokens that the routing's one workgroup reads itself (64 KB: 5.4 us; 320 KB took 15.5 against 3.5 + 5.9
+// with the logits in a launch of their own).
+constexpr int64_t kRouteBytes = 65536;
+
+// Ranges of the second products: one up to 64 items (8 a wave: 23.4 us a call against 27.1 with a launch more; 2 tokens, 2
+// of 16 experts of 1024 x 2048), otherwise about two items a wave, and at most 512 workgroups.
 MoePlan plan_moe(int tokens, int64_t dim, int64_t hidden, int experts, int shared, int top_k, bool router_bf16) {
   auto up = [](size_t b) { return (b + 255) & ~(size_t)255; };
   const int slots = top_k + shared;
@@ -787,11 +782,11 @@ MoePlan plan_moe(int tokens, int64_t dim, int64_t hidden, int experts, int share
   p.used = std::min(experts, tokens * top_k) + shared;
   const int64_t items = p.used * (hidden / kSuperblock);
   const int64_t blocks = dim / (16 * kDownTiles);
-  p.ranges = (int)std::max<int64_t>(1, std::min((items + 2 * kDownWaves - 1) / (2 * kDownWaves), (512 + blocks - 1) / blocks));
+  p.ranges = items <= 64 ? 1 : (int)std::max<int64_t>(1, std::min((items + 2 * kDownWaves - 1) / (2 * kDownWaves), (512 + blocks - 1) / blocks));
   p.h_plane = (int64_t)tokens * slots * hidden;
   p.logits_offset = up(sizeof(MoeRoute));
   const int64_t read = (experts * (router_bf16 ? 2 : 4) + tokens * 2) * dim;
-  p.parts = experts <= 64 && read <= SHERRY_ROUTE_BYTES ? 0 : (int)std::min<int64_t>(kMoeParts, (dim + 511) / 512);
+  p.parts = experts <= 64 && read <= kRouteBytes ? 0 : (int)std::min<int64_t>(kMoeParts, (dim + 511) / 512);
   p.h_offset = p.logits_offset + up((size_t)p.parts * tokens * experts * 4);
   p.partial_offset = p.h_offset + up((size_t)p.h_plane * 4);
   p.workspace_bytes = p.partial_offset + (p.ranges > 1 ? up((size_t)p.ranges * tokens * dim * 4) : 0);

@@ -37,36 +37,37 @@ def _indexes(t, name, shape, dev):
 
 def _rows(t, vocab):
     """[..., V] as rows of V consecutive elements: (tensor, rows, elements from one row to the next)."""
+    if t.is_contiguous():
+        return t, t.numel() // vocab, vocab
     flat = t.reshape(-1, vocab) if t.dim() != 2 else t
     rows, stride = flat.shape[0], flat.stride(0)
     if vocab > 1 and flat.stride(1) != 1 or rows > 1 and stride < vocab:   # (broadcast rows too)
-        flat = flat.contiguous()
-        stride = vocab
+        return flat.contiguous(), rows, vocab
     return flat, rows, (stride if rows > 1 else vocab)
 
 
-def _operands(logits, ids, labels):
+def _layout(logits, ids, labels):
     """(vocab, leading shape, slots, dtype code, int64 ids, int64 labels) of checked operands."""
-    _need_gpu(logits, "logits")
-    if logits.dim() < 1 or logits.shape[-1] < 1:
-        raise ValueError(f"logits must be [..., V], got {tuple(logits.shape)}")
-    dev, lead, vocab = logits.device, logits.shape[:-1], logits.shape[-1]
+    dev, shape = logits.device, logits.shape
+    if not shape or shape[-1] < 1:
+        raise ValueError(f"logits must be [..., V], got {tuple(shape)}")
+    code = _floats(logits, "logits", shape, dev)
     _need_current(dev)
-    code = _floats(logits, "logits", logits.shape, dev)
-    if ids.dim() != len(lead) + 1 or ids.shape[-1] < 1:
+    lead = shape[:-1]
+    if ids.dim() != len(shape) or ids.shape[-1] < 1:
         raise ValueError(f"ids must be {[*lead]} + [slots], got {tuple(ids.shape)}")
     slots = ids.shape[-1]
     ids_64 = _indexes(ids, "ids", (*lead, slots), dev)
-    return vocab, lead, slots, code, ids_64, 0 if labels is None else _indexes(labels, "labels", lead, dev)
+    return shape[-1], lead, slots, code, ids_64, 0 if labels is None else _indexes(labels, "labels", lead, dev)
 
 
 def _contiguous(t):
     return t if t is None or t.is_contiguous() else t.contiguous()
 
 
-def _forward(logits, teacher, ids, temperature, teacher_lse, labels, kd_weight, want_stats, stream):
+def _forward(layout, logits, teacher, ids, temperature, teacher_lse, labels, kd_weight, want_stats, stream):
+    vocab, lead, slots, code, ids_64, labels_64 = layout
     torch = _torch()
-    vocab, lead, slots, code, ids_64, labels_64 = _operands(logits, ids, labels)
     dev = logits.device
     t_code = _floats(teacher, "teacher", ids.shape, dev)
     if teacher_lse is not None and (teacher_lse.dtype != torch.float32 or teacher_lse.shape != lead
@@ -74,7 +75,7 @@ def _forward(logits, teacher, ids, temperature, teacher_lse, labels, kd_weight, 
         _need_gpu(teacher_lse, "teacher_lse", dev)
         raise ValueError(f"teacher_lse must be float32 {tuple(lead)}, got {teacher_lse.dtype} {tuple(teacher_lse.shape)}")
     flat, rows, stride = _rows(logits, vocab)
-    teacher, ids, teacher_lse, labels = (_contiguous(t) for t in (teacher, ids, teacher_lse, labels))
+    teacher, ids, teacher_lse, labels = _contiguous(teacher), _contiguous(ids), _contiguous(teacher_lse), _contiguous(labels)
     loss = torch.empty(lead, dtype=torch.float32, device=dev)
     stats = torch.empty((rows, 4 + slots), dtype=torch.float32, device=dev) if want_stats else None
     if rows:
@@ -83,27 +84,17 @@ def _forward(logits, teacher, ids, temperature, teacher_lse, labels, kd_weight, 
         ws = torch.empty(nbytes if nbytes != (1 << 64) - 1 else 0, dtype=torch.uint8, device=dev)
         check(lib.sherry_distill_loss(rows, vocab, flat.data_ptr(), stride, code, teacher.data_ptr(), t_code,
                                       ids.data_ptr(), ids_64, slots, temperature, _ptr(teacher_lse), _ptr(labels),
-                                      labels_64, kd_weight, loss.data_ptr(), _ptr(stats), ws.data_ptr(), ws.numel(),
+                                      labels_64, kd_weight, loss.data_ptr(), _ptr(stats), ws.data_ptr(), nbytes,
                                       _stream(stream)))
     return loss, stats
 
 
-def _backward(g, logits, ids, stats, temperature, labels, kd_weight, out, stream):
-    torch = _torch()
-    vocab, lead, slots, code, ids_64, labels_64 = _operands(logits, ids, labels)
-    dev = logits.device
-    if g.dtype != torch.float32 or g.shape != lead or g.device != dev:
-        _need_gpu(g, "g", dev)
-        raise ValueError(f"g must be float32 {tuple(lead)}, got {g.dtype} {tuple(g.shape)}")
+def _backward(layout, g, logits, ids, stats, temperature, labels, kd_weight, out, stream):
+    """The gradient of checked operands."""
+    vocab, _, slots, code, ids_64, labels_64 = layout
     flat, rows, stride = _rows(logits, vocab)
-    if stats.dtype != torch.float32 or stats.shape != (rows, 4 + slots) or not stats.is_contiguous() \
-            or stats.device != dev:
-        raise ValueError(f"stats must be those of the forward pass, float32 {(rows, 4 + slots)}")
     if out is None:
-        out = torch.empty(logits.shape, dtype=logits.dtype, device=dev)
-    elif out.dtype != logits.dtype or out.shape != logits.shape or out.device != dev:
-        _need_gpu(out, "out", dev)
-        raise ValueError(f"out must be {logits.dtype} {tuple(logits.shape)}, got {out.dtype} {tuple(out.shape)}")
+        out = _torch().empty(logits.shape, dtype=logits.dtype, device=logits.device)
     place, _, out_stride = _rows(out, vocab)
     if place.data_ptr() != out.data_ptr():
         raise ValueError("out must have rows of consecutive elements at one distance")
@@ -125,9 +116,14 @@ def distill_loss(logits, teacher, ids, temperature: float = 1.0, teacher_lse=Non
     (None: p is normalised over the slots).  ``labels`` [...] (int32 or int64; outside [0, V): none) with the weight
     1 - kd_weight.  A row without slots and label has the loss 0.  J is at most 1024.
     ``with_stats``: (loss, what `distill_loss_backward` needs)."""
-    with _on_stream(stream):
-        loss, stats = _forward(logits, teacher, ids, temperature, teacher_lse, labels, kd_weight, with_stats, stream)
-    return (loss, stats) if with_stats else loss
+    if stream is None:
+        out = _forward(_layout(logits, ids, labels), logits, teacher, ids, temperature, teacher_lse, labels, kd_weight,
+                       with_stats, None)
+    else:
+        with _on_stream(stream):
+            out = _forward(_layout(logits, ids, labels), logits, teacher, ids, temperature, teacher_lse, labels,
+                           kd_weight, with_stats, stream)
+    return out if with_stats else out[0]
 
 
 def distill_loss_backward(g, logits, ids, stats, temperature: float = 1.0, labels=None, kd_weight: float = 1.0,
@@ -136,7 +132,20 @@ def distill_loss_backward(g, logits, ids, stats, temperature: float = 1.0, label
     of the forward pass with the same arguments.  ``out`` may be ``logits``.  A row whose g is 0 gets zeros, whatever
     it holds."""
     with _on_stream(stream):
-        return _backward(g, logits, ids, stats, temperature, labels, kd_weight, out, stream)
+        layout = _layout(logits, ids, labels)
+        torch, dev, lead, slots = _torch(), logits.device, layout[1], layout[2]
+        if g.dtype != torch.float32 or g.shape != lead or g.device != dev:
+            _need_gpu(g, "g", dev)
+            raise ValueError(f"g must be float32 {tuple(lead)}, got {g.dtype} {tuple(g.shape)}")
+        rows = logits.numel() // layout[0]
+        if stats.dtype != torch.float32 or stats.shape != (rows, 4 + slots) or not stats.is_contiguous() \
+                or stats.device != dev:
+            _need_gpu(stats, "stats", dev)
+            raise ValueError(f"stats must be those of the forward pass, float32 {(rows, 4 + slots)}")
+        if out is not None and (out.dtype != logits.dtype or out.shape != logits.shape or out.device != dev):
+            _need_gpu(out, "out", dev)
+            raise ValueError(f"out must be {logits.dtype} {tuple(logits.shape)}, got {out.dtype} {tuple(out.shape)}")
+        return _backward(layout, g, logits, ids, stats, temperature, labels, kd_weight, out, stream)
 
 
 def _make_ad():
@@ -159,17 +168,20 @@ def _make_ad():
 
         @staticmethod
         def forward(ctx, logits, teacher, ids, temperature, teacher_lse, labels, kd_weight):
-            loss, stats = _forward(logits, teacher, ids, temperature, teacher_lse, labels, kd_weight, True, None)
+            layout = _layout(logits, ids, labels)
+            loss, stats = _forward(layout, logits, teacher, ids, temperature, teacher_lse, labels, kd_weight, True, None)
             ctx.save_for_backward(logits, ids, stats, labels)
-            ctx.args = temperature, kd_weight
+            ctx.args = layout, temperature, kd_weight
             return loss
 
         @staticmethod
         def backward(ctx, g):
             logits, ids, stats, labels = ctx.saved_tensors
-            temperature, kd_weight = ctx.args
+            layout, temperature, kd_weight = ctx.args
+            _need_current(logits.device)
             grad = Gradient.apply if torch.is_grad_enabled() else _backward   # create_graph, or not
-            return (grad(g, logits, ids, stats, temperature, labels, kd_weight, None, None),) + (None,) * 6
+            return grad(layout, g, logits, ids, stats, temperature, labels, kd_weight, None, None), None, None, None, \
+                None, None, None
 
     return DistillLoss
 

@@ -14,6 +14,13 @@ from . import _gran, _lib, _need_current, _need_gpu, _on_stream, _stream, _torch
 from ._lib import check, load
 
 _NONE = (1 << 64) - 1
+_BF16_OUT = None
+
+
+def _bf16_out():
+    global _BF16_OUT
+    _BF16_OUT = _torch().bfloat16, _lib.BF16
+    return _BF16_OUT
 
 
 def _planes(packed, alpha, n, k, granularity, group_size, count, dev, name=""):
@@ -115,10 +122,11 @@ def linear_gemv(pw, x, bias=None, activation: str = "none", gated: bool = False,
     ``bias`` [N] fp32 or bf16; ``activation`` none, relu, relu2 (squared), silu, gelu or gelu_tanh; ``gated``: the
     weight's rows are [gate; values] and y is [B, N/2]; ``residual`` bf16 of y's shape.  ``out`` may be ``residual``
     (the residual stream updated in place)."""
-    return _on(stream, pw, x, bias, activation, gated, residual, res_scale, True, _y_dtype(y_dtype), out)
+    kind = _BF16_OUT if y_dtype == "bfloat16" else _y_dtype(y_dtype)
+    return _on(stream, pw, x, bias, activation, gated, residual, res_scale, True, kind or _bf16_out(), out)
 
 
 def linear_gemm(pw, x, bias=None, activation: str = "none", gated: bool = False, residual=None, res_scale: float = 1.0,
                 stream=None, out=None):
     """The same for prefill activations ``x`` [M, K] bf16 -> bf16 [M, N or N/2], on MFMA."""
-    return _on(stream, pw, x, bias, activation, gated, residual, res_scale, False, (_torch().bfloat16, _lib.BF16), out)
+    return _on(stream, pw, x, bias, activation, gated, residual, res_scale, False, _BF16_OUT or _bf16_out(), out)
