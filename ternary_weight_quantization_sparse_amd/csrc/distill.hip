@@ -12,7 +12,8 @@
 //
 // HBM bounds both directions: the forward pass reads the logits once (running
 // maximum and sums), the backward pass reads them once more and writes the
-// gradient.  Everything that belongs to a row (sums over threads, logarithms,
+// gradient: 2048 x 128000 bf16 with 64 slots 102 us (5.1 TB/s) + 12 us (the rows' losses) and 180 to 208 us (5.0 to 5.8 TB/s), 300 us
+// together; three passes at a copy's 5.13 TB/s take 307.  Everything that belongs to a row (sums over threads, logarithms,
 // the teacher's probabilities) is in 64 bits: the loss is a difference of
 // terms of its own size or larger.
 #include <algorithm>
@@ -63,7 +64,12 @@ struct RowGroups {
     groups = (mis + vocab + kLane<BF16> - 1) / kLane<BF16>;
   }
   __device__ bool whole(int64_t g) const { return g * kLane<BF16> >= mis && (g + 1) * kLane<BF16> <= mis + vocab; }
-  __device__ u32x4 raw(int64_t g) const { return *reinterpret_cast<const u32x4*>(base + g * 16); }
+  template <bool STREAM>
+  __device__ u32x4 raw(int64_t g) const {
+    const u32x4* p = reinterpret_cast<const u32x4*>(base + g * 16);
+    if constexpr (STREAM) return __builtin_nontemporal_load(p);
+    else return *p;
+  }
   __device__ static void unpack(const u32x4 r, float (&x)[kLane<BF16>]) {
     if constexpr (BF16) {
 #pragma unroll
@@ -114,7 +120,7 @@ __device__ inline double wave_max(double v) {
 // m).  A thread rescales its sums when its maximum rises, once per four
 // groups; threads and waves join in 64 bits.  The maximum starts at the
 // lowest finite value, so that ranges of -infinity add zeros.
-template <bool BF16, bool TAIL, bool SOFT1>
+template <bool BF16, bool TAIL, bool SOFT1, bool STREAM>
 __global__ __launch_bounds__(kThreads) void distill_range(DistillArgs a, int64_t row0) {
   constexpr int L = kLane<BF16>, kAhead = 4;
   extern __shared__ uint32_t marks[];
@@ -187,7 +193,7 @@ __global__ __launch_bounds__(kThreads) void distill_range(DistillArgs a, int64_t
     u32x4 r[kAhead];
 #pragma unroll
     for (int u = 0; u < kAhead; ++u)
-      if (g + u * kThreads < w1) r[u] = v.raw(g + u * kThreads);
+      if (g + u * kThreads < w1) r[u] = v.template raw<STREAM>(g + u * kThreads);
     float x[kAhead][L], top = -FLT_MAX;
 #pragma unroll
     for (int u = 0; u < kAhead; ++u)
@@ -354,7 +360,7 @@ __global__ __launch_bounds__(64) void distill_finish(DistillArgs a, int64_t row0
 // before the range is written, so that the gradient may take the logits'
 // place.  An id in several slots takes the sum of its slots' probabilities in
 // slot order, whichever slot writes it.
-template <bool BF16, bool SOFT1>
+template <bool BF16, bool SOFT1, bool STREAM>
 __global__ __launch_bounds__(kThreads) void distill_grad(DistillGrad a, int64_t row0) {
   constexpr int L = kLane<BF16>, kAhead = 4;
   __shared__ int32_t ids[kDistillSlots];
@@ -436,7 +442,8 @@ __global__ __launch_bounds__(kThreads) void distill_grad(DistillGrad a, int64_t 
 #pragma unroll
         for (int i = 0; i < 4; ++i) o[i] = __float_as_uint(r[i]);
       }
-      *reinterpret_cast<u32x4*>(ob + g * 16) = o;
+      if constexpr (STREAM) __builtin_nontemporal_store(o, reinterpret_cast<u32x4*>(ob + g * 16));
+      else *reinterpret_cast<u32x4*>(ob + g * 16) = o;
     } else {
 #pragma unroll
       for (int i = 0; i < L; ++i) {
@@ -459,7 +466,7 @@ __global__ __launch_bounds__(kThreads) void distill_grad(DistillGrad a, int64_t 
     u32x4 r[kAhead];
 #pragma unroll
     for (int u = 0; u < kAhead; ++u)
-      if (g + u * kThreads < w1) r[u] = v.raw(g + u * kThreads);
+      if (g + u * kThreads < w1) r[u] = v.template raw<STREAM>(g + u * kThreads);
 #pragma unroll
     for (int u = 0; u < kAhead; ++u)
       if (g + u * kThreads < w1) {
@@ -477,20 +484,26 @@ __global__ __launch_bounds__(kThreads) void distill_grad(DistillGrad a, int64_t 
   if (label_here) store_one<BF16>(a.out, first + label, label_fix);
 }
 
+// Logits that the last-level cache (256 MB) cannot keep from one pass to the next are streamed past it, and so are their
+// gradients: 2048 x 128000 bf16, both directions, 332 -> 302 us.  Smaller ones find them there (333 x 50001
+// fp32: 123 us a call by itself, streamed 138).
+bool streams(int64_t rows, int64_t vocab, bool bf16) { return rows * vocab * (bf16 ? 2 : 4) > (int64_t)192 << 20; }
+
 // Rows of a launch: at most 2^22 workgroups (2^30 threads).
 int64_t rows_of_launch(int ranges) { return std::max<int64_t>(1, ((int64_t)1 << 22) / ranges); }
 
 }  // namespace
 
 // Ranges of a row: about 2048 workgroups, at least 4096 elements each (16 a
-// thread), at most 2^18 (the bitmap's 32 KB).  A range is whole groups; one
+// thread; 4096 and 8192 workgroups took as long), at most 2^18 (the bitmap's 32 KB); backward 16384 elements (8192
+// as long, 32768 and 65536 5% longer).  A range is whole groups; one
 // group more than the row's own covers a row that begins inside a group.
 DistillSplit plan_distill(int64_t rows, int64_t vocab, bool bf16, bool backward) {
   const int64_t lane = bf16 ? 8 : 4, groups = (vocab + lane - 1) / lane + 1;
   DistillSplit p{};
   int64_t ranges;
   if (backward) {
-    ranges = (vocab + 16383) / 16384;
+    ranges = (vocab + 16384 - 1) / 16384;
   } else {
     ranges = std::min<int64_t>((2048 + rows - 1) / rows, (vocab + 4095) / 4096);
     ranges = std::max<int64_t>(ranges, (groups * lane + (1 << 18) - 1) >> 18);
@@ -506,8 +519,13 @@ hipError_t launch_distill(const DistillArgs& a, int64_t rows, bool bf16, bool te
   const bool tail = a.teacher_lse != nullptr, soft1 = a.labels && a.inv_t != 1.;
   const size_t lds = tail ? (size_t)((a.range_groups * (bf16 ? 8 : 4) + 31) / 32) * 4 : 0;
   const int64_t step = rows_of_launch(a.ranges);
-#define SHERRY_RANGE(B, T, S) \
-  hipLaunchKernelGGL((distill_range<B, T, S>), dim3((unsigned)(n * a.ranges)), dim3(kThreads), lds, s, a, r0)
+  const bool stream = streams(rows, a.vocab, bf16);
+#define SHERRY_RANGE(B, T, S)                                                                                             \
+  do {                                                                                                                    \
+    const dim3 grid((unsigned)(n * a.ranges));                                                                            \
+    if (stream) hipLaunchKernelGGL((distill_range<B, T, S, true>), grid, dim3(kThreads), lds, s, a, r0);                  \
+    else hipLaunchKernelGGL((distill_range<B, T, S, false>), grid, dim3(kThreads), lds, s, a, r0);                        \
+  } while (0)
 #define SHERRY_RANGE_T(B)                 \
   do {                                    \
     if (tail && soft1) SHERRY_RANGE(B, true, true);  \
@@ -538,14 +556,20 @@ hipError_t launch_distill(const DistillArgs& a, int64_t rows, bool bf16, bool te
 }
 
 hipError_t launch_distill_backward(const DistillGrad& a, int64_t rows, bool bf16, hipStream_t s) {
-  const bool soft1 = a.labels && a.inv_t != 1.;
+  const bool soft1 = a.labels && a.inv_t != 1., stream = streams(rows, a.vocab, bf16);
   const int64_t step = rows_of_launch(a.ranges);
   for (int64_t r0 = 0; r0 < rows; r0 += step) {
     const dim3 grid((unsigned)(std::min(step, rows - r0) * a.ranges));
-    if (bf16 && soft1) hipLaunchKernelGGL((distill_grad<true, true>), grid, dim3(kThreads), 0, s, a, r0);
-    else if (bf16) hipLaunchKernelGGL((distill_grad<true, false>), grid, dim3(kThreads), 0, s, a, r0);
-    else if (soft1) hipLaunchKernelGGL((distill_grad<false, true>), grid, dim3(kThreads), 0, s, a, r0);
-    else hipLaunchKernelGGL((distill_grad<false, false>), grid, dim3(kThreads), 0, s, a, r0);
+#define SHERRY_GRAD(B, S)                                                                                    \
+  do {                                                                                                       \
+    if (stream) hipLaunchKernelGGL((distill_grad<B, S, true>), grid, dim3(kThreads), 0, s, a, r0);           \
+    else hipLaunchKernelGGL((distill_grad<B, S, false>), grid, dim3(kThreads), 0, s, a, r0);                 \
+  } while (0)
+    if (bf16 && soft1) SHERRY_GRAD(true, true);
+    else if (bf16) SHERRY_GRAD(true, false);
+    else if (soft1) SHERRY_GRAD(false, true);
+    else SHERRY_GRAD(false, false);
+#undef SHERRY_GRAD
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
