@@ -962,6 +962,21 @@ hipError_t launch_gemm_adapted(const GemmPlan& p, int64_t n, int64_t k, int gran
 #undef SHERRY_GEMM_LAUNCH
 }
 
+// Splits of the product with an epilogue, whose finishing pass costs more: past one workgroup a CU only while a split
+// keeps 8 superblocks (one split more of 4 took 22.6 us against 20.7 at 517 x 2048 x 2048 and 19.1 against 14.4 at 1024 x 512 x
+// 2048; of 16, 33.4 against 39.6 at 517 x 2048 x 8192).  Never more than the product's own.
+GemmPlan plan_linear(int64_t n, int64_t k, int gran, int group_size, int64_t m) {
+  GemmPlan p = plan_gemm(n, k, gran, group_size, m, true);
+  if (p.splits == 1) return p;
+  const int64_t chunk = gemm_chunk_rows(k), mc = chunk > 0 && m > chunk ? chunk : m, nsb = k / kSuperblock;
+  const int64_t tiles = (mc + p.tile_m - 1) / p.tile_m * ((n + p.tile_n - 1) / p.tile_n);
+  int splits = 1;
+  while (splits < p.splits && (tiles * splits < 256 || nsb / (2 * splits) >= 8)) splits *= 2;
+  p.splits = splits;
+  p.workspace_bytes = splits > 1 ? (size_t)splits * (size_t)mc * (size_t)n * sizeof(float) : 0;
+  return p;
+}
+
 hipError_t launch_linear_gemm(const GemmPlan& p, const LinearArgs& a, const uint16_t* x, int64_t m, uint16_t* y,
                               float* ws, hipStream_t s) {
 #define SHERRY_GEMM_LAUNCH(G, TN)                                   \

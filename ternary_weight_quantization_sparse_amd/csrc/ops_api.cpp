@@ -386,7 +386,7 @@ int32_t sherry_linear_gemm(int64_t n, int64_t k, int32_t granularity, int32_t gr
                               activation, gated, residual, res_scale);
   if (st != SHERRY_OK) return st;
   if (!aligned16(y) || !multiple_of(residual, 8)) return SHERRY_ERR_ALIGN;
-  const GemmPlan plan = plan_gemm(n, k, granularity, group_size, m, true);
+  const GemmPlan plan = plan_linear(n, k, granularity, group_size, m);
   if (plan.workspace_bytes > 0 && (!workspace || workspace_bytes < plan.workspace_bytes)) return SHERRY_ERR_WORKSPACE;
   if (plan.workspace_bytes > 0 && !aligned16(workspace)) return SHERRY_ERR_ALIGN;
   const LinearArgs a{static_cast<const uint8_t*>(packed), alpha, n, k, granularity, group_sbs_of(granularity, group_size),
