@@ -90,15 +90,15 @@ def _moe(x, router, up, down, top_k, shared, scoring, normalize, bias, scale, ac
         bias = bias if bias.is_contiguous() else bias.contiguous()
     if residual is not None:
         residual = _rows(residual, "residual", (m, dim), dev)
-    ydt, y_code = _y_dtype(y_dtype)
-    y = _place(out, ydt, (m, dim), dev)
+    ydt, y_code = (x.dtype, _lib.BF16) if y_dtype == "bfloat16" else _y_dtype(y_dtype)
+    y = _place(out, ydt, (m, dim), dev, x)
     lib = load()
     nbytes = lib.sherry_moe_workspace_bytes(m, dim, hidden, experts, shared, top_k)
-    ws = torch.empty(nbytes if nbytes != (1 << 64) - 1 else 0, dtype=torch.uint8, device=dev)
+    ws = x.new_empty(nbytes if nbytes != (1 << 64) - 1 else 0, dtype=torch.uint8)
     check(lib.sherry_moe_decode(
         m, dim, hidden, x.data_ptr(), router.data_ptr(), r_code, experts, shared, top_k, _lib.SCORING[scoring],
         bool(normalize), None if bias is None else bias.data_ptr(), scale, _activation(activation), up.n != hidden,
         up.packed.data_ptr(), up.alpha.data_ptr(), up_gran, up.group_size, down.packed.data_ptr(),
         down.alpha.data_ptr(), down_gran, down.group_size, None if residual is None else residual.data_ptr(),
-        y.data_ptr(), y_code, ws.data_ptr(), ws.numel(), _stream(stream)))
+        y.data_ptr(), y_code, ws.data_ptr(), nbytes, _stream(stream)))
     return y

@@ -26,14 +26,21 @@ def _bf16_out():
 def _planes(packed, alpha, n, k, granularity, group_size, count, dev, name=""):
     """Checks the planes and scales of ``count`` packed weights [n, k]; their granularity's code."""
     torch = _torch()
-    gran = _gran(granularity)
+    gran = _lib.GRANULARITY.get(granularity)
+    if gran is None:
+        gran = _gran(granularity)
     if n < 1 or k < 1 or (gran == _lib.PER_GROUP and group_size < 1):
         raise ValueError(f"{name}packed weight [{n}, {k}], group size {group_size}: not a shape")
-    scales = {_lib.PER_TENSOR: 1, _lib.PER_CHANNEL: n}.get(gran, n * (k // group_size) if group_size > 0 else 0)
-    for t, what, dtype, size in ((packed, "packed", torch.uint8, n * k // 32 * 5), (alpha, "alpha", torch.float32, scales)):
-        if t.dtype != dtype or t.device != dev or not t.is_contiguous() or t.numel() < count * size:
-            _need_gpu(t, name + what, dev)
-            raise ValueError(f"{name}{what} must be a contiguous {dtype} tensor of {count} x {size} elements")
+    nbytes = n * k // 32 * 5
+    scales = n * (k // group_size) if gran == _lib.PER_GROUP else n if gran == _lib.PER_CHANNEL else 1
+    if packed.dtype != torch.uint8 or packed.device != dev or not packed.is_contiguous() \
+            or packed.numel() < count * nbytes:
+        _need_gpu(packed, name + "packed", dev)
+        raise ValueError(f"{name}packed must be a contiguous uint8 tensor of {count} x {nbytes} bytes")
+    if alpha.dtype != torch.float32 or alpha.device != dev or not alpha.is_contiguous() \
+            or alpha.numel() < count * scales:
+        _need_gpu(alpha, name + "alpha", dev)
+        raise ValueError(f"{name}alpha must be a contiguous float32 tensor of {count} x {scales} scales")
     return gran
 
 
@@ -53,10 +60,10 @@ def _rows(t, name, shape, dev):
     return t if t.is_contiguous() else t.contiguous()
 
 
-def _place(out, dtype, shape, dev):
-    """The caller's output, or a new one."""
+def _place(out, dtype, shape, dev, like):
+    """The caller's output, or a new one (of ``like``'s type if that is it: half the time)."""
     if out is None:
-        return _torch().empty(shape, dtype=dtype, device=dev)
+        return like.new_empty(shape) if dtype is like.dtype else _torch().empty(shape, dtype=dtype, device=dev)
     if out.dtype != dtype or out.shape != shape or out.device != dev or not out.is_contiguous():
         _need_gpu(out, "out", dev)
         raise ValueError(f"out must be contiguous {dtype} {tuple(shape)}, got {out.dtype} {tuple(out.shape)}")
@@ -79,7 +86,7 @@ def _linear(pw, x, bias, activation, gated, residual, res_scale, decode, y_dtype
         residual = residual if residual is None or residual.dim() != 1 else residual.unsqueeze(0)
     m, outs = x.shape[0] if x.dim() == 2 else -1, n // 2 if gated else n
     x = _rows(x, "x", (m, k), dev)
-    y = _place(out, y_dtype[0], (m, outs), dev)
+    y = _place(out, y_dtype[0], (m, outs), dev, x)
     res = None
     if residual is not None:
         residual = _rows(residual, "residual", (m, outs), dev)
