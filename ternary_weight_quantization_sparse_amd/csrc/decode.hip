@@ -650,7 +650,7 @@ __global__ __launch_bounds__(64 * WAVES) void moe_up(MoeArgs a) {
 // Second products, weighted and added over the experts in use: TR row tiles of y, one of gridDim.y
 // ranges of the (expert, superblock) items; the waves share a range evenly.  A token's row of the A operand is its h of
 // the expert at hand, or zeros.  Several ranges leave fp32 partials for moe_join.
-constexpr int kDownTiles = 4, kDownWaves = 8, kDownRing = 2, kDownXRing = 1;
+constexpr int kDownTiles = 4, kDownWaves = 8, kDownRing = 1, kDownXRing = 1;
 __device__ inline void store_moe(const MoeArgs& a, int64_t to, float s, void* y, bool y_bf16) {
   if (a.residual) s += bf16_to_f32(a.residual[to]);
   if (y_bf16) static_cast<__bf16*>(y)[to] = (__bf16)s;
