@@ -154,7 +154,7 @@ size_t sherry_distill_workspace_bytes(int64_t rows, int64_t vocab, int32_t dtype
  *            -infinity) has kd = 0; where the ids are the whole vocabulary, rest is 0.
  *   teacher_lse [rows] fp32: log of the sum of exp(u / t) over the teacher's whole vocabulary.
  *   labels   [rows] int32 (labels_64: int64) or NULL; outside [0, vocab): no label, the second term is 0.
- *   loss     [rows] fp32.  stats [rows, 4 + slots] fp32 for the backward pass, or NULL.
+ *   loss     [rows] fp32.  stats [rows, 6 + slots] fp32 for the backward pass, or NULL.
  *   A kd_weight of 0 (1) leaves the first (second) term out, whatever it is.
  *   rows 1 .. 2^31 - 1, vocab 1 .. 2^30, slots 1 .. 1024, temperature 1e-3 .. 1e3; pointers need
  *   their element's alignment (16-byte aligned rows are not needed for 16-byte loads).  Sums and logarithms of a

@@ -38,7 +38,7 @@ __device__ inline Planes planes(const uint8_t* packed, const float* alpha, int64
 __device__ inline __amdgpu_buffer_rsrc_t buffer(const void* p, uint32_t bytes) {
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), (short)0, (int)bytes, kBufferWord3);
 }
-constexpr uint32_t kNowhere = 1u << 31; // an offset outside every buffer here: reads zeros, without traffic
+constexpr uint32_t kNowhere = 1u << 31;   // an offset outside every buffer here: reads zeros, without traffic
 
 struct Block {   // one superblock's slices of the planes and scales
   __amdgpu_buffer_rsrc_t nib, sgn, al;
@@ -197,7 +197,7 @@ __device__ inline void run_items(int j0, int j1, const char* dtab, int q, R reco
 
 // One output tile of a packed weight: TR row tiles (GATED: half gate rows, half the same outputs' rows of the
 // weight's second half).  The waves split K; a wave issues all its loads at once where it has up to XS superblocks (0: more,
-// through a ring), and the waves join through LDS: sums(which, token, column) afterwards adds them in order.  Short
+// through a ring), and the waves join through LDS: wave_sums adds them in order.  Short
 // workgroups, eight waves a SIMD, hide the latency better than ones that walk several tiles and load
 // ahead (mixture of experts, 16 tokens, 56 experts of 2048 x 2048: 18 us against 20 to 25).
 template <int TR, int WAVES, bool GATED, int XS>
@@ -287,47 +287,6 @@ __global__ __launch_bounds__(64 * WAVES) void linear_decode(LinearArgs a, const 
     if (y_bf16) static_cast<__bf16*>(y)[to] = (__bf16)z;
     else static_cast<float*>(y)[to] = z;
   }
-}
-
-// ------------------------------------------------------------ linear, 1..16 tokens
-template <int TR, int WAVES, bool GATED, int XS, int AHEAD>
-__global__ __launch_bounds__(64 * WAVES) void linear_decode(LinearArgs a, const uint16_t* __restrict__ x, int tokens,
-                                                            void* __restrict__ y, bool y_bf16) {
-  static_assert(!GATED || TR % 2 == 0, "a gate tile and its other half");
-  constexpr int kOut = GATED ? TR / 2 : TR;   // output tiles
-  __shared__ __attribute__((aligned(16))) uint2 dtab[32];
-  __shared__ f32x4 part[AHEAD == 1 ? 1 : 2][WAVES][TR][64];
-  const int tid = threadIdx.x, lane = tid & 63, r = lane & 15, q = lane >> 4;
-  if (tid < 32) dtab[tid] = decode_bf16(tid);
-  const int64_t outs = GATED ? a.n / 2 : a.n;
-  const Planes p = planes(a.packed, a.alpha, a.n, a.k, a.gran, a.group_sbs);
-  const int tiles = (int)((outs + 16 * kOut - 1) / (16 * kOut));
-  // consecutive workgroups land on different XCDs: give each XCD neighbouring tiles
-  const int xcd = blockIdx.x & 7, share = gridDim.x >> 3, more = gridDim.x & 7;
-  const int64_t group = xcd * share + min(xcd, more) + (blockIdx.x >> 3);
-  const uint32_t x_lane = r < tokens ? (uint32_t)(r * a.k + 8 * q) * 2u : kNowhere;
-  __syncthreads();
-  walk_tiles<TR, WAVES, GATED, XS, AHEAD>(
-      p, outs, (int)(a.k / kSuperblock), buffer(x, (uint32_t)(tokens * a.k * 2)), x_lane,
-      (int)((int64_t)tiles * group / gridDim.x), (int)((int64_t)tiles * (group + 1) / gridDim.x), reinterpret_cast<const char*>(dtab), part, [&](int tile, auto sums) {
-        for (int o = tid; o < tokens * 16 * kOut; o += 64 * WAVES) {
-          const int token = o / (16 * kOut), which = o / 16 % kOut, c = o % 16;
-          const int64_t col = (int64_t)tile * (16 * kOut) + which * 16 + c;
-          if (col >= outs) continue;
-          float z = sums(which, token, c);
-          if (a.bias) z += load_float(a.bias, col, a.bias_bf16);
-          z = activate(z, a.activation);
-          if constexpr (GATED) {
-            float u = sums(kOut + which, token, c);
-            if (a.bias) u += load_float(a.bias, outs + col, a.bias_bf16);
-            z *= u;
-          }
-          const int64_t to = (int64_t)token * outs + col;
-          if (a.residual) z += a.res_scale * bf16_to_f32(a.residual[to]);
-          if (y_bf16) static_cast<__bf16*>(y)[to] = (__bf16)z;
-          else static_cast<float*>(y)[to] = z;
-        }
-      });
 }
 
 // ------------------------------------------------------------ mixture of experts
@@ -573,6 +532,12 @@ __global__ __launch_bounds__(64 * kRouteWaves) void moe_route(MoeArgs a) {
       w = expf(l - top) / wave_sumf(sum);
     } else {
       w = 1.f / (1.f + expf(-l));
+    }
+    if (a.softmax) {   // a logit that is not a number leaves no softmax
+      bool bad = false;
+#pragma unroll
+      for (int i = 0; i < R; ++i) bad = bad || k.logit[i] != k.logit[i];
+      if (__any(bad)) w = NAN;
     }
     if (lane < a.top_k) {
       chosen[wave][lane] = mine;

@@ -28,7 +28,7 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kThreads = 256;
-constexpr int kStatHead = 4;   // a row's statistics: the maximum and three factors, then its slots
+constexpr int kStatHead = kDistillHead;   // a row's statistics before its slots
 
 template <bool BF16> constexpr int kLane = BF16 ? 8 : 4;   // elements of 16 bytes
 
@@ -114,10 +114,10 @@ __device__ inline double wave_max(double v) {
 }
 
 // ------------------------------------------------------------------- forward
-// One range of a row: its maximum m, sum of exp((s - m) / t) (TAIL: over the
-// elements outside the ids, which a bitmap of the range marks in LDS, so that
-// the tail is never a difference of sums), and with SOFT1 the sum of exp(s -
-// m).  A thread rescales its sums when its maximum rises, once per four
+// One range of a row: its maximum m, sum of exp((s - m) / t) and with SOFT1 the
+// sum of exp(s - m).  TAIL: of the elements outside the ids, which a bitmap of
+// the range marks in LDS; so the tail is never a difference of sums, and it has a maximum of its own, however
+// far below the ids it lies.  A thread rescales its sums when its maximum rises, once per four
 // groups; threads and waves join in 64 bits.  The maximum starts at the
 // lowest finite value, so that ranges of -infinity add zeros.
 template <bool BF16, bool TAIL, bool SOFT1, bool STREAM>
@@ -150,17 +150,18 @@ __global__ __launch_bounds__(kThreads) void distill_range(DistillArgs a, int64_t
   // log2(e) / t in two terms: rounded to one, every exponential of a far element would be off the same way
   const float c = a.exp_hi, c_lo = a.exp_lo;
   float m = -FLT_MAX, s = 0.f, s1 = 0.f;
-  auto add = [&](const float (&x)[L], int64_t g) {
-    uint32_t mark = 0;
+  auto drop_marked = [&](float (&x)[L], int64_t g) {
     if constexpr (TAIL) {
-      const uint32_t p = (uint32_t)((g - g0) * L);
-      mark = marks[p >> 5] >> (p & 31);
+      const uint32_t p = (uint32_t)((g - g0) * L), mark = marks[p >> 5] >> (p & 31);
+#pragma unroll
+      for (int i = 0; i < L; ++i) x[i] = (mark >> i) & 1u ? -INFINITY : x[i];
     }
+  };
+  auto add = [&](const float (&x)[L]) {
 #pragma unroll
     for (int i = 0; i < L; ++i) {
       const float d = x[i] - m;
-      const float e = __builtin_amdgcn_exp2f(fmaf(d, c, d * c_lo));
-      s += TAIL && ((mark >> i) & 1u) ? 0.f : e;
+      s += __builtin_amdgcn_exp2f(fmaf(d, c, d * c_lo));
       if constexpr (SOFT1) s1 += __builtin_amdgcn_exp2f(d * kLog2e);
     }
   };
@@ -185,8 +186,9 @@ __global__ __launch_bounds__(kThreads) void distill_range(DistillArgs a, int64_t
     if (tid == 0 ? w0 > g0 : w1 < g1) {
       float x[L];
       v.edge(g, x);
+      drop_marked(x, g);
       raise(peak(x));
-      add(x, g);
+      add(x);
     }
   }
   for (int64_t g = w0 + tid; g < w1; g += kAhead * kThreads) {
@@ -199,12 +201,13 @@ __global__ __launch_bounds__(kThreads) void distill_range(DistillArgs a, int64_t
     for (int u = 0; u < kAhead; ++u)
       if (g + u * kThreads < w1) {
         v.unpack(r[u], x[u]);
+        drop_marked(x[u], g + u * kThreads);
         top = fmaxf(top, peak(x[u]));
       }
     raise(top);
 #pragma unroll
     for (int u = 0; u < kAhead; ++u)
-      if (g + u * kThreads < w1) add(x[u], g + u * kThreads);
+      if (g + u * kThreads < w1) add(x[u]);
   }
   const float wmax = wave_max(m);
   const double sum = wave_sum((double)s * (double)__builtin_amdgcn_exp2f((m - wmax) * c));
@@ -229,8 +232,9 @@ __global__ __launch_bounds__(kThreads) void distill_range(DistillArgs a, int64_t
   }
 }
 
-// A row's loss and, for the backward pass, its maximum, the factors of
-// exp((s - m) / t) at the ids and elsewhere, that of exp(s - m), and each
+// A row's loss and, for the backward pass, two references and the factors of
+// the exponentials below them (m: off exp((s - m) / t) + c1 exp(s - m) for the
+// elements outside the ids; top: at and c2 for those at the ids), then each
 // slot's probability; all with the weights and the temperature in them.  One
 // wave a row: ranges, then slots, 64 at a time.
 template <bool BF16, bool T_BF16>
@@ -296,23 +300,34 @@ __global__ __launch_bounds__(64) void distill_finish(DistillArgs a, int64_t row0
   }
   __syncthreads();
 
-  // student: the ids' exponentials join the sum (TAIL left them out), an id
-  // that stands in several slots once
-  double inside = 0., cross = 0.;
+  // student: the ids' exponentials join the sums (TAIL left them out), an id
+  // that stands in several slots once; the larger of both maxima is the reference
+  auto logit = [&](int64_t id) { return (double)load_one<BF16>(a.logits, row * a.stride + id); };
+  double top_s = (double)m, cross = 0.;
   int distinct = 0;
-  for (int j = lane; j < a.slots; j += 64) {
-    if (ids[j] < 0) continue;
-    bool first = true;
-    if (twice)
-      for (int i = 0; i < j; ++i) first = first && ids[i] != ids[j];
-    if (first) {
-      ++distinct;
-      inside += exp(((double)load_one<BF16>(a.logits, row * a.stride + ids[j]) - (double)m) * inv_t);
-    }
-  }
-  const double left = s;
   if (tail) {
-    s += wave_sum(inside);
+    for (int j = lane; j < a.slots; j += 64)
+      if (ids[j] >= 0) top_s = fmax(top_s, logit(ids[j]));
+    top_s = wave_max(top_s);
+  }
+  const double below = (double)m - top_s, left = s;
+  s *= exp(below * inv_t);
+  s1 *= exp(below);
+  if (tail) {
+    double in_t = 0., in_1 = 0.;
+    for (int j = lane; j < a.slots; j += 64) {
+      if (ids[j] < 0) continue;
+      bool first = true;
+      if (twice)
+        for (int i = 0; i < j; ++i) first = first && ids[i] != ids[j];
+      if (!first) continue;
+      ++distinct;
+      const double d = logit(ids[j]) - top_s;
+      in_t += exp(d * inv_t);
+      in_1 += exp(d);
+    }
+    s += wave_sum(in_t);
+    s1 += wave_sum(in_1);
 #pragma unroll
     for (int o = 32; o > 0; o >>= 1) distinct += __shfl_xor(distinct, o);
     if (distinct == a.vocab) rest = 0.;   // nothing is outside the ids
@@ -321,41 +336,40 @@ __global__ __launch_bounds__(64) void distill_finish(DistillArgs a, int64_t row0
   for (int j = lane; j < a.slots; j += 64) {
     const double u = prob[j];
     const double p = u == -inf || !teach ? 0. : exp(u - ref) * norm;
-    if (p != 0. && ids[j] >= 0) {
-      const double logq = ((double)load_one<BF16>(a.logits, row * a.stride + ids[j]) - (double)m) * inv_t - logs;
-      cross += p * (u - ref - lognorm - logq);
-    }
+    if (p != 0. && ids[j] >= 0) cross += p * (u - ref - lognorm - ((logit(ids[j]) - top_s) * inv_t - logs));
     prob[j] = p;
   }
   cross = wave_sum(cross);
-  if (rest != 0.) cross += rest * (log(rest) - log(left / s));
+  if (rest != 0.) cross += rest * (log(rest) - (log(left) + below * inv_t - logs));
   const double w = a.kd_weight, t = 1. / inv_t;
   double loss = w == 0. ? 0. : w * t * t * cross;
-  const double one = a.inv_t == 1. ? s : s1;   // the sum of exp(s - m)
+  const double one = a.inv_t == 1. ? s : s1;   // the sum of exp(s - top_s)
   const double hard = has_label ? 1. - w : 0.;
-  if (hard != 0.) loss += hard * (log(one) - ((double)load_one<BF16>(a.logits, row * a.stride + label) - (double)m));
+  if (hard != 0.) loss += hard * (log(one) - (logit(label) - top_s));
   if (lane == 0) a.loss[row] = (float)loss;
   if (!a.stats) return;
   float* st = a.stats + row * (kStatHead + a.slots);
   if (lane == 0) {
-    const double soft = w * t, all = soft * (mass + rest) == 0. ? 0. : soft * (mass + rest) / s;
-    const double out = soft * rest == 0. || left == 0. ? 0. : soft * rest / left;
-    double at = all, off = all - out, c1 = hard == 0. ? 0. : hard / one;
+    const double soft = w * t, all = w == 0. || mass + rest == 0. ? 0. : soft * (mass + rest) / s;
+    const double out = w == 0. || rest == 0. || left == 0. ? 0. : soft * rest / left;
+    double at = all, off = all * exp(below * inv_t) - out, c2 = hard == 0. ? 0. : hard / one, c1 = c2 * exp(below);
     if (a.inv_t == 1.) {
-      at += c1;
+      at += c2;
       off += c1;
-      c1 = 0.;
+      c1 = c2 = 0.;
     }
     st[0] = m;
-    st[1] = (float)at;
-    st[2] = (float)off;
-    st[3] = (float)c1;
+    st[1] = (float)off;
+    st[2] = (float)c1;
+    st[3] = (float)top_s;
+    st[4] = (float)at;
+    st[5] = (float)c2;
   }
   for (int j = lane; j < a.slots; j += 64) st[kStatHead + j] = w == 0. ? 0.f : (float)(w * t * prob[j]);
 }
 
 // ------------------------------------------------------------------ backward
-// One range of a row: gradient = g (off exp((s - m) / t) + c1 exp(s - m)),
+// One range of a row: gradient = g (off exp((s - m) / t) + c1 exp(s - m)) of the statistics,
 // then the elements at the ids and the label over it.  Those values are made
 // before the range is written, so that the gradient may take the logits'
 // place.  An id in several slots takes the sum of its slots' probabilities in
@@ -391,11 +405,11 @@ __global__ __launch_bounds__(kThreads) void distill_grad(DistillGrad a, int64_t 
     return;
   }
   const float* st = a.stats + row * (kStatHead + a.slots);
-  const float m = st[0], at = st[1] * gr, off = st[2] * gr, c1 = st[3] * gr;
-  auto value = [&](float x, float f) {
-    const float d = x - m;
+  const float m = st[0], off = st[1] * gr, c1 = st[2] * gr, top = st[3], at = st[4] * gr, c2 = st[5] * gr;
+  auto value = [&](float x, float reference, float f, float f1) {
+    const float d = x - reference;
     float r = f == 0.f ? 0.f : f * __builtin_amdgcn_exp2f(fmaf(d, a.exp_hi, d * a.exp_lo));
-    if constexpr (SOFT1) r += c1 == 0.f ? 0.f : c1 * __builtin_amdgcn_exp2f(d * kLog2e);
+    if constexpr (SOFT1) r += f1 == 0.f ? 0.f : f1 * __builtin_amdgcn_exp2f(d * kLog2e);
     return r;
   };
 
@@ -416,21 +430,21 @@ __global__ __launch_bounds__(kThreads) void distill_grad(DistillGrad a, int64_t 
     if (j >= a.slots || ids[j] < 0) continue;
     float p = 0.f;
     for (int i = 0; i < a.slots; ++i) p += ids[i] == ids[j] ? prob[i] : 0.f;
-    fix[u] = value(load_one<BF16>(a.logits, row * a.stride + ids[j]), at) - p * gr - (ids[j] == label ? hard : 0.f);
+    fix[u] = value(load_one<BF16>(a.logits, row * a.stride + ids[j]), top, at, c2) - p * gr - (ids[j] == label ? hard : 0.f);
   }
   float label_fix = 0.f;
   bool label_here = false;
   if (tid == 0 && label >= 0) {
     label_here = true;
     for (int i = 0; i < a.slots; ++i) label_here = label_here && ids[i] != label;
-    label_fix = value(load_one<BF16>(a.logits, row * a.stride + label), off) - hard;
+    label_fix = value(load_one<BF16>(a.logits, row * a.stride + label), m, off, c1) - hard;
   }
   __syncthreads();
 
   auto store = [&](const float (&x)[L], int64_t g, bool whole) {
     float r[L];
 #pragma unroll
-    for (int i = 0; i < L; ++i) r[i] = value(x[i], off);
+    for (int i = 0; i < L; ++i) r[i] = value(x[i], m, off, c1);
     if (same && whole) {
       u32x4 o;
       if constexpr (BF16) {

@@ -139,6 +139,7 @@ int check_linear(int64_t n, int64_t k, int32_t gran, int32_t group_size, const v
   const size_t outs = (size_t)tokens * (size_t)(gated ? n / 2 : n);
   if (overlap(y, outs * item, x, (size_t)tokens * (size_t)k * 2)) return SHERRY_ERR_ARG;
   if (overlap(y, outs * item, residual, outs * 2) && !(y == residual && item == 2)) return SHERRY_ERR_ARG;
+  if (overlap(y, outs * item, bias, (size_t)n * (bias_dtype == SHERRY_F32 ? 4 : 2))) return SHERRY_ERR_ARG;
   return SHERRY_OK;
 }
 

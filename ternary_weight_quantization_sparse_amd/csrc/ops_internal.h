@@ -171,6 +171,7 @@ hipError_t launch_muon(const MuonPlan& p, const MuonArgs& a, bool bf16, char* ws
 
 // ---------------------------------------------------------------- distillation
 constexpr int kDistillSlots = 1024;   // teacher slots a row
+constexpr int kDistillHead = 6;       // floats of a row's statistics before its slots
 struct DistillRange {
   double s, s1;      // sums of exp((s - m) / t) and exp(s - m)
   float m;

@@ -18,6 +18,9 @@ from . import _lib, _need_current, _need_gpu, _on_stream, _ptr, _stream, _torch
 from ._lib import check, load
 
 
+_HEAD = 6     # floats of a row's statistics before its slots
+
+
 def _floats(t, name, shape, dev):
     torch = _torch()
     _need_gpu(t, name, dev)
@@ -77,7 +80,7 @@ def _forward(layout, logits, teacher, ids, temperature, teacher_lse, labels, kd_
     flat, rows, stride = _rows(logits, vocab)
     teacher, ids, teacher_lse, labels = _contiguous(teacher), _contiguous(ids), _contiguous(teacher_lse), _contiguous(labels)
     loss = torch.empty(lead, dtype=torch.float32, device=dev)
-    stats = torch.empty((rows, 4 + slots), dtype=torch.float32, device=dev) if want_stats else None
+    stats = torch.empty((rows, _HEAD + slots), dtype=torch.float32, device=dev) if want_stats else None
     if rows:
         lib = load()
         nbytes = lib.sherry_distill_workspace_bytes(rows, vocab, code)
@@ -138,10 +141,10 @@ def distill_loss_backward(g, logits, ids, stats, temperature: float = 1.0, label
             _need_gpu(g, "g", dev)
             raise ValueError(f"g must be float32 {tuple(lead)}, got {g.dtype} {tuple(g.shape)}")
         rows = logits.numel() // layout[0]
-        if stats.dtype != torch.float32 or stats.shape != (rows, 4 + slots) or not stats.is_contiguous() \
+        if stats.dtype != torch.float32 or stats.shape != (rows, _HEAD + slots) or not stats.is_contiguous() \
                 or stats.device != dev:
             _need_gpu(stats, "stats", dev)
-            raise ValueError(f"stats must be those of the forward pass, float32 {(rows, 4 + slots)}")
+            raise ValueError(f"stats must be those of the forward pass, float32 {(rows, _HEAD + slots)}")
         if out is not None and (out.dtype != logits.dtype or out.shape != logits.shape or out.device != dev):
             _need_gpu(out, "out", dev)
             raise ValueError(f"out must be {logits.dtype} {tuple(logits.shape)}, got {out.dtype} {tuple(out.shape)}")

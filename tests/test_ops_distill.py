@@ -76,9 +76,11 @@ def oracle(z, u, ids, lse, y, tau, w, g):
         G.index_add_(0, at, -p)
         G2.index_add_(0, at, p)
         if rest > 0:
-            logr = torch.logsumexp(logq[outside], 0)
+            # (from the logits: at 1e30 a log of q has steps of 1e14, in which the tail's own differences are lost)
+            away = (z[r] / tau).masked_fill(~outside, -float("inf"))
+            logr = torch.logsumexp(away, 0) - torch.logsumexp(z[r] / tau, 0)
             kd = kd + rest * (torch.log(torch.tensor(rest, dtype=F64)) - logr)
-            tail = torch.where(outside, rest * torch.exp(logq - logr), 0.)
+            tail = rest * torch.softmax(away, 0)
             G, G2 = G - tail, G2 + tail
         if w != 0 and (len(at) or rest > 0):
             loss[r] += w * tau ** 2 * kd
@@ -190,6 +192,38 @@ def test_masked_vocabulary(fill, dtype):
     z[1, ids[1, 0].long()] = float("-inf")
     loss, stats = S.distill_loss(z, u, ids, with_stats=True)
     assert loss[1] == float("inf") and torch.isfinite(loss[[0, 2, 3, 4]]).all()
+
+
+@pytest.mark.parametrize("gap", [50.0, 300.0, 1e4, 1e30])
+@pytest.mark.parametrize("tau", [1.0, 2.0])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_a_tail_far_below_the_ids(gap, tau, dtype):
+    """The student's mass outside the ids is what fp32 exponentials below the largest logit cannot hold."""
+    z, u, ids, lse, y = make(5, 2000, 6, dtype, True, True, tau=tau)
+    far = torch.ones_like(z, dtype=torch.bool).scatter(1, ids.long(), False)
+    z[far] -= gap
+    y[0], y[2] = int(far[0].nonzero()[0]), ids[2, 1]
+    loss, grad = check(z, u, ids, lse, y, tau=tau)
+    assert (loss > gap / 1e3).all() and grad.isfinite().all()
+    z[3, far[3]] = float("-inf")                 # what the student cannot say at all
+    assert S.distill_loss(z, u, ids, tau, lse)[3] == float("inf")
+
+
+def test_ids_far_below_the_tail():
+    z, u, ids, lse, y = make(4, 2000, 6, F32, True, True)
+    z.scatter_add_(1, ids.long(), torch.full(ids.shape, -500.0, device=DEV))
+    check(z, u, ids, lse, y)
+    check(z, u, ids, None, y)
+
+
+def test_a_term_of_weight_zero_is_left_out():
+    z, u, ids, lse, y = make(4, 900, 6, F32, True, True)
+    want = check(z, u, ids, lse, y, w=0.0)
+    u[1, 2], lse[2], u[3] = float("nan"), float("nan"), float("inf")
+    for tail in (lse, None):
+        loss, stats = S.distill_loss(z, u, ids, 2.0, tail, y, 0.0, with_stats=True)
+        grad = S.distill_loss_backward(torch.linspace(0.3, 1.0, 4, device=DEV), z, ids, stats, 2.0, y, 0.0)
+        assert torch.allclose(loss, want[0], rtol=2.0 ** -20) and torch.allclose(grad, want[1], rtol=2.0 ** -17, atol=1e-9)
 
 
 def test_not_a_number_stays_in_its_row():
