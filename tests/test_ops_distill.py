@@ -299,6 +299,53 @@ def test_autograd():
         S.distill_loss_ad(z, u.float().requires_grad_(True), ids)
 
 
+def test_one_row_without_its_axis():
+    z, u, ids, lse, y = make(1, 700, 5, F32, True, True)
+    loss, stats = S.distill_loss(z[0], u[0], ids[0], 2.0, lse[0], y[0], 0.7, with_stats=True)
+    grad = S.distill_loss_backward(torch.ones((), device=DEV), z[0], ids[0], stats, 2.0, y[0], 0.7)
+    want, stats = S.distill_loss(z, u, ids, 2.0, lse, y, 0.7, with_stats=True)
+    assert loss.shape == () and loss == want[0] and grad.shape == (700,)
+    assert torch.equal(grad, S.distill_loss_backward(torch.ones(1, device=DEV), z, ids, stats, 2.0, y, 0.7)[0])
+
+
+def test_more_rows_than_one_launch():
+    rows = (1 << 22) + 7
+    gen = torch.Generator(device=DEV).manual_seed(0)
+    z = torch.randn(rows, 3, generator=gen, device=DEV)
+    ids = torch.randint(0, 3, (rows, 1), generator=gen, device=DEV)
+    u = torch.zeros(rows, 1, device=DEV)
+    loss, stats = S.distill_loss(z, u, ids, with_stats=True)
+    grad = S.distill_loss_backward(torch.ones(rows, device=DEV), z, ids, stats)
+    q = z.double().softmax(1)                    # one slot has all of the teacher: cross entropy
+    want = -q.gather(1, ids).log()[:, 0]
+    assert ((loss.double() - want).abs() <= 2.0 ** -20 + 2.0 ** -24 * want).all()
+    hot = torch.zeros_like(q).scatter(1, ids, 1.0)
+    assert ((grad.double() - (q - hot)).abs() <= 2.0 ** -18 * (q + hot)).all()
+
+
+def test_refusals():
+    z, u, ids, lse, y = make(4, 300, 6, BF16, True, True)
+    g = torch.ones(4, device=DEV)
+    loss, stats = S.distill_loss(z, u, ids, 2.0, lse, y, with_stats=True)
+    for args, kw in [((z.half(), u, ids), {}), ((z, u.half(), ids), {}), ((z, u[:3], ids), {}), ((z, u, ids.float()), {}),
+                     ((z, u, ids[:, :3]), {}), ((z, u, ids[0]), {}), ((z, u.cpu(), ids), {}), ((z, u, ids.cpu()), {}),
+                     ((z, u, ids), dict(temperature=0.0)), ((z, u, ids), dict(teacher_lse=lse.double())),
+                     ((z, u, ids), dict(teacher_lse=lse[:2])), ((z, u, ids), dict(labels=y.float())),
+                     ((z, u, ids), dict(labels=y[:2])), ((z, u, ids), dict(kd_weight=float("nan"))),
+                     ((z, u[:, :0], ids[:, :0]), {}), ((z[:, :0], u, ids), {})]:
+        with pytest.raises(ValueError):
+            S.distill_loss(*args, **kw)
+    for args, kw in [((g.double(), z, ids, stats), {}), ((g[:2], z, ids, stats), {}), ((g, z, ids, stats[:, :5]), {}),
+                     ((g, z, ids, stats[:2]), {}), ((g, z, ids, stats.double()), {}), ((g, z, ids, stats.cpu()), {}),
+                     ((g, z, ids, stats), dict(out=z.float())), ((g, z, ids, stats), dict(out=z[:2])),
+                     ((g, z, ids, stats), dict(out=z.t().contiguous().t())), ((g.cpu(), z, ids, stats), {})]:
+        with pytest.raises(ValueError):
+            S.distill_loss_backward(*args, temperature=2.0, labels=y, **kw)
+    store = torch.zeros(4 * 300 + 8, dtype=BF16, device=DEV)     # over the logits, but not in their place
+    with pytest.raises(ValueError):
+        S.distill_loss_backward(g, store[:1200].view(4, 300), ids, stats, 2.0, out=store[8:].view(4, 300))
+
+
 def test_no_rows():
     z = torch.zeros(0, 100, device=DEV, requires_grad=True)
     loss = S.distill_loss_ad(z, torch.zeros(0, 4, device=DEV), torch.zeros(0, 4, dtype=torch.int32, device=DEV))

@@ -115,6 +115,33 @@ def test_sizes(dim, hidden, tokens, grain, group):
     Layer(5, dim, hidden, 1, grain, group).check(tokens, 2)
 
 
+@pytest.mark.parametrize("dim", [512, 1024, 2048, 4096, 8192, 8320])
+@pytest.mark.parametrize("gated", [False, True])
+def test_wide_tiles(dim, gated):
+    """64 weight rows a workgroup (4 tokens may use 32 experts), at every count of superblocks a wave."""
+    Layer(36, dim, 512, gated=gated).check(4, 8)
+
+
+def test_long_hidden():
+    Layer(3, 256, 8320, 1).check(2, 2)
+    Layer(3, 8320, 8320).check(1, 1)
+
+
+def test_a_router_row_that_is_not_a_number():
+    layer = Layer(9, 256, 128, 1)
+    x, res = layer.tokens(3)
+    layer.router[4, 7] = float("nan")
+    for normalize in (True, False):
+        y = S.moe_decode(x, layer.router, layer.up, layer.down, 2, shared=1, normalize=normalize, residual=res)
+        assert y.isnan().all()                   # no softmax without it
+    y = S.moe_decode(x, layer.router, layer.up, layer.down, 2, shared=1, scoring="sigmoid", residual=res)
+    layer.router[4, 7] = 0                       # a sigmoid for each: the others are chosen before it
+    off = torch.zeros(9, device=DEV)
+    off[4] = -INF
+    want, tol = layer.oracle(x, 2, "sigmoid", True, off, 1.0, "silu", res, margin=False)
+    close(y, want, tol)
+
+
 @pytest.mark.parametrize("activation", ["none", "relu", "relu2", "silu", "gelu", "gelu_tanh"])
 @pytest.mark.parametrize("gated", [False, True])
 def test_activations(activation, gated):

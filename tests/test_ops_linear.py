@@ -135,6 +135,26 @@ def test_wide_tiles():
         check(pw, x, b, "relu2", False, res)
 
 
+@pytest.mark.parametrize("k", [512, 1024, 2048, 4096, 8192, 12416])
+@pytest.mark.parametrize("gated", [False, True])
+def test_decode_tiles(k, gated):
+    """64 weight rows a workgroup and 16, at every count of superblocks a wave, ragged."""
+    for tokens, n in ((5, 16390), (16, 70), (1, 1030)):
+        pw, x, b, res = make(tokens, n, k, bias="bfloat16", gated=gated)
+        check(pw, x, b, "silu", gated, res)
+
+
+def test_prompts_in_several_launches():
+    """Rows past one launch's address range (3968 of them at K = 2^18)."""
+    n, k, tokens = 32, 1 << 18, 4100
+    pw, x, b, res = make(tokens, n, k, "per_channel", gated=True)
+    y = S.linear_gemm(pw, x, bias=b, activation="silu", gated=True, residual=res, res_scale=0.8)
+    dense = S.unpack(pw, "float32")
+    rows = [0, 63, 3967, 3968, 4031, 4032, 4099]
+    want, tol = oracle(dense, x[rows], b, "silu", True, res[rows], 0.8)
+    close(y[rows], want, tol)
+
+
 def test_no_epilogue_is_the_product():
     for tokens in (1, 16, 400):
         pw, x, _, _ = make(tokens, 512, 1024, bias=None, residual=False)
