@@ -738,8 +738,9 @@ hipError_t launch_linear_decode(const LinearArgs& a, const uint16_t* x, int toke
 // with the logits in a launch of their own).
 constexpr int64_t kRouteBytes = 65536;
 
-// Ranges of the second products: one up to 64 items (8 a wave: 23.4 us a call against 27.1 with a launch more; 2 tokens, 2
-// of 16 experts of 1024 x 2048), otherwise about two items a wave, and at most 512 workgroups.
+// Ranges of the second products: one up to 32 items (4 a wave: a launch less, the same time in a graph), otherwise about
+// two items a wave, and at most 512 workgroups (1 token, 8 of 64 experts of 2048 x 1024, 64 items: 20.4 us in a graph, in
+// one range 26.4; called from Python 28.6 and 26.5).
 MoePlan plan_moe(int tokens, int64_t dim, int64_t hidden, int experts, int shared, int top_k, bool router_bf16) {
   auto up = [](size_t b) { return (b + 255) & ~(size_t)255; };
   const int slots = top_k + shared;
@@ -747,7 +748,7 @@ MoePlan plan_moe(int tokens, int64_t dim, int64_t hidden, int experts, int share
   p.used = std::min(experts, tokens * top_k) + shared;
   const int64_t items = p.used * (hidden / kSuperblock);
   const int64_t blocks = dim / (16 * kDownTiles);
-  p.ranges = items <= 64 ? 1 : (int)std::max<int64_t>(1, std::min((items + 2 * kDownWaves - 1) / (2 * kDownWaves), (512 + blocks - 1) / blocks));
+  p.ranges = items <= 32 ? 1 : (int)std::max<int64_t>(1, std::min((items + 2 * kDownWaves - 1) / (2 * kDownWaves), (512 + blocks - 1) / blocks));
   p.h_plane = (int64_t)tokens * slots * hidden;
   p.logits_offset = up(sizeof(MoeRoute));
   const int64_t read = (experts * (router_bf16 ? 2 : 4) + tokens * 2) * dim;
