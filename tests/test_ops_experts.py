@@ -224,6 +224,25 @@ def test_tokens_do_not_meet():
     close(y[others], want, tol)
 
 
+@pytest.mark.parametrize("value", [INF, float("nan")])
+@pytest.mark.parametrize("hidden", [256, 1024])
+def test_an_expert_that_is_not_finite_reaches_its_own_tokens_alone(value, hidden):
+    """Another expert's scales change nothing of a token's sums, so the others' results stay the same bit for bit."""
+    layer = Layer(8, 256, hidden)
+    x, res, clean = layer.check(9, 2)
+    logits = x.double() @ layer.router.double().t().contiguous()
+    chosen = torch.zeros_like(logits).scatter_(1, logits.topk(2, 1).indices, 1)
+    e = int(chosen.sum(0).sub(4.5).abs().argmin())          # some take it, some do not
+    takes = chosen[:, e] > 0
+    assert takes.any() and not takes.all()
+    for planes in (layer.up, layer.down):
+        kept = planes.alpha[e].clone()
+        planes.alpha[e] = value
+        y = S.moe_decode(x, layer.router, layer.up, layer.down, 2, residual=res)
+        planes.alpha[e] = kept
+        assert torch.equal(y[~takes], clean[~takes]) and not y[takes].isfinite().any()
+
+
 def test_one_expert_for_all_and_all_experts():
     layer = Layer(64, 256, 128)
     x, res = layer.tokens(16)

@@ -259,3 +259,16 @@ def test_refusals():
         S.linear_gemm(short, x)
     with pytest.raises(ValueError, match="alpha"):
         S.linear_gemm(S.PackedWeight(pw.packed, pw.alpha[:-1], 64, 256), x)
+
+
+@pytest.mark.parametrize("grain", ["per_group", "per_channel", "per_tensor"])
+@pytest.mark.parametrize("n,k", [(40, 128), (40, 640), (40, 1152), (20000, 640)])
+def test_a_scale_that_is_infinite_stays_so(n, k, grain):
+    """Waves without a superblock of their own add nothing.  The sums of a superblock are far from zero: x is one
+    there, and each row's weights have one sign."""
+    gen = torch.Generator(device=DEV).manual_seed(n + k)
+    sign = torch.where(torch.arange(n, device=DEV) % 3 == 0, -1.0, 1.0)[:, None]
+    pw = S.quantize_pack(rand(gen, n, k).abs() * sign, grain, 128)
+    pw.alpha.fill_(INF)
+    y = S.linear_gemv(pw, torch.ones(2, k, dtype=BF16, device=DEV))
+    assert torch.equal(y, (sign[:, 0] * INF).to(BF16).expand(2, -1))
