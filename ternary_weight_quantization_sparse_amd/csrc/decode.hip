@@ -310,29 +310,33 @@ __device__ inline uint32_t order(float f) {
 }
 constexpr uint32_t kOff = 1u;
 
-template <int CTRL>
-__device__ inline uint32_t dpp_max(uint32_t v) {
-  return max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, false));
+// Reductions over a wave (the result in every lane): within rows of 16 lanes, then across them.
+template <int CTRL, typename F>
+__device__ inline uint32_t dpp_step(uint32_t v, uint32_t none, F f) {
+  return f(v, (uint32_t)__builtin_amdgcn_update_dpp((int)none, (int)v, CTRL, 0xF, 0xF, false));
 }
-// The largest of a wave's values (in every lane): within rows of 16, then across them.
-__device__ inline uint32_t wave_max_u32(uint32_t v) {
-  v = dpp_max<0x111>(v);   // row_shr 1, 2, 4, 8
-  v = dpp_max<0x112>(v);
-  v = dpp_max<0x114>(v);
-  v = dpp_max<0x118>(v);
-  v = dpp_max<0x142>(v);   // row_bcast 15, 31
-  v = dpp_max<0x143>(v);
+template <typename F>
+__device__ inline uint32_t wave_reduce(uint32_t v, uint32_t none, F f) {
+  v = dpp_step<0x111>(v, none, f);   // row_shr 1, 2, 4, 8
+  v = dpp_step<0x112>(v, none, f);
+  v = dpp_step<0x114>(v, none, f);
+  v = dpp_step<0x118>(v, none, f);
+  v = dpp_step<0x142>(v, none, f);   // row_bcast 15, 31
+  v = dpp_step<0x143>(v, none, f);
   return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
 }
+__device__ inline uint32_t wave_max_u32(uint32_t v) {
+  return wave_reduce(v, 0u, [](uint32_t a, uint32_t b) { return max(a, b); });
+}
 __device__ inline float wave_maxf(float v) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor(v, o));
-  return v;
+  return __uint_as_float(wave_reduce(__float_as_uint(v), 0xFF800000u, [](uint32_t a, uint32_t b) {
+    return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
+  }));
 }
 __device__ inline float wave_sumf(float v) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
-  return v;
+  return __uint_as_float(wave_reduce(__float_as_uint(v), 0u, [](uint32_t a, uint32_t b) {
+    return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
+  }));
 }
 
 // A token's keys: lane l holds experts l, l + 64, ...  Without a bias the
@@ -397,63 +401,54 @@ __device__ inline int take_best(Keys<R>& k, int lane) {
   }
   return e;
 }
-// Router logits of TILES tiles of 16 experts on MFMA (A: the tokens, B: the router's
+// Router logits of a tile of 16 experts on MFMA (A: the tokens, B: the router's
 // rows): 32-channel steps [s0, s1), consecutive ones, so that a row's memory lines are read whole.  A float32 router goes in as
 // three bf16 terms (24 bits).
-template <bool R_BF16, int TILES>
-__device__ inline void logit_tiles(const MoeArgs& a, int tile0, int s0, int s1, int lane, f32x4 (&acc)[TILES]) {
-  constexpr int kAhead = TILES == 1 ? 4 : 2;
+template <bool R_BF16>
+__device__ inline f32x4 logit_tile(const MoeArgs& a, int tile, int s0, int s1, int lane) {
+  constexpr int kAhead = R_BF16 ? 8 : 4;
   const int r = lane & 15, q = lane >> 4;
   const uint16_t* xr = a.x + (int64_t)r * a.dim + 8 * q;
-  int64_t rr[TILES];
-#pragma unroll
-  for (int i = 0; i < TILES; ++i) {
-    rr[i] = (int64_t)min((tile0 + i) * 16 + r, a.experts - 1) * a.dim + 8 * q;
-    acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-  }
+  const int64_t rr = (int64_t)min(tile * 16 + r, a.experts - 1) * a.dim + 8 * q;
+  f32x4 acc = {0.f, 0.f, 0.f, 0.f};
   for (int s = s0; s < s1; s += kAhead) {
-    u32x4 xv[kAhead], w[kAhead][TILES][R_BF16 ? 1 : 2];
+    u32x4 xv[kAhead], w[kAhead][R_BF16 ? 1 : 2];
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
       const bool in = s + u < s1;
       xv[u] = in && r < a.tokens ? *reinterpret_cast<const u32x4*>(xr + (int64_t)(s + u) * 32) : u32x4{0u, 0u, 0u, 0u};
-#pragma unroll
-      for (int i = 0; i < TILES; ++i) {
-        const int64_t at = rr[i] + (int64_t)(s + u) * 32;
-        if constexpr (R_BF16) {
-          w[u][i][0] = in ? *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(a.router) + at) : u32x4{0u, 0u, 0u, 0u};
-        } else {
-          const u32x4* src = reinterpret_cast<const u32x4*>(static_cast<const float*>(a.router) + at);
-          w[u][i][0] = in ? src[0] : u32x4{0u, 0u, 0u, 0u};
-          w[u][i][R_BF16 ? 0 : 1] = in ? src[1] : u32x4{0u, 0u, 0u, 0u};
-        }
+      const int64_t at = rr + (int64_t)(s + u) * 32;
+      if constexpr (R_BF16) {
+        w[u][0] = in ? *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(a.router) + at) : u32x4{0u, 0u, 0u, 0u};
+      } else {
+        const u32x4* src = reinterpret_cast<const u32x4*>(static_cast<const float*>(a.router) + at);
+        w[u][0] = in ? src[0] : u32x4{0u, 0u, 0u, 0u};
+        w[u][R_BF16 ? 0 : 1] = in ? src[1] : u32x4{0u, 0u, 0u, 0u};
       }
     }
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
       if (s + u >= s1) continue;
       const bf16x8 xb = __builtin_bit_cast(bf16x8, xv[u]);
+      if constexpr (R_BF16) {
+        acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xb, __builtin_bit_cast(bf16x8, w[u][0]), acc, 0, 0, 0);
+      } else {
+        bf16x8 term[3];
 #pragma unroll
-      for (int i = 0; i < TILES; ++i) {
-        if constexpr (R_BF16) {
-          acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xb, __builtin_bit_cast(bf16x8, w[u][i][0]), acc[i], 0, 0, 0);
-        } else {
-          bf16x8 term[3];
+        for (int e = 0; e < 8; ++e) {
+          float rest = __uint_as_float(w[u][R_BF16 ? 0 : e / 4][e % 4]);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            float rest = __uint_as_float(w[u][i][R_BF16 ? 0 : e / 4][e % 4]);
-#pragma unroll
-            for (int t = 0; t < 3; ++t) {
-              term[t][e] = (__bf16)rest;
-              rest -= (float)term[t][e];
-            }
+          for (int t = 0; t < 3; ++t) {
+            term[t][e] = (__bf16)rest;
+            rest -= (float)term[t][e];
           }
-#pragma unroll
-          for (int t = 2; t >= 0; --t) acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xb, term[t], acc[i], 0, 0, 0);
         }
+#pragma unroll
+        for (int t = 2; t >= 0; --t) acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xb, term[t], acc, 0, 0, 0);
       }
     }
   }
+  return acc;
 }
 
 // Logits of many experts, in parts over the channels [part, tokens, experts]: one CU alone reads a cold router slowly (64
@@ -465,124 +460,151 @@ __global__ __launch_bounds__(64 * kLogitWaves) void moe_logits(MoeArgs a) {
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int steps = (int)(a.dim / 32), share = a.parts * kLogitWaves, mine = blockIdx.y * kLogitWaves + wave;
-  f32x4 acc[1];
-  logit_tiles<R_BF16, 1>(a, blockIdx.x, steps * mine / share, steps * (mine + 1) / share, lane, acc);
-  part[wave][0][lane] = acc[0];
+  part[wave][0][lane] = logit_tile<R_BF16>(a, blockIdx.x, steps * mine / share, steps * (mine + 1) / share, lane);
   __syncthreads();
   const int token = tid / 16, c = tid % 16, e = blockIdx.x * 16 + c;
   if (token < a.tokens && e < a.experts)
     a.logits[((int64_t)blockIdx.y * a.tokens + token) * a.experts + e] = wave_sums<1, kLogitWaves>(part, 0, token, c);
 }
 
-// The tokens' experts and weights, a token a wave, and from them the experts in use, in rising order
-// (then the shared ones), each with its place among every token's choices (-1: not chosen) and weight.
-// One workgroup; with a small router it makes the logits too (LOGITS tiles of them; 0: moe_logits did), which
-// saves a launch.
-constexpr int kRouteWaves = 16;
-template <int R, int LOGITS, bool R_BF16>
-__global__ __launch_bounds__(64 * kRouteWaves) void moe_route(MoeArgs a) {
-  static_assert(LOGITS == 0 || R == 1, "logits of up to 64 experts");
-  constexpr int kTiles = LOGITS ? LOGITS : 1;
-  __shared__ f32x4 part[LOGITS ? kRouteWaves : 1][kTiles][64];
-  __shared__ float logits[LOGITS ? 16 : 1][64];
-  __shared__ uint32_t used[kMoeExperts / 32];
-  __shared__ int list[kMoeSlots];
-  __shared__ int chosen[16][kMoeTopK];
-  __shared__ float chosen_w[16][kMoeTopK];
-  const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  if (tid < kMoeExperts / 32) used[tid] = 0u;
-  if constexpr (LOGITS != 0) {
-    const int steps = (int)(a.dim / 32);
-    f32x4 acc[kTiles];
-    logit_tiles<R_BF16, kTiles>(a, 0, steps * wave / kRouteWaves, steps * (wave + 1) / kRouteWaves, lane, acc);
+// The routing of a workgroup of WAVES waves: each token's experts and weights, a token a wave, and from them the
+// experts in use.  OWN: the logits (of up to 64 experts) are made here.
+struct Routing {
+  __attribute__((aligned(16))) int chosen[16][kMoeTopK];
+  float weight[16][kMoeTopK];
+  uint32_t used[kMoeExperts / 32];
+};
+// Logits of up to 64 experts: the waves take the tiles in turn and share the channels of each.
+template <int WAVES>
+__device__ inline void own_logits(const MoeArgs& a, f32x4 (*part)[64], float (*logits)[64], int tid, int wave) {
+  const int tiles = a.experts <= 16 ? 1 : a.experts <= 32 ? 2 : 4, shares = WAVES / tiles;
+  const int steps = (int)(a.dim / 32), tile = wave % tiles, share = wave / tiles, lane = tid & 63;
+  const int s0 = steps * share / shares, s1 = steps * (share + 1) / shares;
+  part[wave][lane] = a.router_bf16 ? logit_tile<true>(a, tile, s0, s1, lane) : logit_tile<false>(a, tile, s0, s1, lane);
+  lds_barrier();
+  for (int o = tid; o < 256 * tiles; o += 64 * WAVES) {
+    const int token = o / (16 * tiles), e = o % (16 * tiles);
+    float v[WAVES], sum = 0.f;   // (loaded together)
 #pragma unroll
-    for (int i = 0; i < kTiles; ++i) part[wave][i][lane] = acc[i];
-    __syncthreads();
-    for (int o = tid; o < 16 * 16 * kTiles; o += 64 * kRouteWaves) {
-      const int token = o / (16 * kTiles), e = o % (16 * kTiles);
-      logits[token][e] = wave_sums<kTiles, kRouteWaves>(part, e / 16, token, e % 16);
-    }
+    for (int w = 0; w < WAVES; ++w)
+      v[w] = w < shares ? part[w * tiles + e / 16][(token >> 2) * 16 + e % 16][token & 3] : 0.f;
+#pragma unroll
+    for (int w = 0; w < WAVES; ++w) sum += v[w];
+    logits[token][e] = sum;
   }
-  __syncthreads();
-  if (wave < a.tokens) {
-    Keys<R> k;
-    if constexpr (LOGITS != 0) load_keys(a, logits[wave], 1, 0, lane, k);
-    else load_keys(a, a.logits + (int64_t)wave * a.experts, a.parts, (int64_t)a.tokens * a.experts, lane, k);
-    int mine = -1;        // lane j: the j-th expert and its logit
-    float l = -INFINITY;
-    for (int j = 0; j < a.top_k; ++j) {
-      const int e = take_best(k, lane);
-      float v = -INFINITY;
-      if (e >= 0) {
-#pragma unroll
-        for (int i = 0; i < R; ++i)
-          if (i == e / 64) v = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(k.logit[i]), e & 63));
-      }
-      if (lane == j) {
-        mine = e;
-        l = v;
-      }
-    }
-    // weights by their logarithms, so that none is lost to the others' size
-    const float g = a.softmax ? l : fminf(l, 0.f) - log1pf(expf(-fabsf(l)));
-    float w;
-    if (a.normalize) {
-      const float top = wave_maxf(mine >= 0 ? g : -INFINITY);
-      w = mine >= 0 ? expf(g - top) : 0.f;
-      w /= wave_sumf(w);
-    } else if (a.softmax) {
-      float top = -INFINITY, sum = 0.f;
-#pragma unroll
-      for (int i = 0; i < R; ++i) top = fmaxf(top, k.logit[i]);
-      top = wave_maxf(top);
+}
+// One token's experts and their weights, from its keys.
+template <int R>
+__device__ inline void choose(const MoeArgs& a, Keys<R>& k, int token, int lane, Routing& to) {
+  int mine = -1;        // lane j: the j-th expert and its logit
+  float l = -INFINITY;
+  for (int j = 0; j < a.top_k; ++j) {
+    const int e = take_best(k, lane);
+    float v = -INFINITY;
+    if (e >= 0) {
 #pragma unroll
       for (int i = 0; i < R; ++i)
-        if (i * 64 + lane < a.experts) sum += expf(k.logit[i] - top);
-      w = expf(l - top) / wave_sumf(sum);
-    } else {
-      w = 1.f / (1.f + expf(-l));
+        if (i == e / 64) v = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(k.logit[i]), e & 63));
     }
-    if (a.softmax) {   // a logit that is not a number leaves no softmax
-      bool bad = false;
-#pragma unroll
-      for (int i = 0; i < R; ++i) bad = bad || k.logit[i] != k.logit[i];
-      if (__any(bad)) w = NAN;
-    }
-    if (lane < a.top_k) {
-      chosen[wave][lane] = mine;
-      chosen_w[wave][lane] = w * a.scale;
-      if (mine >= 0) atomicOr(&used[mine / 32], 1u << (mine & 31));
+    if (lane == j) {
+      mine = e;
+      l = v;
     }
   }
-  __syncthreads();
+  // weights by their logarithms, so that none is lost to the others' size
+  const float g = a.softmax ? l : fminf(l, 0.f) - log1pf(expf(-fabsf(l)));
+  float w;
+  if (a.normalize) {
+    const float top = wave_maxf(mine >= 0 ? g : -INFINITY);
+    w = mine >= 0 ? expf(g - top) : 0.f;
+    w /= wave_sumf(w);
+  } else if (a.softmax) {
+    float top = -INFINITY, sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < R; ++i) top = fmaxf(top, k.logit[i]);
+    top = wave_maxf(top);
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+      if (i * 64 + lane < a.experts) sum += expf(k.logit[i] - top);
+    w = expf(l - top) / wave_sumf(sum);
+  } else {
+    w = 1.f / (1.f + expf(-l));
+  }
+  if (a.softmax) {   // a logit that is not a number leaves no softmax
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < R; ++i) bad = bad || k.logit[i] != k.logit[i];
+    if (__any(bad)) w = NAN;
+  }
+  if (lane < a.top_k) {
+    to.chosen[token][lane] = mine;
+    to.weight[token][lane] = w * a.scale;
+    if (mine >= 0) atomicOr(&to.used[mine / 32], 1u << (mine & 31));
+  }
+}
+// The routing, into LDS.  scratch, logits: OWN's.
+template <int R, bool OWN, int WAVES>
+__device__ inline void route_tokens(const MoeArgs& a, Routing& to, f32x4 (*scratch)[64], float (*logits)[64], int tid,
+                                   int wave) {
+  static_assert(!OWN || R == 1, "logits of up to 64 experts");
+  const int lane = tid & 63;
+  if (tid < kMoeExperts / 32) to.used[tid] = 0u;
+  if constexpr (OWN) own_logits<WAVES>(a, scratch, logits, tid, wave);
+  lds_barrier();
+  for (int token = wave; token < a.tokens; token += WAVES) {
+    Keys<R> k;
+    if constexpr (OWN) load_keys(a, logits[token], 1, 0, lane, k);
+    else load_keys(a, a.logits + (int64_t)token * a.experts, a.parts, (int64_t)a.tokens * a.experts, lane, k);
+    choose(a, k, token, lane, to);
+  }
+  lds_barrier();
+}
+// An expert's place among a token's choices (-1: not chosen) and its weight.
+__device__ inline int place_of(const MoeArgs& a, const Routing& from, int expert, int token, float& w) {
+  int s = -1;
+  w = 0.f;
+  if (token >= a.tokens) return s;
+  if (expert >= a.experts) {
+    w = 1.f;
+    return a.top_k + expert - a.experts;
+  }
+  for (int j0 = 0; j0 < a.top_k; j0 += 4) {   // (choices past top_k are not looked at)
+    const int4 c = *reinterpret_cast<const int4*>(&from.chosen[token][j0]);
+    if (c.x == expert) s = j0;
+    if (c.y == expert && j0 + 1 < a.top_k) s = j0 + 1;
+    if (c.z == expert && j0 + 2 < a.top_k) s = j0 + 2;
+    if (c.w == expert && j0 + 3 < a.top_k) s = j0 + 3;
+  }
+  if (s >= 0) w = from.weight[token][s];
+  return s;
+}
+
+// The routing in a launch of its own, one workgroup.
+constexpr int kRouteWaves = 16;
+template <int R, bool OWN>
+__global__ __launch_bounds__(64 * kRouteWaves) void moe_route(MoeArgs a) {
+  __shared__ Routing rt;
+  __shared__ f32x4 part[OWN ? kRouteWaves : 1][64];
+  __shared__ float logits[OWN ? 16 : 1][64];
+  const int tid = threadIdx.x;
+  __shared__ int list[kMoeSlots];   // the experts in use, in rising order, then the shared ones
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
+  route_tokens<R, OWN, kRouteWaves>(a, rt, part, logits, tid, wave);
   int count = 0;
   for (int w = 0; w < (a.experts + 31) / 32; ++w) {
-    const uint32_t bits = used[w];
+    const uint32_t bits = rt.used[w];
     if (wave == 0 && lane < 32 && (bits >> lane & 1u)) list[count + __popc(bits & ((1u << lane) - 1u))] = w * 32 + lane;
     count += __popc(bits);
   }
   if (tid < a.shared) list[count + tid] = a.experts + tid;
+  lds_barrier();
   const int total = count + a.shared;
-  __syncthreads();
   if (tid == 0) a.route->count = total;
   for (int i = tid; i < total * 16; i += 64 * kRouteWaves) {
-    const int at = i / 16, token = i % 16, e = list[at];
-    if (token == 0) a.route->list[at] = e;
-    int s = -1;
-    float w = 0.f;
-    if (token < a.tokens) {
-      if (at >= count) {
-        s = a.top_k + at - count;
-        w = 1.f;
-      } else {
-        for (int j = 0; j < a.top_k; ++j)
-          if (chosen[token][j] == e) {
-            s = j;
-            w = chosen_w[token][j];
-          }
-      }
-    }
+    const int at = i / 16, token = i % 16;
+    float w;
+    const int s = place_of(a, rt, list[at], token, w);
+    if (token == 0) a.route->list[at] = list[at];
     a.route->place[at][token] = (int8_t)s;
     a.route->weight[at][token] = w;
   }
@@ -590,7 +612,7 @@ __global__ __launch_bounds__(64 * kRouteWaves) void moe_route(MoeArgs a) {
 
 // First products and the activation: h[token, place] of the blockIdx.y-th expert in use, for its tokens.
 // h is kept as two bf16 terms (16 bits, 2^-17 of the value, beside y's 2^-9 or the float32 sums').
-template <int TR, int WAVES, bool GATED, int XS>
+template <int TR, int WAVES, bool GATED, int XS, bool OWN>
 __global__ __launch_bounds__(64 * WAVES) void moe_up(MoeArgs a) {
   constexpr int kOut = GATED ? TR / 2 : TR;
   __shared__ __attribute__((aligned(16))) uint2 dtab[32];
@@ -598,11 +620,38 @@ __global__ __launch_bounds__(64 * WAVES) void moe_up(MoeArgs a) {
   __shared__ int place[16];
   const int tid = threadIdx.x, lane = tid & 63, r = lane & 15, q = lane >> 4;
   const int at = blockIdx.y;
-  const MoeRoute& route = *a.route;
-  const int count = route.count, expert = route.list[at], mine = route.place[at][r];   // (loaded together)
-  if (at >= count) return;
-  if (tid < 16) place[tid] = mine;
   if (tid < 32) dtab[tid] = decode_bf16(tid);
+  int expert, mine;
+  if constexpr (OWN) {
+    __shared__ Routing rt;
+    __shared__ float logits[16][64];
+    route_tokens<1, true, WAVES>(a, rt, part[0], logits, tid, __builtin_amdgcn_readfirstlane(tid >> 6));
+    uint32_t bits[2] = {(uint32_t)__builtin_amdgcn_readfirstlane((int)rt.used[0]),
+                        (uint32_t)__builtin_amdgcn_readfirstlane((int)rt.used[1])};
+    const int low = __popc(bits[0]), count = low + __popc(bits[1]);
+    if (blockIdx.x == 0 && at == 0 && tid == 0) a.route->count = count + a.shared;   // (the route is for moe_down)
+    if (at >= count + a.shared) return;
+    if (at >= count) {
+      expert = a.experts + at - count;
+    } else {   // the at-th expert in use
+      uint32_t left = at < low ? bits[0] : bits[1];
+      for (int i = at < low ? at : at - low; i > 0; --i) left &= left - 1u;
+      expert = __builtin_ctz(left) + (at < low ? 0 : 32);
+    }
+    float w;
+    mine = place_of(a, rt, expert, r, w);
+    if (blockIdx.x == 0 && tid < 16) {
+      if (tid == 0) a.route->list[at] = expert;
+      a.route->place[at][tid] = (int8_t)mine;
+      a.route->weight[at][tid] = w;
+    }
+  } else {
+    const MoeRoute& route = *a.route;
+    const int count = route.count;
+    expert = route.list[at], mine = route.place[at][r];   // (loaded together)
+    if (at >= count) return;
+  }
+  if (tid < 16) place[tid] = mine;
   const int64_t outs = a.hidden, n = GATED ? 2 * outs : outs, tile = blockIdx.x;
   const Planes p = planes(a.up + expert * a.up_bytes, a.up_alpha + expert * a.up_scales, n, a.dim, a.up_gran, a.up_group_sbs);
   const uint32_t x_lane = mine >= 0 ? (uint32_t)(r * a.dim + 8 * q) * 2u : kNowhere;
@@ -625,16 +674,15 @@ __global__ __launch_bounds__(64 * WAVES) void moe_up(MoeArgs a) {
 // Second products, weighted and added over the experts in use: TR row tiles of y, one of gridDim.y
 // ranges of the (expert, superblock) items; the waves share a range evenly.  A token's row of the A operand is its h of
 // the expert at hand, or zeros.  Several ranges leave fp32 partials for moe_join.
-constexpr int kDownTiles = 4, kDownWaves = 8, kDownRing = 1, kDownXRing = 1;
 __device__ inline void store_moe(const MoeArgs& a, int64_t to, float s, void* y, bool y_bf16) {
   if (a.residual) s += bf16_to_f32(a.residual[to]);
   if (y_bf16) static_cast<__bf16*>(y)[to] = (__bf16)s;
   else static_cast<float*>(y)[to] = s;
 }
-__global__ __launch_bounds__(64 * kDownWaves) void moe_down(MoeArgs a, void* __restrict__ y, bool y_bf16) {
-  constexpr int TR = kDownTiles;
+template <int TR, int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void moe_down(MoeArgs a, void* __restrict__ y, bool y_bf16) {
   __shared__ __attribute__((aligned(16))) uint2 dtab[32];
-  __shared__ f32x4 part[kDownWaves][TR][64];
+  __shared__ f32x4 part[WAVES][TR][64];
   __shared__ int list[kMoeSlots];
   __shared__ int8_t place[kMoeSlots][16];
   __shared__ __attribute__((aligned(16))) float weight[kMoeSlots][16];
@@ -646,7 +694,7 @@ __global__ __launch_bounds__(64 * kDownWaves) void moe_down(MoeArgs a, void* __r
   const int sbs = (int)(a.hidden / kSuperblock), items = route.count * sbs;
   const int i0 = (int)((int64_t)items * blockIdx.y / gridDim.y), i1 = (int)((int64_t)items * (blockIdx.y + 1) / gridDim.y);
   const int a0 = i0 / sbs, a1 = (i1 + sbs - 1) / sbs;
-  for (int i = tid; i < (a1 - a0) * 16; i += 64 * kDownWaves) {
+  for (int i = tid; i < (a1 - a0) * 16; i += 64 * WAVES) {
     const int at = i / 16, t = i % 16;
     place[at][t] = route.place[a0 + at][t];
     weight[at][t] = route.weight[a0 + at][t];
@@ -660,8 +708,8 @@ __global__ __launch_bounds__(64 * kDownWaves) void moe_down(MoeArgs a, void* __r
 #pragma unroll
   for (int i = 0; i < TR; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
   const auto h = buffer(a.h, (uint32_t)(2 * a.h_plane * 2));
-  run_items<TR, 2, kDownRing, kDownXRing>(
-      i0 + (i1 - i0) * wave / kDownWaves, i0 + (i1 - i0) * (wave + 1) / kDownWaves, reinterpret_cast<const char*>(dtab), q,
+  run_items<TR, 2, 1, 1>(
+      i0 + (i1 - i0) * wave / WAVES, i0 + (i1 - i0) * (wave + 1) / WAVES, reinterpret_cast<const char*>(dtab), q,
       [&](int j, bool live, Records<TR>& rec) {
         const int e = __builtin_amdgcn_readfirstlane(list[j / sbs - a0]);
         const Planes p = planes(a.down + e * a.down_bytes, a.down_alpha + e * a.down_scales, a.dim, a.hidden, a.down_gran,
@@ -681,9 +729,9 @@ __global__ __launch_bounds__(64 * kDownWaves) void moe_down(MoeArgs a, void* __r
   __syncthreads();
   const int64_t size = (int64_t)a.tokens * a.dim;
   float* mine = a.partial + (int64_t)blockIdx.y * size;
-  for (int o = tid; o < a.tokens * 16 * TR; o += 64 * kDownWaves) {
+  for (int o = tid; o < a.tokens * 16 * TR; o += 64 * WAVES) {
     const int token = o / (16 * TR), c = o % (16 * TR);
-    const float s = wave_sums<TR, kDownWaves>(part, c / 16, token, c % 16);
+    const float s = wave_sums<TR, WAVES>(part, c / 16, token, c % 16);
     const int64_t to = (int64_t)token * a.dim + col0 + c;
     if (gridDim.y == 1) store_moe(a, to, s, y, y_bf16);
     else mine[to] = s;
@@ -748,9 +796,17 @@ hipError_t launch_linear_decode(const LinearArgs& a, const uint16_t* x, int toke
 // with the logits in a launch of their own).
 constexpr int64_t kRouteBytes = 65536;
 
-// Ranges of the second products: one up to 32 items (4 a wave: a launch less, the same time in a graph), otherwise about
-// two items a wave, and at most 512 workgroups (1 token, 8 of 64 experts of 2048 x 1024, 64 items: 20.4 us in a graph, in
-// one range 26.4; called from Python 28.6 and 26.5).
+// Up to this many workgroups the first products make a small router's routing each for itself, which saves its launch:
+// 3 us of a call from Python; in a graph, at 512, 17.2 us against 18.0 (4 tokens, 2 of 16 experts of 1024 x 2048), 14.8 against 16.4 (4
+// tokens, 4 of 32 of 512 x 512), 18.1 against 17.1 (16 tokens, 2 of 16 of 512 x 1024); at 1024 workgroups 22.4 against 21.3, at 2048 32
+// against 25.5.
+constexpr int64_t kOwnRouting = 512;
+
+// The second products in one range of 16 waves and 16 rows a workgroup up to kNarrowItems items (4 a wave), which saves
+// the joining launch; past it 64 rows, 8 waves and ranges of about two items a wave, at most 512 workgroups (in a graph, 1 token: 2 of
+// 16 experts of 4096 x 2048, 32 items, 18.9 us against 21.2; 8 of 64 of 2048 x 1024, 64 items, 20.9 against 20.1, but called from
+// Python 23.7 against 25.9; 2 of 8 of 2048 x 8192, 128 items, 26.3 against 20.4).
+constexpr int kNarrowItems = 64, kDownTiles = 4, kDownWaves = 8;
 MoePlan plan_moe(int tokens, int64_t dim, int64_t hidden, int experts, int shared, int top_k, bool router_bf16) {
   auto up = [](size_t b) { return (b + 255) & ~(size_t)255; };
   const int slots = top_k + shared;
@@ -758,7 +814,9 @@ MoePlan plan_moe(int tokens, int64_t dim, int64_t hidden, int experts, int share
   p.used = std::min(experts, tokens * top_k) + shared;
   const int64_t items = p.used * (hidden / kSuperblock);
   const int64_t blocks = dim / (16 * kDownTiles);
-  p.ranges = items <= 32 ? 1 : (int)std::max<int64_t>(1, std::min((items + 2 * kDownWaves - 1) / (2 * kDownWaves), (512 + blocks - 1) / blocks));
+  p.narrow = items <= kNarrowItems;
+  p.ranges = 1;
+  if (!p.narrow) p.ranges = (int)std::min((items + 2 * kDownWaves - 1) / (2 * kDownWaves), (512 + blocks - 1) / blocks);
   p.h_plane = (int64_t)tokens * slots * hidden;
   p.logits_offset = up(sizeof(MoeRoute));
   const int64_t read = (experts * (router_bf16 ? 2 : 4) + tokens * 2) * dim;
@@ -774,31 +832,29 @@ hipError_t launch_moe(const MoePlan& p, MoeArgs a, void* y, bool y_bf16, hipStre
   hipError_t e;
   a.ranges = p.ranges;
   a.parts = p.parts;
-  if (p.parts == 0) {
-#define SHERRY_ROUTE(T)                                                                     \
-  do {                                                                                      \
-    if (a.router_bf16) hipLaunchKernelGGL((moe_route<1, T, true>), dim3(1), wg, 0, s, a);   \
-    else hipLaunchKernelGGL((moe_route<1, T, false>), dim3(1), wg, 0, s, a);                \
-  } while (0)
-    if (a.experts <= 16) SHERRY_ROUTE(1);
-    else if (a.experts <= 32) SHERRY_ROUTE(2);
-    else SHERRY_ROUTE(4);
-#undef SHERRY_ROUTE
-  } else {
+  const bool wide = wide_tiles((a.gated ? 2 : 1) * a.hidden / 64 * p.used);
+  const dim3 first((unsigned)(a.hidden / (wide ? (a.gated ? 32 : 64) : 16)), (unsigned)p.used);
+  const bool own = p.parts == 0 && (int64_t)first.x * first.y <= kOwnRouting;
+  if (p.parts > 0) {
     const dim3 tiles((unsigned)((a.experts + 15) / 16), (unsigned)p.parts);
     if (a.router_bf16) hipLaunchKernelGGL(moe_logits<true>, tiles, dim3(64 * kLogitWaves), 0, s, a);
     else hipLaunchKernelGGL(moe_logits<false>, tiles, dim3(64 * kLogitWaves), 0, s, a);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
-    if (a.experts <= 64) hipLaunchKernelGGL((moe_route<1, 0, true>), dim3(1), wg, 0, s, a);
-    else if (a.experts <= 128) hipLaunchKernelGGL((moe_route<2, 0, true>), dim3(1), wg, 0, s, a);
-    else hipLaunchKernelGGL((moe_route<8, 0, true>), dim3(1), wg, 0, s, a);
   }
-  e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  const bool wide = wide_tiles((a.gated ? 2 : 1) * a.hidden / 64 * p.used);
-  const dim3 first((unsigned)(a.hidden / (wide ? (a.gated ? 32 : 64) : 16)), (unsigned)p.used);
-#define SHERRY_UP_T(TR, W, G, XS) hipLaunchKernelGGL((moe_up<TR, W, G, XS>), first, dim3(64 * W), 0, s, a)
+  if (!own) {
+    if (p.parts == 0) hipLaunchKernelGGL((moe_route<1, true>), dim3(1), wg, 0, s, a);
+    else if (a.experts <= 64) hipLaunchKernelGGL((moe_route<1, false>), dim3(1), wg, 0, s, a);
+    else if (a.experts <= 128) hipLaunchKernelGGL((moe_route<2, false>), dim3(1), wg, 0, s, a);
+    else hipLaunchKernelGGL((moe_route<8, false>), dim3(1), wg, 0, s, a);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+#define SHERRY_UP_T(TR, W, G, XS)                                                                     \
+  do {                                                                                                \
+    if (own) hipLaunchKernelGGL((moe_up<TR, W, G, XS, true>), first, dim3(64 * W), 0, s, a);          \
+    else hipLaunchKernelGGL((moe_up<TR, W, G, XS, false>), first, dim3(64 * W), 0, s, a);             \
+  } while (0)
 #define SHERRY_UP(W, XS)                              \
   do {                                                \
     if (wide && a.gated) SHERRY_UP_T(4, W, true, XS); \
@@ -811,8 +867,11 @@ hipError_t launch_moe(const MoePlan& p, MoeArgs a, void* y, bool y_bf16, hipStre
 #undef SHERRY_UP_T
   e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(moe_down, dim3((unsigned)(a.dim / (16 * kDownTiles)), (unsigned)p.ranges), dim3(64 * kDownWaves), 0,
-                     s, a, y, y_bf16);
+  if (p.narrow)
+    hipLaunchKernelGGL((moe_down<1, 16>), dim3((unsigned)(a.dim / 16)), dim3(64 * 16), 0, s, a, y, y_bf16);
+  else
+    hipLaunchKernelGGL((moe_down<kDownTiles, kDownWaves>), dim3((unsigned)(a.dim / (16 * kDownTiles)), (unsigned)p.ranges),
+                       dim3(64 * kDownWaves), 0, s, a, y, y_bf16);
   e = hipGetLastError();
   if (e != hipSuccess || p.ranges == 1) return e;
   hipLaunchKernelGGL(moe_join, dim3((unsigned)((a.tokens * a.dim + 255) / 256)), dim3(256), 0, s, a, y, y_bf16);

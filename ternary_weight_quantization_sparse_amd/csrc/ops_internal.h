@@ -271,6 +271,7 @@ struct MoeArgs {
 struct MoePlan {
   int used;                                    // experts in use at most
   int ranges;                                  // of the second products
+  bool narrow;                                 // they take 16 rows a workgroup
   int parts;                                   // of the logits' channels
   int64_t h_plane;
   size_t logits_offset, h_offset, partial_offset, workspace_bytes;

@@ -122,6 +122,23 @@ def test_wide_tiles(dim, gated):
     Layer(36, dim, 512, gated=gated).check(4, 8)
 
 
+@pytest.mark.parametrize("router", [BF16, F32])
+@pytest.mark.parametrize("experts,tokens,top_k,hidden", [(8, 16, 2, 4096), (16, 11, 2, 2048), (27, 16, 3, 1024), (60, 7, 8, 512),
+                                                         (16, 3, 2, 1024), (32, 5, 4, 256), (64, 2, 8, 128)])
+def test_routing_by_itself_and_in_the_first_products(router, experts, tokens, top_k, hidden):
+    """A router that one workgroup reads, with few and with many workgroups of first products."""
+    Layer(experts, 128, hidden, router=router).check(tokens, top_k)
+    Layer(experts, 128, hidden, 1, gated=False, router=router).check(tokens, top_k, "sigmoid", bias=torch.zeros(experts, device=DEV),
+                                                                     margin=False)
+
+
+@pytest.mark.parametrize("hidden", [1024, 1920, 2048, 2176])
+def test_items_of_the_second_products(hidden):
+    """One to five superblocks a wave in one range, and ranges (4 experts a token)."""
+    for tokens in (1, 2):
+        Layer(12, 256, hidden).check(tokens, 4)
+
+
 def test_long_hidden():
     Layer(3, 256, 8320, 1).check(2, 2)
     Layer(3, 8320, 8320).check(1, 1)
