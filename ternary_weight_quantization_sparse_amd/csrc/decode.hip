@@ -262,6 +262,19 @@ __device__ inline float wave_sums(const f32x4 (&part)[WAVES][TR][64], int which,
   return sum;
 }
 
+// Bias, activation, gate and residual of one output; `to` its place in y.
+template <bool GATED>
+__device__ inline float finish_output(const LinearArgs& a, float z, float u, int64_t col, int64_t outs, int64_t to) {
+  if (a.bias) z += load_float(a.bias, col, a.bias_bf16);
+  z = activate(z, a.activation);
+  if constexpr (GATED) {
+    if (a.bias) u += load_float(a.bias, outs + col, a.bias_bf16);
+    z *= u;
+  }
+  if (a.residual) z += a.res_scale * bf16_to_f32(a.residual[to]);
+  return z;
+}
+
 // ------------------------------------------------------------ linear, 1..16 tokens
 template <int TR, int WAVES, bool GATED, int XS>
 __global__ __launch_bounds__(64 * WAVES) void linear_decode(LinearArgs a, const uint16_t* __restrict__ x, int tokens,
@@ -284,18 +297,91 @@ __global__ __launch_bounds__(64 * WAVES) void linear_decode(LinearArgs a, const 
     const int token = o / (16 * kOut), which = o / 16 % kOut, c = o % 16;
     const int64_t col = tile * (16 * kOut) + which * 16 + c;
     if (col >= outs) continue;
-    float z = wave_sums<TR, WAVES>(part, which, token, c);
-    if (a.bias) z += load_float(a.bias, col, a.bias_bf16);
-    z = activate(z, a.activation);
-    if constexpr (GATED) {
-      float u = wave_sums<TR, WAVES>(part, kOut + which, token, c);
-      if (a.bias) u += load_float(a.bias, outs + col, a.bias_bf16);
-      z *= u;
-    }
     const int64_t to = (int64_t)token * outs + col;
-    if (a.residual) z += a.res_scale * bf16_to_f32(a.residual[to]);
+    const float u = GATED ? wave_sums<TR, WAVES>(part, kOut * GATED + which, token, c) : 1.f;
+    const float z = finish_output<GATED>(a, wave_sums<TR, WAVES>(part, which, token, c), u, col, outs, to);
     if (y_bf16) static_cast<__bf16*>(y)[to] = (__bf16)z;
     else static_cast<float*>(y)[to] = z;
+  }
+}
+
+// ------------------------------------------------------------ linear, prompts of few tiles
+// More tokens than 16, in tiles of 16 by 64 weight rows a workgroup: no staging of the tokens and no partials in memory, so
+// a launch of many short workgroups instead of a few long ones and a second launch (517 x 2048 x 2048: 15.4 us against 20.1; 64 x
+// 2048 x 2048: 6.5 against 10.2).  A superblock's loads are waited for: the other waves of the SIMD cover them (loads
+// a superblock ahead 17.0 us, two tiles of tokens a workgroup 18.6); what bounds many tiles is the tokens' traffic, each row block's own.
+template <int WAVES, bool GATED>
+__global__ __launch_bounds__(64 * WAVES) void linear_tiles(LinearArgs a, const uint16_t* __restrict__ x, int64_t m,
+                                                           __bf16* __restrict__ y, int tiles_m) {
+  constexpr int TR = 4, kOut = GATED ? TR / 2 : TR;
+  __shared__ __attribute__((aligned(16))) uint2 dtab[32];
+  __shared__ f32x4 part[WAVES][TR][64];
+  const int tid = threadIdx.x, lane = tid & 63, r = lane & 15, q = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  if (tid < 32) dtab[tid] = decode_bf16(tid);
+  const int64_t outs = GATED ? a.n / 2 : a.n;
+  const Planes p = planes(a.packed, a.alpha, a.n, a.k, a.gran, a.group_sbs);
+  // each XCD takes neighbouring workgroups: all the tokens of a few rows
+  const int xcd = blockIdx.x & 7, share = gridDim.x >> 3, more = gridDim.x & 7;
+  const int id = xcd * share + min(xcd, more) + (blockIdx.x >> 3), tm = id % tiles_m, tn = id / tiles_m;
+  const int64_t m0 = (int64_t)tm * 16, col0 = (int64_t)tn * (16 * kOut);
+  uint32_t row[kRowsOf<TR>];
+  lane_rows<TR>(
+      [&](int i, int rr) {
+        const int64_t col = col0 + (i % kOut) * 16 + rr;
+        return col < outs ? (uint32_t)(i < kOut ? col : outs + col) : kNoRow;
+      },
+      r, q, row);
+  const uint32_t x_lane = m0 + r < m ? (uint32_t)((m0 + r) * a.k + 8 * q) * 2u : kNowhere;
+  const auto xb = buffer(x, (uint32_t)(m * a.k * 2));
+  f32x4 acc[TR];
+#pragma unroll
+  for (int i = 0; i < TR; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+  const int sbs = (int)(a.k / kSuperblock), j0 = sbs * wave / WAVES, j1 = sbs * (wave + 1) / WAVES;
+  Records<TR> rec;
+  u32x4 xf[4];
+  auto load = [&](int j) {
+    rec.load(block(p, j), row, p.row_step, q);
+    load_tokens(xb, x_lane + (uint32_t)j * (2 * kSuperblock), xf);
+  };
+  if (j0 < j1) load(j0);
+  lds_barrier();   // the table is written
+  for (int j = j0; j < j1; ++j) {
+    const TileRecords<TR> rt = rec.tiles();
+    const char* tab = reinterpret_cast<const char*>(dtab);
+#pragma unroll
+    for (int i = 0; i < TR; ++i) {
+      const uint32_t lo = quad_offsets8(rt.nib[i], rt.sgn[i], 2 * q), hi = quad_offsets8(rt.nib[i], rt.sgn[i], 2 * q + 1);
+      f32x4 g = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        const uint2 e0 = *reinterpret_cast<const uint2*>(tab + __builtin_amdgcn_ubfe(lo, 8 * s, 8));
+        const uint2 e1 = *reinterpret_cast<const uint2*>(tab + __builtin_amdgcn_ubfe(hi, 8 * s, 8));
+        const bf16x8 w = __builtin_bit_cast(bf16x8, u32x4{e0.x, e0.y, e1.x, e1.y});
+        g = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, xf[s]), w, g, 0, 0, 0);
+      }
+      acc[i] += rt.al[i] * g;
+    }
+    if (j + 1 < j1) load(j + 1);
+  }
+#pragma unroll
+  for (int i = 0; i < TR; ++i) part[wave][i][lane] = acc[i];
+  lds_barrier();
+  for (int i = wave; i < kOut; i += WAVES) {   // four tokens of an output a lane
+    const int64_t col = col0 + i * 16 + r;
+    if (col >= outs) continue;
+    f32x4 z = part[0][i][lane], u = {1.f, 1.f, 1.f, 1.f};
+    if constexpr (GATED) u = part[0][kOut + i][lane];
+#pragma unroll
+    for (int w = 1; w < WAVES; ++w) {
+      z += part[w][i][lane];
+      if constexpr (GATED) u += part[w][kOut + i][lane];
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int64_t token = m0 + 4 * q + e;
+      if (token < m) y[token * outs + col] = (__bf16)finish_output<GATED>(a, z[e], u[e], col, outs, token * outs + col);
+    }
   }
 }
 
@@ -789,6 +875,23 @@ hipError_t launch_linear_decode(const LinearArgs& a, const uint16_t* x, int toke
   SHERRY_TILES(SHERRY_LINEAR, a.k / kSuperblock);
 #undef SHERRY_LINEAR
 #undef SHERRY_LINEAR_T
+  return hipGetLastError();
+}
+
+// Workgroups of 16 tokens by 64 rows, of 8 waves where there is at most one a CU (64 x 2048 x 8192: 12.2 us, with 4 waves 15.4),
+// otherwise of 4 (517 x 2048 x 2048: 15.4 us, with 8 17.5).
+hipError_t launch_linear_tiles(const LinearArgs& a, const uint16_t* x, int64_t m, uint16_t* y, hipStream_t s) {
+  const int64_t outs = a.gated ? a.n / 2 : a.n, tile = a.gated ? 32 : 64;
+  const int tiles_m = (int)((m + 15) / 16);
+  const dim3 grid((unsigned)(tiles_m * ((outs + tile - 1) / tile)));
+  __bf16* to = reinterpret_cast<__bf16*>(y);
+#define SHERRY_LINEAR_TILES(W, G) \
+  hipLaunchKernelGGL((linear_tiles<W, G>), grid, dim3(64 * W), 0, s, a, x, m, to, tiles_m)
+  if (grid.x <= 256 && a.gated) SHERRY_LINEAR_TILES(8, true);
+  else if (grid.x <= 256) SHERRY_LINEAR_TILES(8, false);
+  else if (a.gated) SHERRY_LINEAR_TILES(4, true);
+  else SHERRY_LINEAR_TILES(4, false);
+#undef SHERRY_LINEAR_TILES
   return hipGetLastError();
 }
 

@@ -155,6 +155,26 @@ def test_prompts_in_several_launches():
     close(y[rows], want, tol)
 
 
+@pytest.mark.parametrize("grain", ["per_group", "per_channel", "per_tensor"])
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("tokens,n,k", [(517, 4098, 2048), (260, 2050, 8192), (2050, 2050, 1024), (2050, 16386, 512)])
+def test_prompts_of_many_tiles(tokens, n, k, grain, gated):
+    """Splits of K, narrow and wide tiles of the long prompts' kernel."""
+    pw, x, b, res = make(tokens, n, k, grain, gated=gated)
+    check(pw, x, b, "silu", gated, res)
+
+
+@pytest.mark.parametrize("tokens,n,k", [(1024, 2048, 2048), (1024, 2050, 2048), (17, 64, 128), (31, 66, 8192), (255, 1002, 384),
+                                        (4096, 128, 2048)])
+def test_prompts_of_few_tiles(tokens, n, k):
+    """Up to the last size of the short workgroups' kernel and past it, with four waves and with eight."""
+    for gated in (False, True):
+        pw, x, b, res = make(tokens, n, k, gated=gated)
+        check(pw, x, b, "gelu_tanh", gated, res)
+        pw, x, _, _ = make(tokens, n, k, "per_channel", bias=None, residual=False, gated=gated)
+        check(pw, x, None, "relu2", gated, None)
+
+
 def test_no_epilogue_is_the_product():
     for tokens in (1, 16, 400):
         pw, x, _, _ = make(tokens, 512, 1024, bias=None, residual=False)
