@@ -1,14 +1,20 @@
-// Packed products of 1..16 tokens with what follows them in one launch, and a
+// Packed products of few tokens with what follows them in one launch, and a
 // mixture-of-experts layer of packed experts.
 //
 // One tile product serves them: a wave multiplies the tokens (the 16 rows of
 // v_mfma_f32_16x16x32_bf16's A operand) with 16-row tiles of a packed weight
 // (the B operand, decoded through a 32-entry LDS table as in the decode
 // product), lane (r, q) of it holding row r's nibble dword q, sign dword and
-// scale: 12 bytes a tile and superblock, straight from memory into registers.
-// The waves of a workgroup split K (or the experts' K) and join through LDS in
-// wave order, so a call needs neither partials in memory nor a second launch,
-// and its sums have one order.
+// scale, straight from memory into registers.  The waves of a workgroup split
+// K (or the experts' K) and join through LDS in wave order, so sums have one
+// order and a product needs neither partials in memory nor a second launch;
+// only the experts' second products, past 64 superblocks, are split over
+// workgroups too and joined by a launch of their own.
+//
+// Latency bounds nearly all of it: the weights of 1 x 2048 x 2048 are read in
+// 0.15 us at a copy's rate, and a launch that waits for one load from memory
+// takes 3.5 us.  What carries it is many short workgroups whose loads are all
+// issued at once, and few launches.
 #include <algorithm>
 #include <cfloat>
 
@@ -79,8 +85,8 @@ struct Records {
     return r;
   }
 };
-// Four tiles: lane (r, q) loads the whole record of row r of tile q (three loads of 1 KB and 256 bytes instead of twelve),
-// and the 4 x 4 words of four lanes change places: M[q][word] to M[tile][q].
+// Four tiles: lane (r, q) loads the whole record of row r of tile q (three loads of 1 KB and 256 bytes instead of
+// twelve), and the 4 x 4 words of four lanes change places: M[q][word] to M[tile][q].
 template <>
 struct Records<4> {
   u32x4 nib;
@@ -206,10 +212,10 @@ __device__ inline void run_items(int j0, int j1, const char* dtab, int q, R reco
 }
 
 // One output tile of a packed weight: TR row tiles (GATED: half gate rows, half the same outputs' rows of the
-// weight's second half).  The waves split K; a wave issues all its loads at once where it has up to XS superblocks (0: more,
-// through a ring), and the waves join through LDS: wave_sums adds them in order.  Short
-// workgroups, eight waves a SIMD, hide the latency better than ones that walk several tiles and load
-// ahead (mixture of experts, 16 tokens, 56 experts of 2048 x 2048: 18 us against 20 to 25).
+// weight's second half).  The waves split K; a wave issues all its loads at once where it has up to XS superblocks
+// (0: more, through a ring), and the waves join through LDS: wave_sums adds them in order.  Short workgroups, eight
+// waves a SIMD, hide the latency better than ones that walk several tiles and load ahead (mixture of experts, 16
+// tokens, 56 experts of 2048 x 2048: 18 us against 20 to 25).
 template <int TR, int WAVES, bool GATED, int XS>
 __device__ inline void tile_product(const Planes& p, int64_t outs, int sbs, __amdgpu_buffer_rsrc_t x, uint32_t x_lane,
                                     int64_t tile, const char* dtab, f32x4 (&part)[WAVES][TR][64]) {
@@ -276,6 +282,7 @@ __device__ inline float finish_output(const LinearArgs& a, float z, float u, int
 }
 
 // ------------------------------------------------------------ linear, 1..16 tokens
+// 1 x 2048 x 2048: 3.7 us; 16 x 16384 x 2048 gated, 6.6 MB: 5.4 us (1.2 TB/s); 5 x 1001 x 8192: 7.6 us.
 template <int TR, int WAVES, bool GATED, int XS>
 __global__ __launch_bounds__(64 * WAVES) void linear_decode(LinearArgs a, const uint16_t* __restrict__ x, int tokens,
                                                             void* __restrict__ y, bool y_bf16) {
@@ -306,10 +313,11 @@ __global__ __launch_bounds__(64 * WAVES) void linear_decode(LinearArgs a, const 
 }
 
 // ------------------------------------------------------------ linear, prompts of few tiles
-// More tokens than 16, in tiles of 16 by 64 weight rows a workgroup: no staging of the tokens and no partials in memory, so
-// a launch of many short workgroups instead of a few long ones and a second launch (517 x 2048 x 2048: 15.4 us against 20.1; 64 x
-// 2048 x 2048: 6.5 against 10.2).  A superblock's loads are waited for: the other waves of the SIMD cover them (loads
-// a superblock ahead 17.0 us, two tiles of tokens a workgroup 18.6); what bounds many tiles is the tokens' traffic, each row block's own.
+// More tokens than 16, in tiles of 16 by 64 weight rows a workgroup: no staging of the tokens and no partials in
+// memory, so a launch of many short workgroups instead of a few long ones and a second launch (517 x 2048 x 2048:
+// 15.4 us against 20.1; 64 x 2048 x 2048: 6.5 against 10.2).  A superblock's loads are waited for: the other waves of
+// the SIMD cover them (loads a superblock ahead 17.0 us, two tiles of tokens a workgroup 18.6); what bounds many
+// tiles is the tokens' traffic, each row block's own.
 template <int WAVES, bool GATED>
 __global__ __launch_bounds__(64 * WAVES) void linear_tiles(LinearArgs a, const uint16_t* __restrict__ x, int64_t m,
                                                            __bf16* __restrict__ y, int tiles_m) {
@@ -487,9 +495,9 @@ __device__ inline int take_best(Keys<R>& k, int lane) {
   }
   return e;
 }
-// Router logits of a tile of 16 experts on MFMA (A: the tokens, B: the router's
-// rows): 32-channel steps [s0, s1), consecutive ones, so that a row's memory lines are read whole.  A float32 router goes in as
-// three bf16 terms (24 bits).
+// Router logits of a tile of 16 experts on MFMA (A: the tokens, B: the router's rows): 32-channel steps [s0, s1),
+// consecutive ones, so that a row's memory lines are read whole.  A float32 router goes in as three bf16 terms (24
+// bits).
 template <bool R_BF16>
 __device__ inline f32x4 logit_tile(const MoeArgs& a, int tile, int s0, int s1, int lane) {
   constexpr int kAhead = R_BF16 ? 8 : 4;
@@ -537,8 +545,8 @@ __device__ inline f32x4 logit_tile(const MoeArgs& a, int tile, int s0, int s1, i
   return acc;
 }
 
-// Logits of many experts, in parts over the channels [part, tokens, experts]: one CU alone reads a cold router slowly (64
-// experts of 2048 channels and 16 tokens, 320 KB: 12 us), so a tile and a part a workgroup.
+// Logits of many experts, in parts over the channels [part, tokens, experts]: one CU alone reads a cold router slowly
+// (64 experts of 2048 channels and 16 tokens, 320 KB: 12 us), so a tile and a part a workgroup.
 constexpr int kLogitWaves = 4;
 template <bool R_BF16>
 __global__ __launch_bounds__(64 * kLogitWaves) void moe_logits(MoeArgs a) {
@@ -665,7 +673,8 @@ __device__ inline int place_of(const MoeArgs& a, const Routing& from, int expert
   return s;
 }
 
-// The routing in a launch of its own, one workgroup.
+// The routing in a launch of its own, one workgroup: 5.4 us for 16 tokens, 8 of 64 experts (logits made before), a
+// chain of the choices, their weights and three barriers.
 constexpr int kRouteWaves = 16;
 template <int R, bool OWN>
 __global__ __launch_bounds__(64 * kRouteWaves) void moe_route(MoeArgs a) {
@@ -696,8 +705,10 @@ __global__ __launch_bounds__(64 * kRouteWaves) void moe_route(MoeArgs a) {
   }
 }
 
-// First products and the activation: h[token, place] of the blockIdx.y-th expert in use, for its tokens.
-// h is kept as two bf16 terms (16 bits, 2^-17 of the value, beside y's 2^-9 or the float32 sums').
+// First products and the activation: h[token, place] of the blockIdx.y-th expert in use, for its tokens. h is kept as
+// two bf16 terms (16 bits, 2^-17 of the value, beside y's 2^-9 or the float32 sums'). 16 tokens, 56 of 64 experts of
+// 2048 x 2 x 1024, 43 MB: 15.7 us (2.7 TB/s).  Of that the LDS lookups take 6 us; without any product it takes 13,
+// without the records' loads 12: no single one of them bounds it.
 template <int TR, int WAVES, bool GATED, int XS, bool OWN>
 __global__ __launch_bounds__(64 * WAVES) void moe_up(MoeArgs a) {
   constexpr int kOut = GATED ? TR / 2 : TR;
@@ -757,9 +768,10 @@ __global__ __launch_bounds__(64 * WAVES) void moe_up(MoeArgs a) {
   }
 }
 
-// Second products, weighted and added over the experts in use: TR row tiles of y, one of gridDim.y
-// ranges of the (expert, superblock) items; the waves share a range evenly.  A token's row of the A operand is its h of
-// the expert at hand, or zeros.  Several ranges leave fp32 partials for moe_join.
+// Second products, weighted and added over the experts in use: TR row tiles of y, one of gridDim.y ranges of the
+// (expert, superblock) items; the waves share a range evenly.  A token's row of the A operand is its h of the expert
+// at hand, or zeros.  Several ranges leave fp32 partials for moe_join. 16 tokens, 56 experts of 1024 x 2048, 25 MB:
+// 13.4 us (1.9 TB/s), each item's h (two terms of 4 KB) beside the weights' 11 KB.
 __device__ inline void store_moe(const MoeArgs& a, int64_t to, float s, void* y, bool y_bf16) {
   if (a.residual) s += bf16_to_f32(a.residual[to]);
   if (y_bf16) static_cast<__bf16*>(y)[to] = (__bf16)s;
@@ -853,8 +865,8 @@ __global__ __launch_bounds__(256) void moe_join(MoeArgs a, void* __restrict__ y,
     else if ((SBS) <= 64) RUN(16, 4);   \
     else RUN(16, 0);                    \
   } while (0)
-// 64 weight rows a workgroup where that leaves work for every CU (16 x 16384 x 2048 gated: 5.7 us, with 16 + 16 rows 7.7);
-// 16 (16 + 16: gate and values) where it does not (1 x 2048 x 2048: 3.8 us in 128 workgroups).
+// 64 weight rows a workgroup where that leaves work for every CU (16 x 16384 x 2048 gated: 5.7 us, with 16 + 16 rows
+// 7.7); 16 (16 + 16: gate and values) where it does not (1 x 2048 x 2048: 3.8 us in 128 workgroups).
 bool wide_tiles(int64_t blocks64) { return blocks64 >= 256; }
 
 hipError_t launch_linear_decode(const LinearArgs& a, const uint16_t* x, int tokens, void* y, bool y_bf16,
@@ -878,8 +890,8 @@ hipError_t launch_linear_decode(const LinearArgs& a, const uint16_t* x, int toke
   return hipGetLastError();
 }
 
-// Workgroups of 16 tokens by 64 rows, of 8 waves where there is at most one a CU (64 x 2048 x 8192: 12.2 us, with 4 waves 15.4),
-// otherwise of 4 (517 x 2048 x 2048: 15.4 us, with 8 17.5).
+// Workgroups of 16 tokens by 64 rows, of 8 waves where there is at most one a CU (64 x 2048 x 8192: 12.2 us, with 4
+// waves 15.4), otherwise of 4 (517 x 2048 x 2048: 15.4 us, with 8 17.5).
 hipError_t launch_linear_tiles(const LinearArgs& a, const uint16_t* x, int64_t m, uint16_t* y, hipStream_t s) {
   const int64_t outs = a.gated ? a.n / 2 : a.n, tile = a.gated ? 32 : 64;
   const int tiles_m = (int)((m + 15) / 16);
@@ -899,16 +911,16 @@ hipError_t launch_linear_tiles(const LinearArgs& a, const uint16_t* x, int64_t m
 // with the logits in a launch of their own).
 constexpr int64_t kRouteBytes = 65536;
 
-// Up to this many workgroups the first products make a small router's routing each for itself, which saves its launch:
-// 3 us of a call from Python; in a graph, at 512, 17.2 us against 18.0 (4 tokens, 2 of 16 experts of 1024 x 2048), 14.8 against 16.4 (4
-// tokens, 4 of 32 of 512 x 512), 18.1 against 17.1 (16 tokens, 2 of 16 of 512 x 1024); at 1024 workgroups 22.4 against 21.3, at 2048 32
-// against 25.5.
+// Up to this many workgroups the first products make a small router's routing each for itself, which saves its
+// launch: 3 us of a call from Python; in a graph, at 512, 17.2 us against 18.0 (4 tokens, 2 of 16 experts of 1024 x
+// 2048), 14.8 against 16.4 (4 tokens, 4 of 32 of 512 x 512), 18.1 against 17.1 (16 tokens, 2 of 16 of 512 x 1024); at
+// 1024 workgroups 22.4 against 21.3, at 2048 32 against 25.5.
 constexpr int64_t kOwnRouting = 512;
 
-// The second products in one range of 16 waves and 16 rows a workgroup up to kNarrowItems items (4 a wave), which saves
-// the joining launch; past it 64 rows, 8 waves and ranges of about two items a wave, at most 512 workgroups (in a graph, 1 token: 2 of
-// 16 experts of 4096 x 2048, 32 items, 18.9 us against 21.2; 8 of 64 of 2048 x 1024, 64 items, 20.9 against 20.1, but called from
-// Python 23.7 against 25.9; 2 of 8 of 2048 x 8192, 128 items, 26.3 against 20.4).
+// The second products in one range of 16 waves and 16 rows a workgroup up to kNarrowItems items (4 a wave), which
+// saves the joining launch; past it 64 rows, 8 waves and ranges of about two items a wave, at most 512 workgroups (in
+// a graph, 1 token: 2 of 16 experts of 4096 x 2048, 32 items, 18.9 us against 21.2; 8 of 64 of 2048 x 1024, 64 items,
+// 20.9 against 20.1, but called from Python 23.7 against 25.9; 2 of 8 of 2048 x 8192, 128 items, 26.3 against 20.4).
 constexpr int kNarrowItems = 64, kDownTiles = 4, kDownWaves = 8;
 MoePlan plan_moe(int tokens, int64_t dim, int64_t hidden, int experts, int shared, int top_k, bool router_bf16) {
   auto up = [](size_t b) { return (b + 255) & ~(size_t)255; };

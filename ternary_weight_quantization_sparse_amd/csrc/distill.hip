@@ -10,12 +10,11 @@
 //   dloss/ds = w t ((P + rest) q - scatter(p) - [outside the ids] rest q / q_rest)
 //              + (1 - w) (softmax(s) - onehot(label)),      P = sum_j p_j
 //
-// HBM bounds both directions: the forward pass reads the logits once (running
-// maximum and sums), the backward pass reads them once more and writes the
-// gradient: 2048 x 128000 bf16 with 64 slots 102 us (5.1 TB/s) + 12 us (the rows' losses) and 180 to 208 us (5.0 to 5.8 TB/s), 300 us
-// together; three passes at a copy's 5.13 TB/s take 307.  Everything that belongs to a row (sums over threads, logarithms,
-// the teacher's probabilities) is in 64 bits: the loss is a difference of
-// terms of its own size or larger.
+// HBM bounds both directions: the forward pass reads the logits once (running maximum and sums), the backward pass
+// reads them once more and writes the gradient: 2048 x 128000 bf16 with 64 slots 89 us (5.9 TB/s) + 12 us (the rows'
+// losses) and 207 us (5.1 TB/s), 300 us together; three passes at a copy's 5.2 TB/s take 302.
+// Everything that belongs to a row (sums over threads, logarithms, the teacher's probabilities) is in 64 bits: the
+// loss is a difference of terms of its own size or larger.
 #include <algorithm>
 #include <cfloat>
 
@@ -498,8 +497,8 @@ __global__ __launch_bounds__(kThreads) void distill_grad(DistillGrad a, int64_t 
   if (label_here) store_one<BF16>(a.out, first + label, label_fix);
 }
 
-// Logits that the last-level cache (256 MB) cannot keep from one pass to the next are streamed past it, and so are their
-// gradients: 2048 x 128000 bf16, both directions, 332 -> 302 us.  Smaller ones find them there (333 x 50001
+// Logits that the last-level cache (256 MB) cannot keep from one pass to the next are streamed past it, and so are
+// their gradients: 2048 x 128000 bf16, both directions, 332 -> 302 us.  Smaller ones find them there (333 x 50001
 // fp32: 123 us a call by itself, streamed 138).
 bool streams(int64_t rows, int64_t vocab, bool bf16) { return rows * vocab * (bf16 ? 2 : 4) > (int64_t)192 << 20; }
 

@@ -962,9 +962,9 @@ hipError_t launch_gemm_adapted(const GemmPlan& p, int64_t n, int64_t k, int gran
 #undef SHERRY_GEMM_LAUNCH
 }
 
-// Prompts of few (16 tokens, 64 rows, superblock) products, 32 for each SIMD, take short workgroups without staging (64 x 2048 x
-// 2048, 2048 products: 6.5 us against 10.2; at 32768: 1024 x 2048 x 2048 25.6 against 26.9, 128 x 16384 x 2048 24.8
-// against 25.5, 256 x 2048 x 8192 21.7 against 21.2; past it 1024 x 4096 x 2048 42 against 29.5).
+// Prompts of few (16 tokens, 64 rows, superblock) products, 32 for each SIMD, take short workgroups without staging
+// (64 x 2048 x 2048, 2048 products: 6.4 us against 10.2; at 32768: 1024 x 2048 x 2048 25.9 against 26.9, 128 x 16384 x
+// 2048 24.0 against 25.5, 256 x 2048 x 8192 21.1 against 21.2; past it 1024 x 4096 x 2048 42 against 29.5).
 constexpr int64_t kLinearTiles = 32768;
 constexpr int kLinearTileRows = 64;
 
@@ -980,8 +980,8 @@ GemmPlan plan_linear(int64_t n, int64_t k, int gran, int group_size, int64_t m) 
   }
   if (p.splits == 1) return p;
   // Splits of K, whose finishing pass costs more than the product's: past one workgroup a CU only while a split keeps 8
-  // superblocks (one split more of 4 took 22.6 us against 20.7 at 517 x 2048 x 2048, of 16 33.4 against 39.6 at 517 x
-  // 2048 x 8192).  Never more than the product's own.
+  // superblocks (in this kernel one split more, of 4, took 22.6 us against 20.7 at 517 x 2048 x 2048; of 16, 33.4
+  // against 39.6 at 517 x 2048 x 8192).  Never more than the product's own.
   const int64_t chunk = gemm_chunk_rows(k), mc = chunk > 0 && m > chunk ? chunk : m, nsb = k / kSuperblock;
   const int64_t tiles = (mc + p.tile_m - 1) / p.tile_m * ((n + p.tile_n - 1) / p.tile_n);
   int splits = 1;
