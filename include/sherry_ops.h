@@ -199,8 +199,8 @@ typedef enum {
  *   residual [tokens, N or N/2] bf16 or NULL (res_scale 1).  y (bf16) may be residual; outputs that overlap it
  *            otherwise, or x, return SHERRY_ERR_ARG.
  *   bias, and gemv's residual and y, need their element's alignment, gemm's residual 8-byte, the rest 16-byte.
- *   Without bias, activation, gate and residual gemm is sherry_gemm.  gemm's workspace is at most that of
- *   sherry_gemm: sherry_workspace_bytes(SHERRY_OP_GEMM, n, k, .., m, 1).
+ *   Without bias, activation, gate and residual gemm is sherry_gemm.  gemm takes sherry_gemm's workspace:
+ *   sherry_workspace_bytes(SHERRY_OP_GEMM, n, k, .., m, 1).
  */
 int32_t sherry_linear_gemv(int64_t n, int64_t k, int32_t granularity, int32_t group_size, const void* packed,
                            const float* alpha, const void* x, int32_t batch, void* y, int32_t y_dtype,

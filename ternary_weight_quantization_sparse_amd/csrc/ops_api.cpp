@@ -387,19 +387,21 @@ int32_t sherry_linear_gemm(int64_t n, int64_t k, int32_t granularity, int32_t gr
                               activation, gated, residual, res_scale);
   if (st != SHERRY_OK) return st;
   if (!aligned16(y) || !multiple_of(residual, 8)) return SHERRY_ERR_ALIGN;
+  // the product's workspace, whichever kernel runs: its callers size it by that
+  const GemmPlan own = plan_gemm(n, k, granularity, group_size, m, true);
+  if (own.workspace_bytes > 0 && (!workspace || workspace_bytes < own.workspace_bytes)) return SHERRY_ERR_WORKSPACE;
+  if (own.workspace_bytes > 0 && !aligned16(workspace)) return SHERRY_ERR_ALIGN;
   // nothing after the product: its own kernels and results
   const bool bare = !bias && !residual && !gated && activation == SHERRY_ACT_NONE;
-  const GemmPlan plan = bare ? plan_gemm(n, k, granularity, group_size, m, true) : plan_linear(n, k, granularity, group_size, m);
-  if (plan.workspace_bytes > 0 && (!workspace || workspace_bytes < plan.workspace_bytes)) return SHERRY_ERR_WORKSPACE;
-  if (plan.workspace_bytes > 0 && !aligned16(workspace)) return SHERRY_ERR_ALIGN;
   if (bare)
-    return hip_status(launch_gemm(plan, n, k, granularity, group_size, static_cast<const uint8_t*>(packed), alpha,
+    return hip_status(launch_gemm(own, n, k, granularity, group_size, static_cast<const uint8_t*>(packed), alpha,
                                   static_cast<const uint16_t*>(x), m, static_cast<uint16_t*>(y),
                                   static_cast<float*>(workspace), static_cast<hipStream_t>(stream)));
   const LinearArgs a{static_cast<const uint8_t*>(packed), alpha, n, k, granularity, group_sbs_of(granularity, group_size),
                      bias, bias_dtype == SHERRY_BF16, activation, gated != 0, static_cast<const uint16_t*>(residual),
                      res_scale};
-  return hip_status(launch_linear_gemm(plan, a, static_cast<const uint16_t*>(x), m, static_cast<uint16_t*>(y),
+  return hip_status(launch_linear_gemm(plan_linear(n, k, granularity, group_size, m), a,
+                                       static_cast<const uint16_t*>(x), m, static_cast<uint16_t*>(y),
                                        static_cast<float*>(workspace), static_cast<hipStream_t>(stream)));
 }
 
