@@ -122,6 +122,17 @@ def test_linear_in_a_graph(tokens, n, k, gated):
     replays(lambda x, r: [f(pw, x, bias=b, activation="gelu", gated=gated, residual=r)], fresh(0), fresh)
 
 
+@pytest.mark.parametrize("tokens,n,k,gated", [(260, 2050, 8192, False), (2050, 4096, 1024, True)])
+def test_long_prompt_in_a_graph(tokens, n, k, gated):
+    """The kernel of many tiles, with K split and not."""
+    gen = torch.Generator(device=DEV).manual_seed(tokens)
+    pw, b = S.quantize_pack(rand(gen, n, k) * 0.02), rand(gen, n)
+
+    def fresh(i):
+        return [rand(gen, tokens, k, dtype=BF16), rand(gen, tokens, n // 2 if gated else n, dtype=BF16)]
+    replays(lambda x, r: [S.linear_gemm(pw, x, bias=b, activation="silu", gated=gated, residual=r)], fresh(0), fresh)
+
+
 @pytest.mark.parametrize("tokens,experts,top_k,dim,hidden", [(1, 8, 2, 512, 1024), (16, 40, 4, 2048, 512), (5, 200, 8, 256, 256)])
 def test_experts_in_a_graph(tokens, experts, top_k, dim, hidden):
     """The experts in use change from replay to replay."""
