@@ -97,15 +97,16 @@ def _backward(layout, g, logits, ids, stats, temperature, labels, kd_weight, out
     vocab, _, slots, code, ids_64, labels_64 = layout
     flat, rows, stride = _rows(logits, vocab)
     if out is None:
-        out = _torch().empty(logits.shape, dtype=logits.dtype, device=logits.device)
-    place, _, out_stride = _rows(out, vocab)
-    if place.data_ptr() != out.data_ptr():
-        raise ValueError("out must have rows of consecutive elements at one distance")
+        out, out_stride = logits.new_empty(logits.shape), vocab
+    else:
+        place, _, out_stride = _rows(out, vocab)
+        if place.data_ptr() != out.data_ptr():
+            raise ValueError("out must have rows of consecutive elements at one distance")
     g, ids, labels = _contiguous(g), _contiguous(ids), _contiguous(labels)
     if rows:
         check(load().sherry_distill_loss_backward(
             rows, vocab, g.data_ptr(), flat.data_ptr(), stride, code, ids.data_ptr(), ids_64, slots, temperature,
-            _ptr(labels), labels_64, kd_weight, stats.data_ptr(), place.data_ptr(), out_stride, _stream(stream)))
+            _ptr(labels), labels_64, kd_weight, stats.data_ptr(), out.data_ptr(), out_stride, _stream(stream)))
     return out
 
 
