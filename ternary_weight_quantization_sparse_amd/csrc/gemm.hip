@@ -968,7 +968,7 @@ hipError_t launch_gemm_adapted(const GemmPlan& p, int64_t n, int64_t k, int gran
 constexpr int64_t kLinearTiles = 32768;
 constexpr int kLinearTileRows = 64;
 
-GemmPlan plan_linear(int64_t n, int64_t k, int gran, int group_size, int64_t m) {
+GemmPlan plan_linear(int64_t n, int64_t k, int gran, int group_size, int64_t m, bool gated) {
   GemmPlan p = plan_gemm(n, k, gran, group_size, m, true);
   if (m < (int64_t)1 << 24 && m * k < (int64_t)1 << 30 &&
       (m + 15) / 16 * ((n + 63) / 64) * (k / kSuperblock) <= kLinearTiles) {
@@ -978,11 +978,20 @@ GemmPlan plan_linear(int64_t n, int64_t k, int gran, int group_size, int64_t m) 
     p.workspace_bytes = 0;
     return p;
   }
+  const int64_t chunk = gemm_chunk_rows(k), mc = chunk > 0 && m > chunk ? chunk : m, nsb = k / kSuperblock;
+  if (p.tile_n == 256) {
+    // Wide tiles only where they fill their 512 places (two workgroups a CU) in every round, and past one round where
+    // K is long or the product gated, so that the epilogue counts little.  With bias, silu and residual 1024 x 8192 x
+    // 2048, 512 tiles, gated 43.7 us against 51.3 in narrow ones (which run three a CU), 2048 x 4096 x 8192 131 against
+    // 151, 2048 x 16384 x 2048 gated without bias and residual 131 against 136; but 517 x 16384 x 2048, 576 tiles, 95.9
+    // against 61.7, 1300 x 8192 x 4096 137 against 109, 2048 x 16384 x 2048 201 against 182.
+    const int64_t tiles = (mc + p.tile_m - 1) / p.tile_m * ((n + 255) / 256), places = (tiles + 511) / 512 * 512;
+    if (tiles * 10 < places * 9 || (tiles > 512 && k < 4096 && !gated)) p.tile_n = 128;
+  }
   if (p.splits == 1) return p;
   // Splits of K, whose finishing pass costs more than the product's: past one workgroup a CU only while a split keeps 8
   // superblocks (in this kernel one split more, of 4, took 22.6 us against 20.7 at 517 x 2048 x 2048; of 16, 33.4
   // against 39.6 at 517 x 2048 x 8192).  Never more than the product's own.
-  const int64_t chunk = gemm_chunk_rows(k), mc = chunk > 0 && m > chunk ? chunk : m, nsb = k / kSuperblock;
   const int64_t tiles = (mc + p.tile_m - 1) / p.tile_m * ((n + p.tile_n - 1) / p.tile_n);
   int splits = 1;
   while (splits < p.splits && (tiles * splits < 256 || nsb / (2 * splits) >= 8)) splits *= 2;

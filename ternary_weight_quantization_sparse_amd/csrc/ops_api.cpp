@@ -400,7 +400,7 @@ int32_t sherry_linear_gemm(int64_t n, int64_t k, int32_t granularity, int32_t gr
   const LinearArgs a{static_cast<const uint8_t*>(packed), alpha, n, k, granularity, group_sbs_of(granularity, group_size),
                      bias, bias_dtype == SHERRY_BF16, activation, gated != 0, static_cast<const uint16_t*>(residual),
                      res_scale};
-  return hip_status(launch_linear_gemm(plan_linear(n, k, granularity, group_size, m), a,
+  return hip_status(launch_linear_gemm(plan_linear(n, k, granularity, group_size, m, gated != 0), a,
                                        static_cast<const uint16_t*>(x), m, static_cast<uint16_t*>(y),
                                        static_cast<float*>(workspace), static_cast<hipStream_t>(stream)));
 }

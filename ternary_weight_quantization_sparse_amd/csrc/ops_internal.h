@@ -232,7 +232,7 @@ struct LinearArgs {
 hipError_t launch_linear_decode(const LinearArgs& a, const uint16_t* x, int tokens, void* y, bool y_bf16,
                                 hipStream_t s);
 hipError_t launch_linear_tiles(const LinearArgs& a, const uint16_t* x, int64_t m, uint16_t* y, hipStream_t s);
-GemmPlan plan_linear(int64_t n, int64_t k, int gran, int group_size, int64_t m);
+GemmPlan plan_linear(int64_t n, int64_t k, int gran, int group_size, int64_t m, bool gated);
 hipError_t launch_linear_gemm(const GemmPlan& p, const LinearArgs& a, const uint16_t* x, int64_t m, uint16_t* y,
                               float* ws, hipStream_t s);
 

@@ -164,6 +164,15 @@ def test_prompts_of_many_tiles(tokens, n, k, grain, gated):
     check(pw, x, b, "silu", gated, res)
 
 
+@pytest.mark.parametrize("grain", ["per_group", "per_channel", "per_tensor"])
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("tokens,n,k", [(1024, 8190, 640), (1000, 8002, 640), (2048, 8190, 4096)])
+def test_prompts_of_wide_tiles(tokens, n, k, grain, gated):
+    """Wide tiles in one full round and in two."""
+    pw, x, b, res = make(tokens, n, k, grain, gated=gated)
+    check(pw, x, b, "gelu", gated, res)
+
+
 @pytest.mark.parametrize("tokens,n,k", [(1024, 2048, 2048), (1024, 2050, 2048), (17, 64, 128), (31, 66, 8192), (255, 1002, 384),
                                         (4096, 128, 2048)])
 def test_prompts_of_few_tiles(tokens, n, k):
