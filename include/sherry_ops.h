@@ -232,7 +232,7 @@ size_t sherry_moe_workspace_bytes(int32_t tokens, int64_t dim, int64_t hidden, i
  *            [experts + shared][sherry_num_scales]; the shared experts, which every token meets with the weight 1,
  *            are the last.  down the same for [dim, hidden].
  *   residual [tokens, dim] bf16 or NULL; y [tokens, dim] SHERRY_BF16 or SHERRY_F32; y may be residual (bf16) or x.
- *   h is kept as two bf16 terms (2^-17 of it); sums are fp32 in an order fixed by the sizes and the choices.
+ *   h is kept in fp32's 24 bits; sums are fp32 in an order fixed by the sizes and the choices.
  *   dim, hidden multiples of 128, at most 65536; experts 1 .. 512, top_k 1 .. min(16, experts), shared 0 .. 4.
  *   No token's values reach another's result, nor does an expert's scale that is not finite reach a token that it
  *   does not serve; but the order of its sums follows the experts that the batch uses.

@@ -142,6 +142,20 @@ __device__ inline void load_tokens(__amdgpu_buffer_rsrc_t x, uint32_t at, u32x4 
   for (int t = 0; t < 4; ++t) xf[t] = __builtin_amdgcn_raw_buffer_load_b128(x, at + 64u * t, 0, 0);
 }
 
+// v as the sum of bf16 terms, fp32's 24 bits: what lies beyond the largest bf16 stays finite, infinities and NaN have no
+// further terms.
+constexpr int kTerms = 3;
+__device__ inline void split_terms(float v, __bf16 (&term)[kTerms]) {
+  const bool finite = __builtin_isfinite(v);
+#pragma unroll
+  for (int t = 0; t < kTerms; ++t) {
+    uint16_t h = __builtin_bit_cast(uint16_t, (__bf16)v);
+    if (t == 0 && finite && (h & 0x7FFF) == 0x7F80) h -= 1;
+    term[t] = __builtin_bit_cast(__bf16, t == 0 || finite ? h : (uint16_t)0);
+    v -= __uint_as_float((uint32_t)h << 16);
+  }
+}
+
 // A row's scale times the tokens' weights of an expert; One: no weights.  A weight of zero (a token that the expert
 // does not serve) gives zero also where the scale is not finite: that is what the legacy product is for, at an
 // ordinary one's cost (a comparison and selections took 0.4 us of moe_down's 13).
@@ -706,7 +720,8 @@ __global__ __launch_bounds__(64 * kRouteWaves) void moe_route(MoeArgs a) {
 }
 
 // First products and the activation: h[token, place] of the blockIdx.y-th expert in use, for its tokens. h is kept as
-// two bf16 terms (16 bits, 2^-17 of the value, beside y's 2^-9 or the float32 sums'). 16 tokens, 56 of 64 experts of
+// three bf16 terms, which together are the fp32 value: two (2^-17 of it) left a float32 y 2.5e-6 from its definition,
+// three 2.2e-7 (16 tokens, 8 of 64 experts). 16 tokens, 56 of 64 experts of
 // 2048 x 2 x 1024, 43 MB: 15.7 us (2.7 TB/s).  Of that the LDS lookups take 6 us; without any product it takes 13,
 // without the records' loads 12: no single one of them bounds it.
 template <int TR, int WAVES, bool GATED, int XS, bool OWN>
@@ -760,18 +775,18 @@ __global__ __launch_bounds__(64 * WAVES) void moe_up(MoeArgs a) {
     if (to_place < 0) continue;
     float z = activate(wave_sums<TR, WAVES>(part, which, token, c), a.activation);
     if constexpr (GATED) z *= wave_sums<TR, WAVES>(part, kOut + which, token, c);
-    const __bf16 hi = (__bf16)z;
-    const float rest = z - (float)hi;
+    __bf16 term[kTerms];
+    split_terms(z, term);
     const int64_t to = ((int64_t)token * a.slots + to_place) * a.hidden + tile * (16 * kOut) + which * 16 + c;
-    a.h[to] = hi;
-    a.h[a.h_plane + to] = __builtin_isfinite(rest) ? (__bf16)rest : (__bf16)0.f;
+#pragma unroll
+    for (int t = 0; t < kTerms; ++t) a.h[t * a.h_plane + to] = term[t];
   }
 }
 
 // Second products, weighted and added over the experts in use: TR row tiles of y, one of gridDim.y ranges of the
 // (expert, superblock) items; the waves share a range evenly.  A token's row of the A operand is its h of the expert
 // at hand, or zeros.  Several ranges leave fp32 partials for moe_join. 16 tokens, 56 experts of 1024 x 2048, 25 MB:
-// 13.4 us (1.9 TB/s), each item's h (two terms of 4 KB) beside the weights' 11 KB.
+// 15.7 us (1.6 TB/s; with two terms of h 13.4), each item's h (three terms of 4 KB) beside the weights' 11 KB.
 __device__ inline void store_moe(const MoeArgs& a, int64_t to, float s, void* y, bool y_bf16) {
   if (a.residual) s += bf16_to_f32(a.residual[to]);
   if (y_bf16) static_cast<__bf16*>(y)[to] = (__bf16)s;
@@ -805,8 +820,8 @@ __global__ __launch_bounds__(64 * WAVES) void moe_down(MoeArgs a, void* __restri
   f32x4 acc[TR];
 #pragma unroll
   for (int i = 0; i < TR; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-  const auto h = buffer(a.h, (uint32_t)(2 * a.h_plane * 2));
-  run_items<TR, 2, 1, 1>(
+  const auto h = buffer(a.h, (uint32_t)(kTerms * a.h_plane * 2));
+  run_items<TR, kTerms, 1, 1>(
       i0 + (i1 - i0) * wave / WAVES, i0 + (i1 - i0) * (wave + 1) / WAVES, reinterpret_cast<const char*>(dtab), q,
       [&](int j, bool live, Records<TR>& rec) {
         const int e = __builtin_amdgcn_readfirstlane(list[j / sbs - a0]);
@@ -814,12 +829,13 @@ __global__ __launch_bounds__(64 * WAVES) void moe_down(MoeArgs a, void* __restri
                                 a.down_group_sbs);
         if (live) rec.load(block(p, j % sbs), row, p.row_step, q);
       },
-      [&](int j, bool live, u32x4 (&xf)[2][4]) {
+      [&](int j, bool live, u32x4 (&xf)[kTerms][4]) {
         const int s = place[j / sbs - a0][r];
         const uint32_t from = (uint32_t)((r * a.slots + s) * a.hidden + j % sbs * kSuperblock + 8 * q) * 2u;
         if (!live) return;
-        load_tokens(h, s >= 0 ? from : kNowhere, xf[0]);
-        load_tokens(h, s >= 0 ? from + (uint32_t)a.h_plane * 2u : kNowhere, xf[1]);
+#pragma unroll
+        for (int t = 0; t < kTerms; ++t)
+          load_tokens(h, s >= 0 ? from + t * (uint32_t)a.h_plane * 2u : kNowhere, xf[t]);
       },
       [&](int j) { return *reinterpret_cast<const f32x4*>(&weight[j / sbs - a0][4 * q]); }, acc);
 #pragma unroll
@@ -937,7 +953,7 @@ MoePlan plan_moe(int tokens, int64_t dim, int64_t hidden, int experts, int share
   const int64_t read = (experts * (router_bf16 ? 2 : 4) + tokens * 2) * dim;
   p.parts = experts <= 64 && read <= kRouteBytes ? 0 : (int)std::min<int64_t>(kMoeParts, (dim + 511) / 512);
   p.h_offset = p.logits_offset + up((size_t)p.parts * tokens * experts * 4);
-  p.partial_offset = p.h_offset + up((size_t)p.h_plane * 4);
+  p.partial_offset = p.h_offset + up((size_t)p.h_plane * 2 * kTerms);
   p.workspace_bytes = p.partial_offset + (p.ranges > 1 ? up((size_t)p.ranges * tokens * dim * 4) : 0);
   return p;
 }

@@ -263,7 +263,7 @@ struct MoeArgs {
   MoeRoute* route;
   float* logits;                               // [parts][tokens, experts]
   int parts;                                   // 0: the routing makes them itself
-  __bf16* h;                                   // [2][tokens, slots, hidden]
+  __bf16* h;                                   // [bf16 terms][tokens, slots, hidden]
   int64_t h_plane;
   float* partial;                              // [ranges][tokens, dim]
   int ranges;

@@ -323,3 +323,64 @@ def test_refusals():
         with pytest.raises(ValueError):
             S.moe_decode(**{**args, **bad})
     assert S.moe_decode(**args).shape == (3, 256)
+
+
+def exact_layer(total, n, k, active, gen, grain="per_channel"):
+    """Packed weights whose rows have the scale 1, and of each weight only ``active`` rows: sums of integers."""
+    p = S.quantize_pack_experts(rand(gen, total, n, k), grain)
+    p.alpha.zero_()
+    for e in range(total):
+        p.alpha[e, torch.randperm(n, generator=gen, device=DEV)[:active]] = 1
+    return p
+
+
+@pytest.mark.parametrize("tokens,experts,top_k,dim,hidden", [(1, 1, 1, 128, 128), (1, 6, 1, 256, 1152), (7, 4, 1, 128, 8192),
+                                                             (16, 70, 1, 128, 512)])
+@pytest.mark.parametrize("gated", [False, True])
+def test_hidden_values_keep_24_bits(tokens, experts, top_k, dim, hidden, gated):
+    """Integers of up to 20 and more bits that no sum rounds (their magnitudes add up to less than 2^24), so fp32 results
+    are exact: h held in 16 bits would be off by whole units."""
+    layer = Layer(experts, dim, hidden, gated=gated)
+    gen = layer.gen
+    layer.up = exact_layer(experts, (2 if gated else 1) * hidden, dim, hidden if gated else 32, gen)
+    layer.down = exact_layer(experts, dim, hidden, dim, gen)
+    if gated:       # 24 hidden values of which both factors count
+        layer.up.alpha.zero_()
+        for e in range(experts):
+            at = torch.randperm(hidden, generator=gen, device=DEV)[:24]
+            layer.up.alpha[e, at], layer.up.alpha[e, hidden + at] = 1, 1
+    top = 8 if gated else 17
+    power = torch.randint(0, top, (tokens, dim), generator=gen, device=DEV)
+    power[:, 64:] = 0       # (64 of the channels large, whatever dim is)
+    sign = torch.randint(0, 2, (tokens, dim), generator=gen, device=DEV) * 2.0 - 1
+    x = (sign * torch.exp2(power.float())).to(BF16)
+    y = S.moe_decode(x, layer.router, layer.up, layer.down, top_k, activation="none", y_dtype="float32")
+    chosen = (x.double() @ layer.router.double().t().contiguous()).argmax(1)
+    bits = 0
+    for t in range(tokens):
+        up, down = layer.dense(layer.up, int(chosen[t])), layer.dense(layer.down, int(chosen[t]))
+        z = up.mv(x[t].double())
+        h = z[:hidden] * z[hidden:] if gated else z
+        assert h.abs().sum() < 2 ** 24 and up.abs().mv(x[t].double().abs()).max() < 2 ** 24
+        bits = max(bits, float((h.abs() / torch.exp2(torch.floor(torch.log2(h.abs().clamp(min=1)) - 16)) % 1).max()))
+        assert torch.equal(y[t].double(), down.mv(h))
+    assert bits > 0       # some have more than 17
+
+
+def test_hidden_values_beyond_bfloat16():
+    """A finite h past the largest bf16 (3.39e38) stays finite."""
+    layer = Layer(2, 128, 128, gated=False)
+    for e in range(2):
+        layer.up.alpha[e], layer.down.alpha[e] = 1, 2.0 ** -100
+    t = layer.dense(layer.up, 0)[5].sign()
+    x = torch.zeros(1, 128, dtype=BF16, device=DEV)
+    at = t.nonzero()[:2, 0]
+    x[0, at] = (t[at] * torch.tensor([255 * 2.0 ** -7, 255 * 2.0 ** -15], device=DEV)).to(BF16)
+    layer.router[:] = 0       # equal logits: the first one
+    layer.up.alpha[0, 5] = 2.0 ** 127
+    h = layer.dense(layer.up, 0).mv(x[0].double())
+    assert torch.finfo(BF16).max * (1 + 2.0 ** -9) < h[5] < torch.finfo(F32).max
+    y = S.moe_decode(x, layer.router, layer.up, layer.down, 1, activation="none", y_dtype="float32")
+    want = layer.dense(layer.down, 0).mv(h)
+    # a sum of which one term is of the order of 2^27 and the others are below it: by steps of fp32
+    assert ((y[0].double() - want).abs() <= 2.0 ** -22 * 2.0 ** 28).all() and y.isfinite().all()
