@@ -157,8 +157,8 @@ size_t sherry_distill_workspace_bytes(int64_t rows, int64_t vocab, int32_t dtype
  *   loss     [rows] fp32.  stats [rows, 6 + slots] fp32 for the backward pass, or NULL.
  *   A kd_weight of 0 (1) leaves the first (second) term out, whatever it is.
  *   rows 1 .. 2^31 - 1, vocab 1 .. 2^30, slots 1 .. 1024, temperature 1e-3 .. 1e3; pointers need
- *   their element's alignment (16-byte aligned rows are not needed for 16-byte loads).  Sums and logarithms of a
- *   row are taken in 64 bits.
+ *   their element's alignment (16-byte aligned rows are not needed for 16-byte loads).  Single exponentials
+ *   and sums of 16 bytes of logits are fp32, a row's sums past those and its logarithms are taken in 64 bits.
  */
 int32_t sherry_distill_loss(int64_t rows, int64_t vocab, const void* logits, int64_t row_stride, int32_t dtype,
                             const void* teacher, int32_t teacher_dtype, const void* ids, int32_t ids_64,

@@ -13,7 +13,7 @@
 // HBM bounds both directions: the forward pass reads the logits once (running maximum and sums), the backward pass
 // reads them once more and writes the gradient: 2048 x 128000 bf16 with 64 slots 89 us (5.9 TB/s) + 12 us (the rows'
 // losses) and 207 us (5.1 TB/s), 300 us together; three passes at a copy's 5.2 TB/s take 302.
-// Everything that belongs to a row (sums over threads, logarithms, the teacher's probabilities) is in 64 bits: the
+// Everything that belongs to a row (sums past a 16-byte group, logarithms, the teacher's probabilities) is in 64 bits: the
 // loss is a difference of terms of its own size or larger.
 #include <algorithm>
 #include <cfloat>
@@ -116,9 +116,11 @@ __device__ inline double wave_max(double v) {
 // One range of a row: its maximum m, sum of exp((s - m) / t) and with SOFT1 the
 // sum of exp(s - m).  TAIL: of the elements outside the ids, which a bitmap of
 // the range marks in LDS; so the tail is never a difference of sums, and it has a maximum of its own, however
-// far below the ids it lies.  A thread rescales its sums when its maximum rises, once per four
-// groups; threads and waves join in 64 bits.  The maximum starts at the
-// lowest finite value, so that ranges of -infinity add zeros.
+// far below the ids it lies.  A thread adds up a group in fp32 and the groups in
+// 64 bits: one fp32 sum over its whole share, 500 elements of 2048 x 128000, drops what lies 2^-24 below the
+// largest and always to the same side (a loss of 5.3e-3 came out 0.4% low).  It rescales its sums when its
+// maximum rises, once per four groups; threads and waves join in 64 bits.  The maximum starts at the lowest
+// finite value, so that ranges of -infinity add zeros.
 template <bool BF16, bool TAIL, bool SOFT1, bool STREAM>
 __global__ __launch_bounds__(kThreads) void distill_range(DistillArgs a, int64_t row0) {
   constexpr int L = kLane<BF16>, kAhead = 4;
@@ -148,7 +150,8 @@ __global__ __launch_bounds__(kThreads) void distill_range(DistillArgs a, int64_t
   }
   // log2(e) / t in two terms: rounded to one, every exponential of a far element would be off the same way
   const float c = a.exp_hi, c_lo = a.exp_lo;
-  float m = -FLT_MAX, s = 0.f, s1 = 0.f;
+  float m = -FLT_MAX;
+  double s = 0., s1 = 0.;
   auto drop_marked = [&](float (&x)[L], int64_t g) {
     if constexpr (TAIL) {
       const uint32_t p = (uint32_t)((g - g0) * L), mark = marks[p >> 5] >> (p & 31);
@@ -156,18 +159,23 @@ __global__ __launch_bounds__(kThreads) void distill_range(DistillArgs a, int64_t
       for (int i = 0; i < L; ++i) x[i] = (mark >> i) & 1u ? -INFINITY : x[i];
     }
   };
+  auto soft = [&](float d) { return __builtin_amdgcn_exp2f(fmaf(d, c, d * c_lo)); };
+  auto soft1 = [&](float d) { return __builtin_amdgcn_exp2f(d * kLog2e); };
   auto add = [&](const float (&x)[L]) {
+    float t = 0.f, t1 = 0.f;
 #pragma unroll
     for (int i = 0; i < L; ++i) {
       const float d = x[i] - m;
-      s += __builtin_amdgcn_exp2f(fmaf(d, c, d * c_lo));
-      if constexpr (SOFT1) s1 += __builtin_amdgcn_exp2f(d * kLog2e);
+      t += soft(d);
+      if constexpr (SOFT1) t1 += soft1(d);
     }
+    s += (double)t;
+    if constexpr (SOFT1) s1 += (double)t1;
   };
   auto raise = [&](float top) {
     if (top > m) {
-      s *= __builtin_amdgcn_exp2f((m - top) * c);
-      if constexpr (SOFT1) s1 *= __builtin_amdgcn_exp2f((m - top) * kLog2e);
+      s *= (double)soft(m - top);
+      if constexpr (SOFT1) s1 *= (double)soft1(m - top);
       m = top;
     }
   };
@@ -209,9 +217,9 @@ __global__ __launch_bounds__(kThreads) void distill_range(DistillArgs a, int64_t
       if (g + u * kThreads < w1) add(x[u]);
   }
   const float wmax = wave_max(m);
-  const double sum = wave_sum((double)s * (double)__builtin_amdgcn_exp2f((m - wmax) * c));
+  const double sum = wave_sum(s * (double)soft(m - wmax));
   double sum1 = 0.;
-  if constexpr (SOFT1) sum1 = wave_sum((double)s1 * (double)__builtin_amdgcn_exp2f((m - wmax) * kLog2e));
+  if constexpr (SOFT1) sum1 = wave_sum(s1 * (double)soft1(m - wmax));
   if ((tid & 63) == 0) {
     wm[tid >> 6] = wmax;
     ws[tid >> 6] = sum;
@@ -224,8 +232,8 @@ __global__ __launch_bounds__(kThreads) void distill_range(DistillArgs a, int64_t
     for (int w = 1; w < kThreads / 64; ++w) out.m = fmaxf(out.m, wm[w]);
 #pragma unroll
     for (int w = 0; w < kThreads / 64; ++w) {
-      out.s += ws[w] * (double)__builtin_amdgcn_exp2f((wm[w] - out.m) * c);
-      out.s1 += ws1[w] * (double)__builtin_amdgcn_exp2f((wm[w] - out.m) * kLog2e);
+      out.s += ws[w] * (double)soft(wm[w] - out.m);
+      out.s1 += ws1[w] * (double)soft1(wm[w] - out.m);
     }
     a.part[row * a.ranges + range] = out;
   }

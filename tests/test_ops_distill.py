@@ -385,3 +385,35 @@ def test_offsets_past_32_bits():
     q = torch.exp(s - total)
     assert torch.allclose(grad[4, [vocab - 1, 5]].cpu().double(), q - p, rtol=2.0 ** -8, atol=2.0 ** -18)
     assert abs(float(grad[4, 12345]) - float(torch.exp(-total))) <= 2.0 ** -8 * float(torch.exp(-total))
+
+
+@pytest.mark.parametrize("rows,vocab,dtype", [(2050, 128000, BF16), (2050, 64003, F32), (2100, 1 << 18, BF16)])
+@pytest.mark.parametrize("tail", [False, True])
+@pytest.mark.parametrize("tau", [1.0, 2.0])
+def test_confident_rows_in_long_ranges(rows, vocab, dtype, tail, tau):
+    """One range a row, so hundreds of elements a thread: one logit far above a flat rest, whose many small exponentials
+    are the loss.  At the row's start, in a thread's middle, in its last groups and at the row's end."""
+    z, u, ids, lse, y = make(rows, vocab, 6, dtype, tail, True, std=0.05, tau=tau)
+    some = list(range(0, rows, rows // 15))[:16]
+    for i, r in enumerate(some):
+        at = (0, vocab // 2, vocab - 2100, vocab - 1)[i % 4]
+        z[r, at] = (16.0, 18.0, 20.0, 36.0)[i // 4]
+        y[r] = at
+        if i % 8 < 4:          # the teacher agrees, or says other things
+            ids[r, 0], u[r, 0] = at, 12.0
+    args = (z, u, ids, tau, lse, y, 0.4)
+    loss, stats = S.distill_loss(*args, with_stats=True)
+    g = torch.linspace(0.3, 1.0, rows, device=DEV)
+    grad = S.distill_loss_backward(g, z, ids, stats, tau, y, 0.4)
+    part = [t if t is None else t[some] for t in (z, u, ids, lse, y)]
+    want, tol, dwant, size = oracle(*part, tau, 0.4, g[some])
+    err = (loss[some].cpu().double() - want).abs()
+    assert (err <= tol).all(), (err / tol).max()
+    dtol = 2.0 ** -18 * size + torch.finfo(dtype).eps / 2 * dwant.abs() + 1e-36
+    err = (grad[some].cpu().double() - dwant).abs()
+    assert (err <= dtol).all(), (err / dtol).max()
+    # hard labels alone, whose loss is nothing but the rest's sum
+    loss = S.distill_loss(z, u, ids, tau, None, y, 0.0)
+    want, tol, _, _ = oracle(*part[:3], None, part[4], tau, 0.0, g[some])
+    err = (loss[some].cpu().double() - want).abs()
+    assert (err <= tol).all(), (err / tol).max()
