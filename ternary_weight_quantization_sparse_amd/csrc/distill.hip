@@ -25,7 +25,12 @@ namespace {
 
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
-constexpr float kLog2e = 1.4426950408889634f;
+// log2(e) / t in two terms: rounded to one, every exponential of a far element would be off the same way.  The upper
+// one is the next below, so that both are above zero and a distance of -infinity stays one.
+constexpr float kLog2e = 1.44269502f, kLog2eRest = (float)(1.4426950408889634 - (double)kLog2e);
+static_assert(kLog2eRest > 0.f, "the upper term lies below log2(e)");
+__device__ inline float exp_below(float d, float c, float rest) { return __builtin_amdgcn_exp2f(fmaf(d, c, d * rest)); }
+__device__ inline float exp_below(float d) { return exp_below(d, kLog2e, kLog2eRest); }   // t = 1
 constexpr int kThreads = 256;
 constexpr int kStatHead = kDistillHead;   // a row's statistics before its slots
 
@@ -148,8 +153,6 @@ __global__ __launch_bounds__(kThreads) void distill_range(DistillArgs a, int64_t
     }
     __syncthreads();
   }
-  // log2(e) / t in two terms: rounded to one, every exponential of a far element would be off the same way
-  const float c = a.exp_hi, c_lo = a.exp_lo;
   float m = -FLT_MAX;
   double s = 0., s1 = 0.;
   auto drop_marked = [&](float (&x)[L], int64_t g) {
@@ -159,15 +162,14 @@ __global__ __launch_bounds__(kThreads) void distill_range(DistillArgs a, int64_t
       for (int i = 0; i < L; ++i) x[i] = (mark >> i) & 1u ? -INFINITY : x[i];
     }
   };
-  auto soft = [&](float d) { return __builtin_amdgcn_exp2f(fmaf(d, c, d * c_lo)); };
-  auto soft1 = [&](float d) { return __builtin_amdgcn_exp2f(d * kLog2e); };
+  auto soft = [&](float d) { return exp_below(d, a.exp_hi, a.exp_lo); };
   auto add = [&](const float (&x)[L]) {
     float t = 0.f, t1 = 0.f;
 #pragma unroll
     for (int i = 0; i < L; ++i) {
       const float d = x[i] - m;
       t += soft(d);
-      if constexpr (SOFT1) t1 += soft1(d);
+      if constexpr (SOFT1) t1 += exp_below(d);
     }
     s += (double)t;
     if constexpr (SOFT1) s1 += (double)t1;
@@ -175,7 +177,7 @@ __global__ __launch_bounds__(kThreads) void distill_range(DistillArgs a, int64_t
   auto raise = [&](float top) {
     if (top > m) {
       s *= (double)soft(m - top);
-      if constexpr (SOFT1) s1 *= (double)soft1(m - top);
+      if constexpr (SOFT1) s1 *= (double)exp_below(m - top);
       m = top;
     }
   };
@@ -219,7 +221,7 @@ __global__ __launch_bounds__(kThreads) void distill_range(DistillArgs a, int64_t
   const float wmax = wave_max(m);
   const double sum = wave_sum(s * (double)soft(m - wmax));
   double sum1 = 0.;
-  if constexpr (SOFT1) sum1 = wave_sum(s1 * (double)soft1(m - wmax));
+  if constexpr (SOFT1) sum1 = wave_sum(s1 * (double)exp_below(m - wmax));
   if ((tid & 63) == 0) {
     wm[tid >> 6] = wmax;
     ws[tid >> 6] = sum;
@@ -233,7 +235,7 @@ __global__ __launch_bounds__(kThreads) void distill_range(DistillArgs a, int64_t
 #pragma unroll
     for (int w = 0; w < kThreads / 64; ++w) {
       out.s += ws[w] * (double)soft(wm[w] - out.m);
-      out.s1 += ws1[w] * (double)soft1(wm[w] - out.m);
+      out.s1 += ws1[w] * (double)exp_below(wm[w] - out.m);
     }
     a.part[row * a.ranges + range] = out;
   }
@@ -415,8 +417,8 @@ __global__ __launch_bounds__(kThreads) void distill_grad(DistillGrad a, int64_t 
   const float m = st[0], off = st[1] * gr, c1 = st[2] * gr, top = st[3], at = st[4] * gr, c2 = st[5] * gr;
   auto value = [&](float x, float reference, float f, float f1) {
     const float d = x - reference;
-    float r = f == 0.f ? 0.f : f * __builtin_amdgcn_exp2f(fmaf(d, a.exp_hi, d * a.exp_lo));
-    if constexpr (SOFT1) r += f1 == 0.f ? 0.f : f1 * __builtin_amdgcn_exp2f(d * kLog2e);
+    float r = f == 0.f ? 0.f : f * exp_below(d, a.exp_hi, a.exp_lo);
+    if constexpr (SOFT1) r += f1 == 0.f ? 0.f : f1 * exp_below(d);
     return r;
   };
 

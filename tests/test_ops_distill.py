@@ -417,3 +417,21 @@ def test_confident_rows_in_long_ranges(rows, vocab, dtype, tail, tau):
     want, tol, _, _ = oracle(*part[:3], None, part[4], tau, 0.0, g[some])
     err = (loss[some].cpu().double() - want).abs()
     assert (err <= tol).all(), (err / tol).max()
+
+
+def test_label_exponentials_of_far_elements():
+    """The label's softmax is as exact far below the largest logit as near it: log2(e) rounded to one fp32 term (1.3e-8 of
+    itself too small) would make elements 16 to 20 below 2.1e-7 of themselves larger than ones 0 to 4 below, on the
+    average.  What remains: roundings of an exponent (below 32, so 2^-20 ln 2, by chance: divided by the root of 20000
+    elements 5e-9), and the exponential's own last place and the row's factor, which are the same near and far."""
+    gen = torch.Generator(device=DEV).manual_seed(4)
+    z = torch.rand(1, 40000, generator=gen, device=DEV) * 4
+    z[0, 20000:] -= 16
+    z[0, 0] = 4
+    ids = torch.zeros(1, 1, dtype=torch.int32, device=DEV)
+    y = torch.tensor([[1]], device=DEV).reshape(1)
+    loss, stats = S.distill_loss(z, torch.zeros(1, 1, device=DEV), ids, 2.0, None, y, 0.0, with_stats=True)
+    grad = S.distill_loss_backward(torch.ones(1, device=DEV), z, ids, stats, 2.0, y, 0.0)
+    q = z.cpu().double().softmax(1)      # (on the host: the device's softmax in 64 bits is off by 2e-7 the same way)
+    off = (grad.cpu().double() / q - 1)[0]
+    assert abs(float(off[20000:].mean() - off[2:20000].mean())) <= 2.0 ** -23
