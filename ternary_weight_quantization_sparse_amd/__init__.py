@@ -93,6 +93,13 @@ def _need_out(t, name, dtype, numel, device):
         raise ValueError(f"{name} holds {t.numel()} elements, {numel} needed")
 
 
+def _written(*tensors):
+    """The library writes through addresses, which autograd does not see: the
+    caller's tensors count as changed in place, so that a graph that saved one
+    refuses its backward pass as after any in-place operation."""
+    _torch().autograd.graph.increment_version(tensors)
+
+
 def _check_pw(pw):
     """Packed planes and scales of the sizes their shape implies."""
     torch = _torch()
@@ -205,6 +212,7 @@ def quantize_pack_noalloc(w, packed, alpha, granularity: str = "per_group", grou
     with torch.cuda.device(w.device):
         check(lib.sherry_quantize_pack_noalloc(n, k, gran, group_size, _ptr(w), dtype, _ptr(packed), _ptr(alpha),
                                                _stream(stream)))
+    _written(packed, alpha)
     return PackedWeight(packed[:nbytes], alpha[:nsc], n, k, granularity, group_size)
 
 
@@ -317,6 +325,8 @@ def gemv(pw: PackedWeight, x, y_dtype="bfloat16", stream=None, out=None):
         check(lib.sherry_gemv(pw.n, pw.k, gran, pw.group_size, _ptr(pw.packed), _ptr(pw.alpha), _ptr(x), b,
                               _ptr(y), code, 1, 0, 0, 0, _ptr(ws), 0 if ws is None else ws.numel(),
                               _stream(stream)))
+    if out is not None:
+        _written(out)
     return y
 
 
@@ -351,6 +361,8 @@ def arenas_gemm(pw: PackedWeight, w, lam: float, x, stream=None, out=None):
         check(lib.sherry_arenas_gemm(pw.n, pw.k, gran, pw.group_size, _ptr(pw.packed), _ptr(pw.alpha), _ptr(wb),
                                      float(lam), _ptr(x), m, _ptr(y), _ptr(ws), 0 if ws is None else ws.numel(),
                                      _stream(stream)))
+    if out is not None:
+        _written(out)
     return y
 
 
@@ -393,6 +405,7 @@ def compare_gemv(fmt: int, planes, alpha, n: int, k: int, x, count: int = 1, pla
             _need_out(y, "y", torch.bfloat16, (count - 1) * y_stride + n, dev)
         check(lib.sherry_compare_gemv(fmt, n, k, _ptr(planes), _ptr(alpha), _ptr(x), _ptr(y), count,
                                       planes_stride, alpha_stride, y_stride, _stream(stream)))
+    _written(y)
     return y
 
 
@@ -475,6 +488,7 @@ def gemv_batched(packed_all, alpha_all, n: int, k: int, x, count: int, packed_st
         check(lib.sherry_gemv(n, k, gran, group_size, _ptr(packed_all), _ptr(alpha_all), _ptr(x), b, _ptr(y),
                               code, count, packed_stride, alpha_stride, y_stride, _ptr(ws),
                               0 if ws is None else ws.numel(), _stream(stream)))
+    _written(y)
     return y
 
 
@@ -495,6 +509,8 @@ def gemm(pw: PackedWeight, x, stream=None, out=None):
         ws = _workspace(ws_bytes if ws_bytes != (1 << 64) - 1 else 0, dev)
         check(lib.sherry_gemm(pw.n, pw.k, gran, pw.group_size, _ptr(pw.packed), _ptr(pw.alpha), _ptr(x), m,
                               _ptr(y), _ptr(ws), 0 if ws is None else ws.numel(), _stream(stream)))
+    if out is not None:
+        _written(out)
     return y
 
 

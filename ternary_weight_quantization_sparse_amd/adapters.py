@@ -10,7 +10,7 @@ from __future__ import annotations
 from dataclasses import dataclass
 
 from . import (_activations, _check_pw, _gran, _need_gpu, _need_out, _on_stream, _ptr, _stream, _torch,
-               _workspace, _y_dtype)
+               _workspace, _written, _y_dtype)
 from ._lib import check, load
 
 
@@ -59,6 +59,8 @@ def _adapted(pw, x, ad, ids, decode, y_dtype, stream, out):
     head = (n, k, gran, pw.group_size, _ptr(pw.packed), _ptr(pw.alpha), _ptr(x), m, y.data_ptr())
     tail += (_ptr(ws), 0 if ws is None else nbytes, _stream(stream))
     check(lib.sherry_adapter_gemv(*head, code, *tail) if decode else lib.sherry_adapter_gemm(*head, *tail))
+    if out is not None:
+        _written(out)
     return y
 
 

@@ -14,7 +14,7 @@ held against the student's mass outside the ids.
 
 from __future__ import annotations
 
-from . import _lib, _need_current, _need_gpu, _on_stream, _ptr, _stream, _torch
+from . import _lib, _need_current, _need_gpu, _on_stream, _ptr, _stream, _torch, _written
 from ._lib import check, load
 
 
@@ -149,7 +149,10 @@ def distill_loss_backward(g, logits, ids, stats, temperature: float = 1.0, label
         if out is not None and (out.dtype != logits.dtype or out.shape != logits.shape or out.device != dev):
             _need_gpu(out, "out", dev)
             raise ValueError(f"out must be {logits.dtype} {tuple(logits.shape)}, got {out.dtype} {tuple(out.shape)}")
-        return _backward(layout, g, logits, ids, stats, temperature, labels, kd_weight, out, stream)
+        grad = _backward(layout, g, logits, ids, stats, temperature, labels, kd_weight, out, stream)
+        if out is not None:
+            _written(out)
+        return grad
 
 
 def _make_ad():

@@ -11,7 +11,7 @@ from __future__ import annotations
 
 from dataclasses import dataclass
 
-from . import _lib, _need_current, _need_gpu, _on_stream, _stream, _torch, _y_dtype, quantize_pack
+from . import _lib, _need_current, _need_gpu, _on_stream, _stream, _torch, _written, _y_dtype, quantize_pack
 from ._lib import check, load
 from .linear import _activation, _place, _planes, _rows
 
@@ -101,4 +101,6 @@ def _moe(x, router, up, down, top_k, shared, scoring, normalize, bias, scale, ac
         up.packed.data_ptr(), up.alpha.data_ptr(), up_gran, up.group_size, down.packed.data_ptr(),
         down.alpha.data_ptr(), down_gran, down.group_size, None if residual is None else residual.data_ptr(),
         y.data_ptr(), y_code, ws.data_ptr(), nbytes, _stream(stream)))
+    if out is not None:
+        _written(out)
     return y

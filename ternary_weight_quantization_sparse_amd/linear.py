@@ -10,7 +10,7 @@ with their rows [gate; values]:
 
 from __future__ import annotations
 
-from . import _gran, _lib, _need_current, _need_gpu, _on_stream, _stream, _torch, _y_dtype
+from . import _gran, _lib, _need_current, _need_gpu, _on_stream, _stream, _torch, _written, _y_dtype
 from ._lib import check, load
 
 _NONE = (1 << 64) - 1
@@ -106,11 +106,13 @@ def _linear(pw, x, bias, activation, gated, residual, res_scale, decode, y_dtype
     tail = (b, b_code, act, bool(gated), res, res_scale)
     if decode:
         check(lib.sherry_linear_gemv(*head, y_dtype[1], *tail, _stream(stream)))
-        return y
-    nbytes = lib.sherry_workspace_bytes(_lib.OP_GEMM, n, k, gran, pw.group_size, m, 1)
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if 0 < nbytes < _NONE else None
-    check(lib.sherry_linear_gemm(*head, *tail, None if ws is None else ws.data_ptr(), 0 if ws is None else nbytes,
-                                 _stream(stream)))
+    else:
+        nbytes = lib.sherry_workspace_bytes(_lib.OP_GEMM, n, k, gran, pw.group_size, m, 1)
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if 0 < nbytes < _NONE else None
+        check(lib.sherry_linear_gemm(*head, *tail, None if ws is None else ws.data_ptr(), 0 if ws is None else nbytes,
+                                     _stream(stream)))
+    if out is not None:
+        _written(out)
     return y
 
 

@@ -5,7 +5,7 @@ from __future__ import annotations
 
 import math
 
-from . import _lib, _need_gpu, _need_out, _on_stream, _ptr, _stream, _torch, _workspace
+from . import _lib, _need_gpu, _need_out, _on_stream, _ptr, _stream, _torch, _workspace, _written
 from ._lib import check, load
 
 #: Quintic coefficients (a, b, c) of X <- a X + (b A + c A A) X, A = X X^T: a
@@ -51,6 +51,8 @@ def orthogonalize(g, steps: int = 5, coeffs=None, eps: float = 1e-7, stream=None
         ws = _ws(count, n, k, g.device)
         check(load().sherry_orthogonalize(count, n, k, _ptr(src), code, _ptr(res), int(steps), *_coeffs(coeffs),
                                           float(eps), _ptr(ws), 0 if ws is None else ws.numel(), _stream(stream)))
+    if out is not None:
+        _written(out)
     return res
 
 
@@ -82,4 +84,6 @@ def muon_step(w, grad, buf, lr: float, momentum: float = 0.95, nesterov: bool = 
                                       float(lr), float(momentum), int(nesterov), float(weight_decay), float(scale),
                                       int(steps), *_coeffs(coeffs), float(eps), _ptr(work),
                                       0 if work is None else work.numel(), _stream(stream)))
+    if out is not None:
+        _written(w_out, buf_out)
     return w_out, buf_out
