@@ -2,15 +2,15 @@
 
     y = f(x (T alpha)^T + bias) + res_scale * residual
 
-or, for a gate and its values packed as one weight (`quantize_pack_fused`),
-with their rows [gate; values]:
+or, for a gate and its values packed as one weight (what `quantize_pack_fused`
+makes of the two, or a `PackedWeight` of their rows [gate; values]):
 
     y = f(z_gate) * z_values + res_scale * residual
 """
 
 from __future__ import annotations
 
-from . import _gran, _lib, _need_current, _need_gpu, _on_stream, _stream, _torch, _written, _y_dtype
+from . import FusedWeight, _gran, _lib, _need_current, _need_gpu, _on_stream, _stream, _torch, _written, _y_dtype
 from ._lib import check, load
 
 _NONE = (1 << 64) - 1
@@ -72,6 +72,10 @@ def _place(out, dtype, shape, dev, like):
 
 def _linear(pw, x, bias, activation, gated, residual, res_scale, decode, y_dtype, stream, out):
     torch = _torch()
+    if isinstance(pw, FusedWeight):
+        if gated and (len(pw.sizes) != 2 or pw.sizes[0] != pw.sizes[1]):
+            raise ValueError(f"a gated product needs two members of the same rows, a gate and its values, got {pw.sizes}")
+        pw = pw.pw
     packed, n, k = pw.packed, pw.n, pw.k
     dev = packed.device
     if not packed.is_cuda:
@@ -128,6 +132,7 @@ def linear_gemv(pw, x, bias=None, activation: str = "none", gated: bool = False,
     """The product of a decode batch ``x`` [B, K] bf16 (B = 1..16) with its epilogue, in one launch and with one
     rounding.
 
+    ``pw`` a `PackedWeight`, or a `FusedWeight`, whose members' rows are stacked (gated: the gate and its values).
     ``bias`` [N] fp32 or bf16; ``activation`` none, relu, relu2 (squared), silu, gelu or gelu_tanh; ``gated``: the
     weight's rows are [gate; values] and y is [B, N/2]; ``residual`` bf16 of y's shape.  ``out`` may be ``residual``
     (the residual stream updated in place)."""

@@ -301,3 +301,22 @@ def test_a_scale_that_is_infinite_stays_so(n, k, grain):
     pw.alpha.fill_(INF)
     y = S.linear_gemv(pw, torch.ones(2, k, dtype=BF16, device=DEV))
     assert torch.equal(y, (sign[:, 0] * INF).to(BF16).expand(2, -1))
+
+
+@pytest.mark.parametrize("grain", ["per_group", "per_channel"])
+@pytest.mark.parametrize("tokens", [3, 60])
+def test_a_gate_and_its_values_packed_together(tokens, grain):
+    """What `quantize_pack_fused` makes of the two, gated and as the stacked product."""
+    gen = torch.Generator(device=DEV).manual_seed(11)
+    gate, values = rand(gen, 200, 512, std=0.04), rand(gen, 200, 512, std=0.04)
+    fw = S.quantize_pack_fused([gate, values], grain)
+    x, b = rand(gen, tokens, 512, dtype=BF16), rand(gen, 400, std=0.5)
+    f = S.linear_gemv if tokens <= 16 else S.linear_gemm
+    for gated in (True, False):
+        y = f(fw, x, bias=b, activation="silu", gated=gated)
+        want, tol = oracle(S.unpack(fw.pw, "float32"), x, b, "silu", gated, None, 1.0)
+        close(y, want, tol)
+        assert torch.equal(y, f(fw.pw, x, bias=b, activation="silu", gated=gated))
+    for members in ([gate, values[:128]], [gate[:128], values], [gate], [gate, values, gate, values]):
+        with pytest.raises(ValueError, match="two members"):
+            f(S.quantize_pack_fused(members, grain), x, activation="silu", gated=True)

@@ -154,3 +154,14 @@ def test_linear_and_moe_binding_reject():
         S.moe_decode(x, torch.zeros(4, 256), up, down, 2)
     with pytest.raises(ValueError, match=r"\[E, N, K\]"):
         S.quantize_pack_experts(torch.zeros(4, 256))
+
+
+def test_gated_products_of_members_that_are_no_pair():
+    pw = S.PackedWeight(torch.zeros(96 * 256 * 5 // 32, dtype=torch.uint8), torch.zeros(192), 96, 256)
+    x = torch.zeros(1, 256, dtype=torch.bfloat16)
+    for f in (S.linear_gemv, S.linear_gemm):
+        for sizes in ((64, 32), (96,), (32, 32, 32)):
+            with pytest.raises(ValueError, match="two members"):
+                f(S.FusedWeight(pw, sizes), x, gated=True)
+        with pytest.raises(ValueError, match="CUDA"):
+            f(S.FusedWeight(pw, (48, 48)), x, gated=True)
