@@ -23,6 +23,11 @@ def _bf16_out():
     return _BF16_OUT
 
 
+def _apart(t, count, size):
+    """Whether ``count`` parts of ``size`` elements do not stand back to back from the start of ``t``."""
+    return t.numel() < count * size or (count > 1 and t.dim() > 1 and t.numel() != count * size and t[0].numel() != size)
+
+
 def _planes(packed, alpha, n, k, granularity, group_size, count, dev, name=""):
     """Checks the planes and scales of ``count`` packed weights [n, k]; their granularity's code."""
     torch = _torch()
@@ -33,12 +38,10 @@ def _planes(packed, alpha, n, k, granularity, group_size, count, dev, name=""):
         raise ValueError(f"{name}packed weight [{n}, {k}], group size {group_size}: not a shape")
     nbytes = n * k // 32 * 5
     scales = n * (k // group_size) if gran == _lib.PER_GROUP else n if gran == _lib.PER_CHANNEL else 1
-    if packed.dtype != torch.uint8 or packed.device != dev or not packed.is_contiguous() \
-            or packed.numel() < count * nbytes:
+    if packed.dtype != torch.uint8 or packed.device != dev or not packed.is_contiguous() or _apart(packed, count, nbytes):
         _need_gpu(packed, name + "packed", dev)
         raise ValueError(f"{name}packed must be a contiguous uint8 tensor of {count} x {nbytes} bytes")
-    if alpha.dtype != torch.float32 or alpha.device != dev or not alpha.is_contiguous() \
-            or alpha.numel() < count * scales:
+    if alpha.dtype != torch.float32 or alpha.device != dev or not alpha.is_contiguous() or _apart(alpha, count, scales):
         _need_gpu(alpha, name + "alpha", dev)
         raise ValueError(f"{name}alpha must be a contiguous float32 tensor of {count} x {scales} scales")
     return gran

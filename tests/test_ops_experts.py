@@ -384,3 +384,22 @@ def test_hidden_values_beyond_bfloat16():
     want = layer.dense(layer.down, 0).mv(h)
     # a sum of which one term is of the order of 2^27 and the others are below it: by steps of fp32
     assert ((y[0].double() - want).abs() <= 2.0 ** -22 * 2.0 ** 28).all() and y.isfinite().all()
+
+
+def test_experts_that_do_not_stand_back_to_back():
+    """Planes or scales with room after each expert are refused; more experts than are counted, and one flat tensor of
+    them, are read as they stand."""
+    layer = Layer(4, 256, 384)
+    x, res, want = layer.check(3, 2)
+    run = lambda up, down: S.moe_decode(x, layer.router, up, down, 2, residual=res)     # noqa: E731
+    new = lambda p, packed, alpha: S.PackedExperts(packed, alpha, 4, p.n, p.k)           # noqa: E731
+    pad = torch.nn.functional.pad
+    for which in ("up", "down"):
+        p, both = getattr(layer, which), {"up": layer.up, "down": layer.down}
+        for name, bad in (("packed", new(p, pad(p.packed, (0, 16)), p.alpha)), ("alpha", new(p, p.packed, pad(p.alpha, (0, 4)))),
+                          ("packed", new(p, pad(p.packed, (0, 16)).view(4, 4, -1), p.alpha))):
+            with pytest.raises(ValueError, match=f"{which}: {name}"):
+                run(**{**both, which: bad})
+        for good in (new(p, pad(p.packed, (0, 0, 0, 1)), pad(p.alpha, (0, 0, 0, 2))), new(p, p.packed.flatten(), p.alpha.flatten()),
+                     new(p, pad(p.packed.flatten(), (0, 16)), p.alpha.view(4, -1, 128))):
+            assert torch.equal(run(**{**both, which: good}), want)
