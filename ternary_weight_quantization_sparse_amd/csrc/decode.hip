@@ -142,17 +142,15 @@ __device__ inline void load_tokens(__amdgpu_buffer_rsrc_t x, uint32_t at, u32x4 
   for (int t = 0; t < 4; ++t) xf[t] = __builtin_amdgcn_raw_buffer_load_b128(x, at + 64u * t, 0, 0);
 }
 
-// v as the sum of bf16 terms, fp32's 24 bits: what lies beyond the largest bf16 stays finite, infinities and NaN have no
-// further terms.
+// v as the sum of bf16 terms, each the upper 8 bits of what is left: fp32's 24 bits exactly.  So what lies beyond the
+// largest bf16 stays finite, and an infinity has no further terms.
 constexpr int kTerms = 3;
 __device__ inline void split_terms(float v, __bf16 (&term)[kTerms]) {
-  const bool finite = __builtin_isfinite(v);
 #pragma unroll
   for (int t = 0; t < kTerms; ++t) {
-    uint16_t h = __builtin_bit_cast(uint16_t, (__bf16)v);
-    if (t == 0 && finite && (h & 0x7FFF) == 0x7F80) h -= 1;
-    term[t] = __builtin_bit_cast(__bf16, t == 0 || finite ? h : (uint16_t)0);
-    v -= __uint_as_float((uint32_t)h << 16);
+    const uint32_t upper = __float_as_uint(v) & 0xFFFF0000u;
+    term[t] = __builtin_bit_cast(__bf16, (uint16_t)(upper >> 16));
+    v = v == __uint_as_float(upper) ? 0.f : v - __uint_as_float(upper);
   }
 }
 
@@ -541,18 +539,16 @@ __device__ inline f32x4 logit_tile(const MoeArgs& a, int tile, int s0, int s1, i
       if constexpr (R_BF16) {
         acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xb, __builtin_bit_cast(bf16x8, w[u][0]), acc, 0, 0, 0);
       } else {
-        bf16x8 term[3];
+        bf16x8 term[kTerms];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          float rest = __uint_as_float(w[u][R_BF16 ? 0 : e / 4][e % 4]);
+          __bf16 of[kTerms];
+          split_terms(__uint_as_float(w[u][R_BF16 ? 0 : e / 4][e % 4]), of);
 #pragma unroll
-          for (int t = 0; t < 3; ++t) {
-            term[t][e] = (__bf16)rest;
-            rest -= (float)term[t][e];
-          }
+          for (int t = 0; t < kTerms; ++t) term[t][e] = of[t];
         }
 #pragma unroll
-        for (int t = 2; t >= 0; --t) acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xb, term[t], acc, 0, 0, 0);
+        for (int t = kTerms - 1; t >= 0; --t) acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xb, term[t], acc, 0, 0, 0);
       }
     }
   }

@@ -403,3 +403,25 @@ def test_experts_that_do_not_stand_back_to_back():
         for good in (new(p, pad(p.packed, (0, 0, 0, 1)), pad(p.alpha, (0, 0, 0, 2))), new(p, p.packed.flatten(), p.alpha.flatten()),
                      new(p, pad(p.packed.flatten(), (0, 16)), p.alpha.view(4, -1, 128))):
             assert torch.equal(run(**{**both, which: good}), want)
+
+
+@pytest.mark.parametrize("experts,dim", [(6, 256), (70, 512)])
+@pytest.mark.parametrize("normalize", [False, True])
+def test_a_float32_router_at_the_ends_of_its_range(experts, dim, normalize):
+    """Infinite entries of the router give the logits that they give by definition, and finite ones past the largest bf16
+    stay finite."""
+    layer = Layer(experts, dim, 128, router=F32)
+    x, res = layer.tokens(4)
+    x[:, 3:6] = torch.tensor([2.0, -0.5, 2.0 ** -127], device=DEV).to(BF16)
+    layer.router[1, 3], layer.router[2, 4], layer.router[4, 3] = INF, INF, -INF       # logits inf, -inf, -inf
+    layer.router[3, 5] = torch.finfo(F32).max                                          # adds 2
+    layer.router[5, 5] = -torch.finfo(F32).max
+    logits = x.double() @ layer.router.double().t().contiguous()
+    assert (logits[:, 1] == INF).all() and (logits[:, 2] == -INF).all() and logits[:, [0, 3, 5]].isfinite().all()
+    y = S.moe_decode(x, layer.router, layer.up, layer.down, 4, scoring="sigmoid", normalize=normalize, residual=res)
+    want, tol = layer.oracle(x, 4, "sigmoid", normalize, None, 1.0, "silu", res, margin=False)
+    close(y, want, tol)
+    y = S.moe_decode(x, layer.router, layer.up, layer.down, 4, residual=res)
+    assert y.isnan().all()                     # no softmax of an infinite logit
+    layer.router[1, 3] = 0
+    layer.check(4, 4, x=x, residual=False, margin=False)
