@@ -425,3 +425,18 @@ def test_a_float32_router_at_the_ends_of_its_range(experts, dim, normalize):
     assert y.isnan().all()                     # no softmax of an infinite logit
     layer.router[1, 3] = 0
     layer.check(4, 4, x=x, residual=False, margin=False)
+
+
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("experts,dim,hidden,tokens,top_k", [
+    (8, 2048, 8192, 1, 2), (8, 2048, 8192, 1, 1), (8, 1024, 4096, 2, 2), (4, 512, 8192, 2, 1),      # wide, 4 and 8 waves
+    (4, 4096, 512, 1, 2), (4, 4096, 8192, 1, 2), (2, 4096, 384, 3, 1),                             # 16 waves, narrow and wide
+    (2, 8192, 384, 1, 2), (2, 8192, 8192, 1, 1), (1, 8320, 256, 2, 1), (1, 8320, 8192, 1, 1)])
+def test_routing_in_the_first_products_at_every_count_of_waves(experts, dim, hidden, tokens, top_k, gated):
+    """At most 64 KB of router and tokens and 512 workgroups of first products: each of them makes the routing for
+    itself, and the waves share the channels of its tiles."""
+    used = min(experts, tokens * top_k)
+    rows = hidden * (2 if gated else 1)
+    tile = (32 if gated else 64) if rows // 64 * used >= 256 else 16
+    assert (experts + tokens) * 2 * dim <= 65536 and hidden // tile * used <= 512
+    Layer(experts, dim, hidden, gated=gated).check(tokens, top_k)
