@@ -726,10 +726,12 @@ __global__ __launch_bounds__(64 * WAVES) void moe_up(MoeArgs a) {
   __shared__ __attribute__((aligned(16))) uint2 dtab[32];
   __shared__ f32x4 part[WAVES][TR][64];
   __shared__ int place[16];
+  __shared__ float weight[16];
   const int tid = threadIdx.x, lane = tid & 63, r = lane & 15, q = lane >> 4;
   const int at = blockIdx.y;
   if (tid < 32) dtab[tid] = decode_bf16(tid);
   int expert, mine;
+  float w;
   if constexpr (OWN) {
     __shared__ Routing rt;
     __shared__ float logits[16][64];
@@ -746,7 +748,6 @@ __global__ __launch_bounds__(64 * WAVES) void moe_up(MoeArgs a) {
       for (int i = at < low ? at : at - low; i > 0; --i) left &= left - 1u;
       expert = __builtin_ctz(left) + (at < low ? 0 : 32);
     }
-    float w;
     mine = place_of(a, rt, expert, r, w);
     if (blockIdx.x == 0 && tid < 16) {
       if (tid == 0) a.route->list[at] = expert;
@@ -756,10 +757,10 @@ __global__ __launch_bounds__(64 * WAVES) void moe_up(MoeArgs a) {
   } else {
     const MoeRoute& route = *a.route;
     const int count = route.count;
-    expert = route.list[at], mine = route.place[at][r];   // (loaded together)
+    expert = route.list[at], mine = route.place[at][r], w = route.weight[at][r];   // (loaded together)
     if (at >= count) return;
   }
-  if (tid < 16) place[tid] = mine;
+  if (tid < 16) place[tid] = mine, weight[tid] = w;
   const int64_t outs = a.hidden, n = GATED ? 2 * outs : outs, tile = blockIdx.x;
   const Planes p = planes(a.up + expert * a.up_bytes, a.up_alpha + expert * a.up_scales, n, a.dim, a.up_gran, a.up_group_sbs);
   const uint32_t x_lane = mine >= 0 ? (uint32_t)(r * a.dim + 8 * q) * 2u : kNowhere;
@@ -771,6 +772,7 @@ __global__ __launch_bounds__(64 * WAVES) void moe_up(MoeArgs a) {
     if (to_place < 0) continue;
     float z = activate(wave_sums<TR, WAVES>(part, which, token, c), a.activation);
     if constexpr (GATED) z *= wave_sums<TR, WAVES>(part, kOut + which, token, c);
+    if (weight[token] != weight[token]) z = NAN;   // also for the outputs whose scale is zero (`weighted`)
     __bf16 term[kTerms];
     split_terms(z, term);
     const int64_t to = ((int64_t)token * a.slots + to_place) * a.hidden + tile * (16 * kOut) + which * 16 + c;

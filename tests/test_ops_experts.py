@@ -440,3 +440,21 @@ def test_routing_in_the_first_products_at_every_count_of_waves(experts, dim, hid
     tile = (32 if gated else 64) if rows // 64 * used >= 256 else 16
     assert (experts + tokens) * 2 * dim <= 65536 and hidden // tile * used <= 512
     Layer(experts, dim, hidden, gated=gated).check(tokens, top_k)
+
+
+@pytest.mark.parametrize("experts,dim,tokens", [(6, 256, 3), (70, 256, 3), (40, 2048, 16)])
+def test_no_softmax_for_outputs_of_scale_zero_either(experts, dim, tokens):
+    """Without a softmax a token's weights are not numbers, nor is their product with a row of zeros."""
+    layer = Layer(experts, dim, 128)
+    x, res = layer.tokens(tokens)
+    for e in range(experts):
+        layer.down.alpha[e].view(-1, dim)[:, ::3] = 0
+    x[:, 0] = 1                              # of token 1 the logit of expert 2 is not a number
+    x[1, 0] = 0
+    layer.router[2, 0] = INF
+    y = S.moe_decode(x, layer.router, layer.up, layer.down, 2, scoring="softmax", residual=res)
+    assert y.isnan().all()
+    x[:, 0], x[1, 0] = 0, 1
+    layer.router[2, 0] = 0
+    layer.router[2, 1] = float("nan")
+    assert S.moe_decode(x, layer.router, layer.up, layer.down, 2, residual=res).isnan().all()
