@@ -156,7 +156,7 @@ __device__ inline void split_terms(float v, __bf16 (&term)[kTerms]) {
 
 // A row's scale times the tokens' weights of an expert; One: no weights.  A weight of zero (a token that the expert
 // does not serve) gives zero also where the scale is not finite: that is what the legacy product is for, at an
-// ordinary one's cost (a comparison and selections took 0.4 us of moe_down's 13).
+// ordinary one's cost (a comparison and selections took 0.4 us of moe_down's 13, with two terms of h).
 struct One {};
 __device__ inline float weighted(float scale, One, int) { return scale; }
 __device__ inline float weighted(float scale, const f32x4& weight, int e) {
@@ -227,7 +227,7 @@ __device__ inline void run_items(int j0, int j1, const char* dtab, int q, R reco
 // weight's second half).  The waves split K; a wave issues all its loads at once where it has up to XS superblocks
 // (0: more, through a ring), and the waves join through LDS: wave_sums adds them in order.  Short workgroups, eight
 // waves a SIMD, hide the latency better than ones that walk several tiles and load ahead (mixture of experts, 16
-// tokens, 56 experts of 2048 x 2048: 18 us against 20 to 25).
+// tokens, 56 experts of 2048 x 2048, both before sets past a wave's range were left out: 18 us against 20 to 25).
 template <int TR, int WAVES, bool GATED, int XS>
 __device__ inline void tile_product(const Planes& p, int64_t outs, int sbs, __amdgpu_buffer_rsrc_t x, uint32_t x_lane,
                                     int64_t tile, const char* dtab, f32x4 (&part)[WAVES][TR][64]) {
@@ -294,7 +294,7 @@ __device__ inline float finish_output(const LinearArgs& a, float z, float u, int
 }
 
 // ------------------------------------------------------------ linear, 1..16 tokens
-// 1 x 2048 x 2048: 3.7 us; 16 x 16384 x 2048 gated, 6.6 MB: 5.4 us (1.2 TB/s); 5 x 1001 x 8192: 7.6 us.
+// 1 x 2048 x 2048: 3.7 us; 16 x 16384 x 2048 gated, 6.6 MB: 5.4 us (1.2 TB/s); 5 x 1001 x 8192: 7.7 us.
 template <int TR, int WAVES, bool GATED, int XS>
 __global__ __launch_bounds__(64 * WAVES) void linear_decode(LinearArgs a, const uint16_t* __restrict__ x, int tokens,
                                                             void* __restrict__ y, bool y_bf16) {
@@ -717,9 +717,8 @@ __global__ __launch_bounds__(64 * kRouteWaves) void moe_route(MoeArgs a) {
 
 // First products and the activation: h[token, place] of the blockIdx.y-th expert in use, for its tokens. h is kept as
 // three bf16 terms, which together are the fp32 value: two (2^-17 of it) left a float32 y 2.5e-6 from its definition,
-// three 2.2e-7 (16 tokens, 8 of 64 experts). 16 tokens, 56 of 64 experts of
-// 2048 x 2 x 1024, 43 MB: 15.7 us (2.7 TB/s).  Of that the LDS lookups take 6 us; without any product it takes 13,
-// without the records' loads 12: no single one of them bounds it.
+// three 2.2e-7 (16 tokens, 8 of 64 experts). 16 tokens, 56 of 64 experts of 2048 x 2 x 1024, 43 MB: 16.2 us (2.7
+// TB/s).  Of that the LDS lookups take 6 us; without any product it took 13, without the records' loads 12.
 template <int TR, int WAVES, bool GATED, int XS, bool OWN>
 __global__ __launch_bounds__(64 * WAVES) void moe_up(MoeArgs a) {
   constexpr int kOut = GATED ? TR / 2 : TR;
@@ -879,8 +878,8 @@ __global__ __launch_bounds__(256) void moe_join(MoeArgs a, void* __restrict__ y,
     else if ((SBS) <= 64) RUN(16, 4);   \
     else RUN(16, 0);                    \
   } while (0)
-// 64 weight rows a workgroup where that leaves work for every CU (16 x 16384 x 2048 gated: 5.7 us, with 16 + 16 rows
-// 7.7); 16 (16 + 16: gate and values) where it does not (1 x 2048 x 2048: 3.8 us in 128 workgroups).
+// 64 weight rows a workgroup where that leaves work for every CU (16 x 16384 x 2048 gated: 5.4 us, with 16 + 16 rows
+// 7.7); 16 (16 + 16: gate and values) where it does not (1 x 2048 x 2048: 3.7 us in 128 workgroups).
 bool wide_tiles(int64_t blocks64) { return blocks64 >= 256; }
 
 hipError_t launch_linear_decode(const LinearArgs& a, const uint16_t* x, int tokens, void* y, bool y_bf16,
@@ -926,15 +925,19 @@ hipError_t launch_linear_tiles(const LinearArgs& a, const uint16_t* x, int64_t m
 constexpr int64_t kRouteBytes = 65536;
 
 // Up to this many workgroups the first products make a small router's routing each for itself, which saves its
-// launch: 3 us of a call from Python; in a graph, at 512, 17.2 us against 18.0 (4 tokens, 2 of 16 experts of 1024 x
-// 2048), 14.8 against 16.4 (4 tokens, 4 of 32 of 512 x 512), 18.1 against 17.1 (16 tokens, 2 of 16 of 512 x 1024); at
-// 1024 workgroups 22.4 against 21.3, at 2048 32 against 25.5.
+// launch.  At 512, in a graph 17.6 us against 18.3 and called from Python 19.6 against 21.9 (4 tokens, 2 of 16 experts
+// of 1024 x 2048); at 256, 16.6 against 18.1 and 17.2 against 19.5 (4 tokens, 4 of 32 of 512 x 512).  Many tokens are
+// routed a few a wave one after another, which costs a graph more than the launch and Python less: 16 tokens, 2 of 16
+// of 512 x 1024, 18.7 against 17.5 and 19.5 against 21.9; 4 of 30 of 512 x 384, 21.9 against 18.6 and 22.6 against
+// 23.0.  At 1024 workgroups 22.4 against 21.3 in a graph, at 2048 32 against 25.5.
 constexpr int64_t kOwnRouting = 512;
 
 // The second products in one range of 16 waves and 16 rows a workgroup up to kNarrowItems items (4 a wave), which
-// saves the joining launch; past it 64 rows, 8 waves and ranges of about two items a wave, at most 512 workgroups (in
-// a graph, 1 token: 2 of 16 experts of 4096 x 2048, 32 items, 18.9 us against 21.2; 8 of 64 of 2048 x 1024, 64 items,
-// 20.9 against 20.1, but called from Python 23.7 against 25.9; 2 of 8 of 2048 x 8192, 128 items, 26.3 against 20.4).
+// saves the joining launch (1 token; 2 of 16 experts of 4096 x 2048, 32 items: in a graph 19.5 us against 20.9; 8 of 64
+// of 2048 x 1024, 64 items: 22.8 against 20.4, but called from Python 23.2 against 26.8; 2 of 8 of 2048 x 8192, 128
+// items: 29.4 against 20.5).  Past it 64 rows, 8 waves and ranges of about two items a wave (2 of 8 of 2048 x 8192:
+// 20.5 us, with one a wave 20.6, with four 23.4), at most 512 workgroups (16 tokens, 8 of 64 of 2048 x 1024: 40.6, with
+// 256 41.6, with 1024, whose partials are twice as many, 43.9).
 constexpr int kNarrowItems = 64, kDownTiles = 4, kDownWaves = 8;
 MoePlan plan_moe(int tokens, int64_t dim, int64_t hidden, int experts, int shared, int top_k, bool router_bf16) {
   auto up = [](size_t b) { return (b + 255) & ~(size_t)255; };

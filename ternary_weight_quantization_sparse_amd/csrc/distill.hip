@@ -517,7 +517,7 @@ int64_t rows_of_launch(int ranges) { return std::max<int64_t>(1, ((int64_t)1 << 
 
 }  // namespace
 
-// Ranges of a row: about 2048 workgroups, at least 4096 elements each (16 a
+// Ranges of a row: about 2048 workgroups, about 4096 elements each or more (16 a
 // thread; 4096 and 8192 workgroups took as long), at most 2^18 (the bitmap's 32 KB); backward 16384 elements (8192
 // as long, 32768 and 65536 5% longer).  A range is whole groups; one
 // group more than the row's own covers a row that begins inside a group.

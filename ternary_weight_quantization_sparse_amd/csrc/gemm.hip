@@ -983,8 +983,9 @@ GemmPlan plan_linear(int64_t n, int64_t k, int gran, int group_size, int64_t m, 
     // Wide tiles only where they fill their 512 places (two workgroups a CU) in every round, and past one round where
     // K is long or the product gated, so that the epilogue counts little.  With bias, silu and residual 1024 x 8192 x
     // 2048, 512 tiles, gated 43.7 us against 51.3 in narrow ones (which run three a CU), 2048 x 4096 x 8192 131 against
-    // 151, 2048 x 16384 x 2048 gated without bias and residual 131 against 136; but 517 x 16384 x 2048, 576 tiles, 95.9
-    // against 61.7, 1300 x 8192 x 4096 137 against 109, 2048 x 16384 x 2048 201 against 182.
+    // 151, 2048 x 16384 x 2048 gated without bias and residual 131 against 136; but 517 x 16384 x 2048, 576 tiles, 95.6
+    // against 60.4, 1300 x 8192 x 4096 135 against 108, 2048 x 16384 x 2048 201 against 178 (with three sets of
+    // operands in turn, more than the last-level cache holds, 219 against 199).
     const int64_t tiles = (mc + p.tile_m - 1) / p.tile_m * ((n + 255) / 256), places = (tiles + 511) / 512 * 512;
     if (tiles * 10 < places * 9 || (tiles > 512 && k < 4096 && !gated)) p.tile_n = 128;
   }
